@@ -97,6 +97,11 @@ typedef enum {
  * slots) fell outside its buffer; it was replaced by 0, so nothing was read or
  * written outside a buffer.  Release builds never set it. */
 #define LORA_DEVERR_BOUNDS 0x8u
+/* paged cache: a page that is needed lies outside the block table's row, or
+ * its id outside [0, n_pages) */
+#define LORA_DEVERR_BAD_PAGE 0x10u
+#define LORA_DEVERR_BAD_POS 0x20u /* a rotary position outside [0, n_pos) was read */
+#define LORA_DEVERR_BAD_LEN 0x40u /* q_off, kv_len, group_off or prefix_len out of order or range */
 
 #define LORA_MAX_SLOTS 16384
 #define LORA_MAX_TOKENS (1 << 20)
@@ -498,6 +503,128 @@ lora_status_t lora_slot_upload(void* A_pool, void* B_pool, float* scale, int32_t
                                const void* A_host, const void* B_host, float s, int32_t d_in,
                                int32_t d_out, int32_t r, int32_t r_a, int32_t n_slots,
                                lora_dtype_t dt, void* stream);
+
+/*
+ * The paged cache of keys and values, and a batch's place in it
+ * -------------------------------------------------------------
+ * Attention between the layers above (q, k, v in, the o projection's input
+ * out).  The pages name the cache as the adapters' neighbour in device
+ * memory ("Serving Many LoRA Adapters", the unified pool of cache pages and
+ * adapter pages); the operators here read and write one.
+ *   k_cache, v_cache  [n_pages, n_kv_heads, page_size, head_dim] bf16.
+ *   block_table [n_seqs, max_pages] int32: position j of sequence s lies in
+ *               page block_table[s, j / page_size], row j % page_size.
+ *               Entries of pages that no row sees (past the length, or left
+ *               behind by a window) are not read and may hold anything.
+ *   q_off  [n_seqs + 1] int32: the new tokens of sequence s are rows
+ *          q_off[s] .. q_off[s+1) of q, k, v and out.  A sequence may have
+ *          none.  Rows from q_off[n_seqs] on belong to no sequence (padding
+ *          of a captured graph) and are left alone.
+ *   kv_len [n_seqs] int32: positions of sequence s that are valid after this
+ *          step's append.  The position of its row i is therefore
+ *          kv_len[s] - (q_off[s+1] - q_off[s]) + i.  A row before position 0
+ *          is not cached and sees nothing.
+ *   n_pages, page_size (8, 16, 32, 64, 128 or 256), n_kv_heads, head_dim (64
+ *          or 128), n_seqs, max_pages, T (rows of q, k, v, out).
+ *   max_q_len  the most new tokens of any one sequence, as the host knows it.
+ *          It selects kernels; results do not depend on it beyond rounding.
+ * All arrays are device memory and 16-byte aligned (the int32 ones: 4-byte);
+ * the struct itself is host memory, read during the call.  q, k, v and out
+ * are bf16 [T, heads, head_dim] with any distance between tokens that is a
+ * multiple of 8 elements (*_stride, in elements), so that they can be parts of
+ * one wider projection's rows.  Offsets are 64-bit throughout.
+ */
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_table;
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int32_t n_seqs, max_pages, T, max_q_len;
+} lora_paged_kv_t;
+
+#define LORA_MAX_SEQS 65536
+#define LORA_MAX_POS_AXES 4
+#define LORA_MAX_HEADS 1024
+
+/*
+ * Bytes of workspace lora_attn_paged (n_groups = 0) or lora_attn_prefix
+ * (n_groups >= 1) needs for any batch of this size; 16 where the arguments
+ * are out of range.  lora_kv_append needs the 16-byte error word only.
+ * Zero-fill the workspace once; the calls leave its counters at zero.  After
+ * LORA_DEVERR_TIMEOUT zero-fill it again.
+ */
+size_t lora_attn_workspace_bytes(const lora_paged_kv_t* kv, int32_t n_q_heads, int32_t n_groups);
+
+/*
+ * Rotates q and k by position and appends k and v to the cache, in one pass:
+ *   q_out[t]                        = rot(q[t])      (skipped with n_q_heads = 0)
+ *   k_cache[page(p), h, p % page_size] = rot(k[t, h])   p = the position of row t
+ *   v_cache[page(p), h, p % page_size] = v[t, h]
+ * rot works on the first rot_dim values of a head (a multiple of 16, 0 ..
+ * head_dim; the rest pass), in pairs i = 0 .. rot_dim/2 - 1:
+ *   (a, b) -> (a c - b s, b c + a s),  c = cos_sin[P, i],  s = cos_sin[P, rot_dim/2 + i]
+ * a = x[i], b = x[i + rot_dim/2], or with `interleaved` a = x[2i], b = x[2i+1];
+ * fp32 arithmetic, rounded once.  cos_sin [n_pos, rot_dim] fp32 is the
+ * caller's table (so any frequency scaling is the caller's).
+ * The rotary position P: pos [n_axes, T] int32.  With n_axes = 1 pos may be
+ * NULL: P = p.  With several axes (time, height, width of images and video;
+ * n_axes <= LORA_MAX_POS_AXES) the first axis_pairs[0] pairs use pos[0, t],
+ * the next axis_pairs[1] use pos[1, t] and so on; axis_pairs is a HOST array
+ * of n_axes counts >= 0 that add up to rot_dim / 2 (NULL with n_axes = 1).
+ * A position outside [0, n_pos) sets LORA_DEVERR_BAD_POS and leaves its pairs
+ * unrotated.  A row whose page is missing (outside the table, or an id
+ * outside [0, n_pages)) sets LORA_DEVERR_BAD_PAGE and is not cached.  Two rows
+ * of one call must not share a cache position.  q_out may be q itself with the
+ * same stride.
+ */
+lora_status_t lora_kv_append(const lora_paged_kv_t* kv, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             int32_t n_q_heads, const float* cos_sin, int32_t n_pos,
+                             int32_t rot_dim, const int32_t* pos, int32_t n_axes,
+                             const int32_t* axis_pairs, int32_t interleaved, void* q_out,
+                             int64_t q_out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Causal attention of the batch's rows over the cache:
+ *   out[t, h] = sum_j w_j v_j,  w = softmax over the visible j of scale * (q[t, h] . k_j)
+ * with the keys and values of key head h / (n_q_heads / n_kv_heads).  A row at
+ * position p sees j <= p; with window >= 1 only j > p - window or j < n_sink
+ * (the first tokens stay visible).  window = 0: no window.  A row that sees
+ * nothing gets zeros.  Scores, maxima, sums and the accumulator are fp32, the
+ * weights enter the product with v as bf16 (single tokens: as a pair of them),
+ * the result is rounded once.
+ * n_q_heads is a multiple of n_kv_heads.  Any mix of lengths in one call:
+ * prompts, chunks, single tokens.  Cache rows that no row of the sequence sees
+ * may hold anything, NaN included; a value that some row sees has to be
+ * finite.  A missing page reads as zeros and sets LORA_DEVERR_BAD_PAGE.
+ * The order of the sums is a function of the batch's lengths, so equal calls
+ * give equal bits.
+ */
+lora_status_t lora_attn_paged(const lora_paged_kv_t* kv, const void* q, int64_t q_stride,
+                              int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,
+                              void* out, int64_t out_stride, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * lora_attn_paged without a window for a batch whose sequences share prefixes:
+ * keys and values depend on the adapter, so the requests of one adapter share
+ * its system prompt's pages.  Group g is sequences group_off[g] ..
+ * group_off[g+1) (int32 [n_groups + 1], device, ascending, group_off[0] = 0;
+ * sequences after the last group share nothing); the first prefix_len[g]
+ * positions of all of them hold the same keys and values and are read ONCE,
+ * through the block table row of the group's first sequence.  The other rows'
+ * entries for pages that lie wholly inside the prefix are not read.
+ * prefix_len [n_groups] int32, device, any length >= 0 up to the positions
+ * before the new tokens of each sequence in the group.  A longer one sets
+ * LORA_DEVERR_BAD_LEN; the positions inside it are still read through the
+ * first sequence's row, and rows still see only positions up to their own.
+ */
+lora_status_t lora_attn_prefix(const lora_paged_kv_t* kv, const int32_t* group_off,
+                               const int32_t* prefix_len, int32_t n_groups, const void* q,
+                               int64_t q_stride, int32_t n_q_heads, float scale, void* out,
+                               int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, copies the workspace error word to *device_err and

@@ -19,6 +19,8 @@ struct DeviceInfo {
   size_t max_smem_optin = 0;
 };
 cudaError_t device_info(DeviceInfo* out);
+// LORA_OK and the facts if the current device is one the library is built for.
+lora_status_t check_device(DeviceInfo* out);
 
 // Segment builder: one CTA, see k_segments.cu.  It also zeroes the n_zero
 // words at `zero` (the counters of the shrink's split fold), if given.

@@ -10,6 +10,14 @@
 #include "lora.h"
 
 namespace lora {
+
+// The library is built for sm_103a only.
+lora_status_t check_device(DeviceInfo* out) {
+  return device_info(out) == cudaSuccess
+             ? ((out->cc_major == 10 && out->cc_minor == 3) ? LORA_OK : LORA_ERR_DEVICE)
+             : LORA_ERR_CUDA;
+}
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -155,13 +163,6 @@ RaggedWs ragged_ws_layout(void* ws, int32_t T, int32_t d_in, int32_t d_out, int3
 }
 
 lora_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA; }
-
-// The library is built for sm_103a only.
-lora_status_t check_device(DeviceInfo* out) {
-  return device_info(out) == cudaSuccess
-             ? ((out->cc_major == 10 && out->cc_minor == 3) ? LORA_OK : LORA_ERR_DEVICE)
-             : LORA_ERR_CUDA;
-}
 
 // SGMV shrink: tensor cores for bf16 pools of rank 64 / 128 (there it is a
 // GEMM the CUDA cores cannot feed), the CUDA-core kernel otherwise.

@@ -25,6 +25,7 @@ OP_SGMV_SHRINK, OP_SGMV_EXPAND, OP_LINEAR_FUSED, OP_BASE_GEMM_EXPAND = 3, 4, 5, 
 OP_LINEAR_FUSED_4BIT = 7
 OP_LINEAR_FUSED_RAGGED = 8
 DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_BAD_RANK, DEVERR_BOUNDS = 0x1, 0x2, 0x4, 0x8
+DEVERR_BAD_PAGE, DEVERR_BAD_POS, DEVERR_BAD_LEN = 0x10, 0x20, 0x40
 RAGGED_RANKS = (8, 16, 32, 64, 128)
 MAX_SLOTS, MAX_TOKENS, MAX_KSPLIT = 16384, 1 << 20, 64
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -35,6 +36,7 @@ EXPORTS = ("lora_workspace_bytes", "lora_build_segments", "lora_bgmv_shrink", "l
            "lora_bgmv_adapter_merge", "lora_base_gemm_splitk", "lora_decode_split",
            "lora_slot_upload", "lora_bgmv_adapter_ragged", "lora_linear_fused_ragged",
            "lora_quantize_base_4bit", "lora_base_gemm_4bit_splitk", "lora_linear_fused_4bit",
+           "lora_attn_workspace_bytes", "lora_kv_append", "lora_attn_paged", "lora_attn_prefix",
            "lora_debug_gemm_wait_timeout", "lora_get_error", "lora_status_string")
 
 
@@ -49,6 +51,15 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _Z = ctypes.c_size_t
 _L = ctypes.c_int64
+_F = ctypes.c_float
+
+
+class PagedKVStruct(ctypes.Structure):
+    """lora_paged_kv_t."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "block_table", "q_off", "kv_len")] +
+                [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "n_seqs",
+                                               "max_pages", "T", "max_q_len")])
+
 
 _SIGS = {
     "lora_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
@@ -77,6 +88,10 @@ _SIGS = {
     "lora_linear_fused_4bit": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P,
                                     _Z, _P]),
     "lora_debug_gemm_wait_timeout": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _Z, _P]),
+    "lora_attn_workspace_bytes": (_Z, [_P, _I, _I]),
+    "lora_kv_append": (_I, [_P, _P, _L, _P, _L, _P, _L, _I, _P, _I, _I, _P, _I, _P, _I, _P, _L, _P, _Z, _P]),
+    "lora_attn_paged": (_I, [_P, _P, _L, _I, _F, _I, _I, _P, _L, _P, _Z, _P]),
+    "lora_attn_prefix": (_I, [_P, _P, _P, _I, _P, _L, _I, _F, _P, _L, _P, _Z, _P]),
     "lora_get_error": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "lora_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -221,6 +236,28 @@ def lora_linear_fused_4bit(x, W0q, absmax, codebook, A_pool, B_pool, slot_ids, s
                            d_out, r, n_slots, ws, ws_bytes, stream):
     return _call("lora_linear_fused_4bit", x, W0q, absmax, codebook, A_pool, B_pool, slot_ids,
                  scale, y, T, d_in, d_out, r, n_slots, ws, ws_bytes, stream)
+
+
+def lora_attn_workspace_bytes(kv, n_q_heads, n_groups):
+    return _call("lora_attn_workspace_bytes", kv, n_q_heads, n_groups)
+
+
+def lora_kv_append(kv, q, q_stride, k, k_stride, v, v_stride, n_q_heads, cos_sin, n_pos, rot_dim, pos,
+                   n_axes, axis_pairs, interleaved, q_out, q_out_stride, ws, ws_bytes, stream):
+    return _call("lora_kv_append", kv, q, q_stride, k, k_stride, v, v_stride, n_q_heads, cos_sin, n_pos,
+                 rot_dim, pos, n_axes, axis_pairs, interleaved, q_out, q_out_stride, ws, ws_bytes, stream)
+
+
+def lora_attn_paged(kv, q, q_stride, n_q_heads, scale, window, n_sink, out, out_stride, ws, ws_bytes,
+                    stream):
+    return _call("lora_attn_paged", kv, q, q_stride, n_q_heads, scale, window, n_sink, out, out_stride, ws,
+                 ws_bytes, stream)
+
+
+def lora_attn_prefix(kv, group_off, prefix_len, n_groups, q, q_stride, n_q_heads, scale, out, out_stride,
+                     ws, ws_bytes, stream):
+    return _call("lora_attn_prefix", kv, group_off, prefix_len, n_groups, q, q_stride, n_q_heads, scale, out,
+                 out_stride, ws, ws_bytes, stream)
 
 
 def lora_get_error(ws, stream):
@@ -570,6 +607,144 @@ def linear_fused_4bit_t(x, base, A_pool, B_pool, slot_ids, scale, ws, y=None, st
                                  _stream(stream)),
           "lora_linear_fused_4bit")
     return y
+
+
+class PagedKV:
+    """A paged cache and a batch's place in it (lora_paged_kv_t): k_cache, v_cache
+    [n_pages, n_kv_heads, page_size, head_dim] bf16, block_table [n_seqs, max_pages], q_off
+    [n_seqs + 1] and kv_len [n_seqs] int32 on the device, T rows of new tokens, of which
+    any one sequence has at most max_q_len (default T).  The object keeps the tensors and
+    their addresses: update them in place from step to step (a decode loop needs no other
+    object), make a new one when T or a tensor changes."""
+
+    def __init__(self, k_cache, v_cache, block_table, q_off, kv_len, T, max_q_len=None):
+        import torch
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
+                raise TypeError(f"{name}: contiguous bf16 [n_pages, n_kv_heads, page_size, head_dim]")
+        for name, t in (("block_table", block_table), ("q_off", q_off), ("kv_len", kv_len)):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise TypeError(f"{name}: contiguous int32")
+        n_pages, n_kv_heads, page_size, head_dim = k_cache.shape
+        n_seqs = kv_len.numel()
+        if v_cache.shape != k_cache.shape or block_table.dim() != 2 or block_table.shape[0] != n_seqs or \
+                q_off.numel() != n_seqs + 1:
+            raise ValueError("k_cache and v_cache of one shape; block_table [n_seqs, max_pages], "
+                             "q_off [n_seqs + 1], kv_len [n_seqs]")
+        if not k_cache.is_cuda or any(t.device != k_cache.device
+                                      for t in (v_cache, block_table, q_off, kv_len)):
+            raise ValueError("the cache and its index tensors have to be on one CUDA device")
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.block_table, self.q_off, self.kv_len = block_table, q_off, kv_len
+        self.T, self.n_kv_heads, self.head_dim = T, n_kv_heads, head_dim
+        self.struct = PagedKVStruct(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(q_off),
+                                    _ptr(kv_len), n_pages, page_size, n_kv_heads, head_dim, n_seqs,
+                                    block_table.shape[1], T, T if max_q_len is None else max_q_len)
+        self.ref = ctypes.addressof(self.struct)
+
+    def rows(self, x, n_heads=None, what="q"):
+        """Checks x [T, heads, head_dim] bf16 and returns its distance between tokens."""
+        import torch
+        st = x.stride()
+        if x.dtype is not torch.bfloat16:
+            raise TypeError(f"{what}: unsupported dtype {x.dtype}")
+        if x.dim() != 3 or x.shape[0] != self.T or x.shape[2] != self.head_dim or \
+                (n_heads is not None and x.shape[1] != n_heads):
+            raise ValueError(f"{what}: shape {tuple(x.shape)}, need [{self.T}, "
+                             f"{'heads' if n_heads is None else n_heads}, {self.head_dim}]")
+        if st[2] != 1 or (x.shape[1] > 1 and st[1] != self.head_dim):
+            raise ValueError(f"{what}: heads of a token must be contiguous")
+        if x.device != self.k_cache.device:
+            raise ValueError(f"{what}: on {x.device}, the cache on {self.k_cache.device}")
+        return st[0] if self.T > 1 else x.shape[1] * x.shape[2]
+
+
+def attn_workspace(kv, n_q_heads, n_groups=0):
+    """A zero-filled workspace for attn_paged_t (n_groups = 0), attn_prefix_t (n_groups >= 1)
+    and kv_append_t over `kv`."""
+    import torch
+    n = lora_attn_workspace_bytes(kv.ref, n_q_heads, n_groups)
+    return torch.zeros(max(int(n), 16), dtype=torch.uint8, device=kv.k_cache.device)
+
+
+def rope_table(n_pos, rot_dim, base=10000.0, device="cuda"):
+    """The cos_sin table [n_pos, rot_dim] of plain rotary frequencies base^(-2i / rot_dim),
+    angles in 64 bits."""
+    import torch
+    freq = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
+                stream=None):
+    """Rotates q [T, n_q_heads, D] and k [T, n_kv_heads, D] by position, writes k and v into
+    kv's cache and returns the rotated q (a new tensor unless q_out is given; q itself is
+    allowed).  q None: keys and values only.  cos_sin [n_pos, rot_dim] fp32 (rope_table) or
+    None for no rotation.  pos: None (the position in the cache), [T], or [n_axes, T] with
+    axis_pairs, the rotated pairs of each axis."""
+    import torch
+    n_q = 0
+    q_stride = q_out_stride = 0
+    if q is not None:
+        q_stride = kv.rows(q)
+        n_q = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((kv.T, n_q, kv.head_dim), dtype=torch.bfloat16, device=q.device)
+        q_out_stride = kv.rows(q_out, n_q, "q_out")
+    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    if cos_sin is not None and (cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous()):
+        raise TypeError("cos_sin: contiguous fp32 [n_pos, rot_dim]")
+    n_axes = 1
+    if pos is not None:
+        n_axes = pos.numel() // kv.T if kv.T else 1
+        if pos.dtype is not torch.int32 or not pos.is_contiguous() or pos.shape[-1] != kv.T:
+            raise TypeError(f"pos: contiguous int32 [{kv.T}] or [n_axes, {kv.T}]")
+    pairs = None
+    if axis_pairs is not None:
+        if len(axis_pairs) != n_axes:
+            raise ValueError(f"axis_pairs: {len(axis_pairs)} counts for {n_axes} axes")
+        pairs = (ctypes.c_int32 * n_axes)(*axis_pairs)
+    check(lora_kv_append(kv.ref, _ptr(q), q_stride, k.data_ptr(), kv.rows(k, kv.n_kv_heads, "k"),
+                         v.data_ptr(), kv.rows(v, kv.n_kv_heads, "v"), n_q, _ptr(cos_sin), n_pos, rot,
+                         _ptr(pos), n_axes, pairs, 1 if interleaved else 0, _ptr(q_out), q_out_stride,
+                         ws.data_ptr(), ws.numel(), _stream(stream)), "lora_kv_append")
+    return q_out
+
+
+def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
+    """Causal attention of q [T, n_q_heads, D] over kv's cache (lora_attn_paged); scale
+    defaults to D^-0.5, window 0 is none."""
+    import torch
+    q_stride = kv.rows(q)
+    n_q = q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    check(lora_attn_paged(kv.ref, q.data_ptr(), q_stride, n_q,
+                          kv.head_dim ** -0.5 if scale is None else scale, window, n_sink, out.data_ptr(),
+                          kv.rows(out, n_q, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
+          "lora_attn_paged")
+    return out
+
+
+def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
+    """attn_paged_t for groups of sequences that share a prefix (lora_attn_prefix):
+    group_off [n_groups + 1], prefix_len [n_groups] int32 on the device."""
+    import torch
+    q_stride = kv.rows(q)
+    n_q = q.shape[1]
+    n_groups = prefix_len.numel()
+    if group_off.dtype is not torch.int32 or prefix_len.dtype is not torch.int32 or \
+            group_off.numel() != n_groups + 1 or not group_off.is_contiguous() or \
+            not prefix_len.is_contiguous():
+        raise TypeError("group_off [n_groups + 1], prefix_len [n_groups]: contiguous int32")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    check(lora_attn_prefix(kv.ref, group_off.data_ptr(), prefix_len.data_ptr(), n_groups, q.data_ptr(),
+                           q_stride, n_q, kv.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                           kv.rows(out, n_q, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
+          "lora_attn_prefix")
+    return out
 
 
 def get_error_t(ws, stream=None):
