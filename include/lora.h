@@ -617,9 +617,8 @@ lora_status_t lora_attn_paged(const lora_paged_kv_t* kv, const void* q, int64_t 
  * through the block table row of the group's first sequence.  The other rows'
  * entries for pages that lie wholly inside the prefix are not read.
  * prefix_len [n_groups] int32, device, any length >= 0 up to the positions
- * before the new tokens of each sequence in the group.  A longer one sets
- * LORA_DEVERR_BAD_LEN; the positions inside it are still read through the
- * first sequence's row, and rows still see only positions up to their own.
+ * before the new tokens of each sequence in the group; where it is longer,
+ * LORA_DEVERR_BAD_LEN is set and that sequence's rows are unspecified.
  */
 lora_status_t lora_attn_prefix(const lora_paged_kv_t* kv, const int32_t* group_off,
                                const int32_t* prefix_len, int32_t n_groups, const void* q,

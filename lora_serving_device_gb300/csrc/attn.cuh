@@ -1,4 +1,18 @@
-// Device helpers shared by the paged-cache kernels.
+// Device helpers shared by the paged-cache kernels: finding a row's sequence,
+// and the schedule of the attention kernels.
+//
+// The schedule.  A problem is a run of consecutive tokens that attend to one
+// block-table row over the keys [k_lo, k_hi): a sequence, or a prefix group
+// (all its sequences' tokens against the shared prefix).  Its rows, (token,
+// query head of one key head), are packed token-major and cut into row tiles
+// of kRows; a row tile sees some 128-key tiles.  An item is (row tile, key
+// head); a unit is one key tile of an item.  All units, numbered row tile by
+// row tile, key head by key head, are cut into equal contiguous shares, one
+// per CTA, whatever the lengths are (they live on the device).  An item that
+// several CTAs share is finished by the last of them to arrive, which adds
+// their parts in CTA order: the result is a function of the lengths alone.
+// Each CTA computes the shares itself, from prefix sums of at most kCoarse
+// coarse entries in shared memory.
 #pragma once
 
 #include "attn.h"
@@ -25,5 +39,356 @@ __device__ __forceinline__ int seq_of_row(const int32_t* q_off, int n_seqs, int 
   }
   return lo < n_seqs && q_off[0] <= t ? lo : -1;
 }
+
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kCoarse = 512;   // prefix-sum entries
+
+struct AttnParams {
+  lora_paged_kv_t kv;
+  const bf16* q;
+  int64_t q_stride, out_stride;
+  bf16* out;
+  const int32_t *group_off, *prefix_len;
+  int n_groups;
+  bool groups_phase;   // problems are the prefix groups (else the sequences)
+  int group;           // query heads of a key head
+  int n_q_heads;
+  float scale_log2;    // scale * log2(e)
+  int window, n_sink;
+  int max_row_tiles;   // row tiles that the counters are laid out for
+  int min_share;       // units a CTA takes at least
+  uint32_t* err;
+  uint32_t* count;     // arrivals per item, zero between calls
+  float* part;         // [CTA][2][kRows][D] partial sums
+  float* part_ml;      // [CTA][2][kRows][2] their maxima (log2 units) and sums
+  float* prior;        // [T][n_q_heads][D] the prefix phase's result, fp32
+  float* prior_lse;    // [T][n_q_heads] its log2-sum-exp
+};
+
+// One problem.
+struct Problem {
+  int tok0, n_rows;    // first token, rows over all row tiles
+  int base;            // position of the first token (sequences)
+  int k_lo, k_hi;
+  int table_row;
+};
+
+// One row tile's view.  Keys [vis_lo, vis_hi] and the first n_sink are those
+// that some row sees; key tile i of n_tiles is i < sink_tiles ? i : tile_lo +
+// i - sink_tiles.  n_tiles >= 1 unless the row tile has nothing to write.
+struct RowTile {
+  int row0, n_rows;
+  int vis_lo, vis_hi, n_sink;
+  int tile_lo, sink_tiles, n_tiles;
+};
+
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
+  return x < lo ? lo : x > hi ? hi : x;
+}
+
+// The group of sequence s (0 .. n_groups - 1), or -1.
+__device__ __forceinline__ int group_of_seq(const AttnParams& P, int s) {
+  int lo = 0, hi = P.n_groups;  // group_off[lo] <= s < group_off[hi], if in any
+  if (s >= P.group_off[hi]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (P.group_off[mid] <= s) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int key_cap(const AttnParams& P) { return P.kv.max_pages * P.kv.page_size; }
+
+// Positions [0, shared_keys) of sequence s are attended in the prefix phase.
+__device__ __forceinline__ int shared_keys(const AttnParams& P, int s) {
+  if (P.n_groups == 0) return 0;
+  const int g = group_of_seq(P, s);
+  return g < 0 ? 0 : clamp_int(P.prefix_len[g], 0, key_cap(P));
+}
+
+// Tokens [*t0, *t1) of problem p.
+__device__ __forceinline__ void problem_tokens(const AttnParams& P, int p, int* t0, int* t1) {
+  int s0 = p, s1 = p + 1;
+  if (P.groups_phase) {
+    s0 = P.group_off[p], s1 = P.group_off[p + 1];
+    if (s0 < 0 || s1 < s0 || s1 > P.kv.n_seqs) {
+      flag_error(P.err, LORA_DEVERR_BAD_LEN);
+      *t0 = *t1 = 0;
+      return;
+    }
+    if (P.prefix_len[p] <= 0) s1 = s0;
+  }
+  int a = P.kv.q_off[s0], b = P.kv.q_off[s1];
+  if (a < 0 || b < a || b > P.kv.T) {
+    flag_error(P.err, LORA_DEVERR_BAD_LEN);
+    a = b = 0;
+  }
+  *t0 = a;
+  *t1 = b;
+}
+
+template <int kRows>
+__device__ __forceinline__ int problem_row_tiles(const AttnParams& P, int p) {
+  int a, b;
+  problem_tokens(P, p, &a, &b);
+  return ((b - a) * P.group + kRows - 1) / kRows;
+}
+
+__device__ __forceinline__ Problem load_problem(const AttnParams& P, int p) {
+  Problem r;
+  int b;
+  problem_tokens(P, p, &r.tok0, &b);
+  r.n_rows = (b - r.tok0) * P.group;
+  const int cap = key_cap(P);
+  if (P.groups_phase) {
+    r.table_row = P.group_off[p];
+    r.base = 0;
+    r.k_lo = 0;
+    r.k_hi = P.prefix_len[p];
+    if (r.k_hi > cap) {
+      flag_error(P.err, LORA_DEVERR_BAD_LEN);
+      r.k_hi = cap;
+    }
+    return r;
+  }
+  r.table_row = p;
+  int len = P.kv.kv_len[p];
+  if (len > cap) {
+    flag_error(P.err, LORA_DEVERR_BAD_LEN);
+    len = cap;
+  }
+  len = len < -(1 << 24) ? -(1 << 24) : len;
+  r.base = len - (b - r.tok0);
+  r.k_lo = shared_keys(P, p);
+  if (r.k_lo > 0 && b > r.tok0 && r.k_lo > r.base) flag_error(P.err, LORA_DEVERR_BAD_LEN);
+  r.k_hi = len;
+  return r;
+}
+
+template <int kRows>
+__device__ __forceinline__ RowTile row_tile(const AttnParams& P, const Problem& pr, int rt) {
+  RowTile t;
+  t.row0 = rt * kRows;
+  t.n_rows = min(kRows, pr.n_rows - t.row0);
+  if (P.groups_phase) {
+    t.vis_lo = 0;
+    t.vis_hi = pr.k_hi - 1;
+    t.n_sink = t.sink_tiles = t.tile_lo = 0;
+    t.n_tiles = (pr.k_hi + kKeys - 1) / kKeys;
+    return t;
+  }
+  const int first = pr.base + t.row0 / P.group;
+  t.vis_hi = min(pr.base + (t.row0 + t.n_rows - 1) / P.group, pr.k_hi - 1);
+  t.vis_lo = P.window > 0 ? max(first - P.window + 1, 0) : 0;
+  t.vis_lo = max(t.vis_lo, pr.k_lo);
+  t.n_sink = P.window > 0 ? max(min(P.n_sink, t.vis_hi + 1), 0) : 0;
+  t.tile_lo = t.vis_lo / kKeys;
+  t.sink_tiles = min((t.n_sink + kKeys - 1) / kKeys, t.tile_lo);
+  t.n_tiles = t.sink_tiles + (t.vis_hi >= t.vis_lo ? t.vis_hi / kKeys - t.tile_lo + 1 : 0);
+  if (t.n_tiles < 1) t.n_tiles = 1;
+  return t;
+}
+
+__device__ __forceinline__ int key_tile(const RowTile& t, int i) {
+  return i < t.sink_tiles ? i : t.tile_lo + i - t.sink_tiles;
+}
+
+// The prefix sums in shared memory.
+struct Schedule {
+  int64_t units[kCoarse + 1];  // key tiles before coarse entry e of row tiles
+  int tiles[kCoarse + 1];      // row tiles before coarse entry e of problems
+  int n_prob, per_prob;        // problems, problems of a coarse entry
+  int n_tiles, per_tile;       // row tiles, row tiles of a coarse entry
+  int64_t total, share;        // units of the call, units of a CTA
+};
+
+// Exclusive prefix sums of v[0 .. kCoarse) in place by one warp, the sum in
+// v[kCoarse].
+template <typename T>
+__device__ __forceinline__ void warp_scan_coarse(T* v) {
+  constexpr int kPer = kCoarse / 32;
+  const int lane = threadIdx.x & 31;
+  T x[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    x[i] = v[lane * kPer + i];
+    sum += x[i];
+  }
+  T incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  T run = incl - sum;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    v[lane * kPer + i] = run;
+    run += x[i];
+  }
+  if (lane == 31) v[kCoarse] = run;
+}
+
+// A place in the list of row tiles.
+struct Cursor {
+  int tile;      // row tile, counted over all problems
+  int prob, rt;  // its problem, and its number in it
+  Problem pr;
+};
+
+template <int kRows>
+__device__ __forceinline__ Cursor seek_tile(const AttnParams& P, const Schedule& S, int tile) {
+  int lo = 0, hi = kCoarse;  // tiles[lo] <= tile < tiles[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (S.tiles[mid] <= tile) lo = mid; else hi = mid;
+  }
+  Cursor c;
+  c.tile = tile;
+  c.prob = lo * S.per_prob;
+  c.rt = tile - S.tiles[lo];
+  for (;;) {
+    const int n = problem_row_tiles<kRows>(P, c.prob);
+    if (c.rt < n || c.prob + 1 >= S.n_prob) break;
+    c.rt -= n;
+    ++c.prob;
+  }
+  c.pr = load_problem(P, c.prob);
+  return c;
+}
+
+// The next row tile; the caller knows that there is one.
+template <int kRows>
+__device__ __forceinline__ void next_tile(const AttnParams& P, const Schedule& S, Cursor* c) {
+  ++c->tile;
+  ++c->rt;
+  if (static_cast<int64_t>(c->rt) * kRows < c->pr.n_rows) return;
+  c->rt = 0;
+  while (c->prob + 1 < S.n_prob) {
+    ++c->prob;
+    if (problem_row_tiles<kRows>(P, c->prob) > 0) break;
+  }
+  c->pr = load_problem(P, c->prob);
+}
+
+// All threads of the CTA; ends with a barrier.
+template <int kRows>
+__device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule& S) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
+  const int per_prob = (n_prob + kCoarse - 1) / kCoarse;
+  for (int e = tid; e < kCoarse; e += nt) {
+    int n = 0;
+    for (int p = e * per_prob; p < min(n_prob, (e + 1) * per_prob); ++p)
+      n += problem_row_tiles<kRows>(P, p);
+    S.tiles[e] = n;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    warp_scan_coarse(S.tiles);
+    if (tid == 31) {
+      // more rows than T allows (lengths out of order): the rest is dropped
+      int n = S.tiles[kCoarse];
+      if (n > P.max_row_tiles) {
+        flag_error(P.err, LORA_DEVERR_BAD_LEN);
+        n = P.max_row_tiles;
+      }
+      S.n_prob = n_prob;
+      S.per_prob = per_prob;
+      S.n_tiles = n;
+      S.per_tile = (n + kCoarse - 1) / kCoarse;
+    }
+  }
+  __syncthreads();
+  const int per_tile = S.per_tile, n_tiles = S.n_tiles;
+  for (int e = tid; e < kCoarse; e += nt) {
+    int64_t n = 0;
+    const int j0 = e * per_tile, j1 = min(n_tiles, j0 + per_tile);
+    if (j0 < j1) {
+      Cursor c = seek_tile<kRows>(P, S, j0);
+      for (;;) {
+        n += row_tile<kRows>(P, c.pr, c.rt).n_tiles;
+        if (c.tile + 1 >= j1) break;
+        next_tile<kRows>(P, S, &c);
+      }
+    }
+    S.units[e] = n;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    warp_scan_coarse(S.units);
+    if (tid == 31) {
+      S.total = S.units[kCoarse] * P.kv.n_kv_heads;
+      const int64_t even = (S.total + gridDim.x - 1) / gridDim.x;
+      S.share = even > P.min_share ? even : P.min_share;
+    }
+  }
+  __syncthreads();
+}
+
+// What a CTA does next: key tiles [tile0, tile0 + n) of an item.
+struct Segment {
+  int n;             // key tiles; 0: the CTA is done
+  int first;         // the item's number of the first of them
+  int head;          // key head
+  int table_row, tok0, base, k_lo;
+  int shared;        // the rows have a prior part from the prefix phase
+  RowTile t;
+  int item;          // its counter
+  int cta0, parts;   // the CTAs that share the item: cta0 .. cta0 + parts - 1
+  int slot;          // where this CTA's part goes, if parts > 1
+};
+
+// Walks a CTA's share (one warp, all lanes alike).
+template <int kRows>
+struct Walker {
+  Cursor c;
+  RowTile t;
+  int64_t u, end;    // next unit, end of the share
+  int64_t tile_unit; // first unit of the row tile
+
+  __device__ __forceinline__ void start(const AttnParams& P, const Schedule& S) {
+    u = S.share * blockIdx.x;
+    end = u + S.share < S.total ? u + S.share : S.total;
+    if (u >= end) return;
+    const int hk = P.kv.n_kv_heads;
+    int lo = 0, hi = kCoarse;  // units[lo] * hk <= u < units[hi] * hk
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (S.units[mid] * hk <= u) lo = mid; else hi = mid;
+    }
+    c = seek_tile<kRows>(P, S, lo * S.per_tile);
+    tile_unit = S.units[lo] * hk;
+    t = row_tile<kRows>(P, c.pr, c.rt);
+    while (tile_unit + static_cast<int64_t>(t.n_tiles) * hk <= u) advance(P, S);
+  }
+  __device__ __forceinline__ void advance(const AttnParams& P, const Schedule& S) {
+    tile_unit += static_cast<int64_t>(t.n_tiles) * P.kv.n_kv_heads;
+    next_tile<kRows>(P, S, &c);
+    t = row_tile<kRows>(P, c.pr, c.rt);
+  }
+  __device__ __forceinline__ Segment next(const AttnParams& P, const Schedule& S) {
+    Segment g;
+    g.n = 0;
+    if (u >= end) return g;
+    while (tile_unit + static_cast<int64_t>(t.n_tiles) * P.kv.n_kv_heads <= u) advance(P, S);
+    g.head = static_cast<int>((u - tile_unit) / t.n_tiles);
+    const int64_t a = tile_unit + static_cast<int64_t>(g.head) * t.n_tiles, b = a + t.n_tiles;
+    g.first = static_cast<int>(u - a);
+    g.n = static_cast<int>((end < b ? end : b) - u);
+    g.table_row = c.pr.table_row;
+    g.tok0 = c.pr.tok0;
+    g.base = c.pr.base;
+    g.k_lo = c.pr.k_lo;
+    g.shared = c.pr.k_lo > 0 ? 1 : 0;
+    g.t = t;
+    g.item = c.tile * P.kv.n_kv_heads + g.head;
+    g.cta0 = static_cast<int>(a / S.share);
+    g.parts = static_cast<int>((b - 1) / S.share) - g.cta0 + 1;
+    g.slot = blockIdx.x == g.cta0 ? 1 : 0;
+    u += g.n;
+    return g;
+  }
+};
 
 }  // namespace lora

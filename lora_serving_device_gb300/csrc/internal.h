@@ -142,6 +142,10 @@ bool encode_tensor_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, ui
 // d2, box box0 x box1 x 1; elements outside the tensor read as zero.
 bool encode_tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1,
                                uint64_t d2, uint32_t box0, uint32_t box1);
+// 4-D bf16 tensor map with 128-byte swizzle and any strides (bytes, of the
+// three outer dimensions); elements outside the tensor read as zero.
+bool encode_tensor_map_bf16_4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
+                               const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 // SGMV shrink on tensor cores (bf16, r in {64, 128}), see k_sgmv_tc.cu; the
 // same contract as launch_sgmv_shrink.  With `fold` (sgmv_shrink_tc_items
 // zeroed words) and ksplit > 1, split 0 of vpart ends as the sum of all

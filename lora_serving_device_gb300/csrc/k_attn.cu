@@ -1,93 +1,109 @@
-// Attention over the paged cache (lora_attn_paged, lora_attn_prefix), one
-// warp to a (row, query head): the lanes hold head_dim / 32 values of q and
-// of the accumulator, keys are taken one by one, the softmax runs along with
-// a running maximum and sum.  The definition, executed.
+// Host side of the attention over the paged cache: workspace, tensor maps,
+// choice of kernels.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "attn.cuh"
 
 namespace lora {
+
+cudaError_t launch_attn_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                               const AttnParams& P, int rows, cudaStream_t st,
+                               const DeviceInfo& dev);
+
 namespace {
 
-constexpr int kWarps = 4;
+// Rows of a key head that the longest run of new tokens has.
+int64_t rows_of(int64_t tokens, int group) { return (tokens > 1 ? tokens : 1) * group; }
+// Row-tile size for that many rows.
+int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(const lora_paged_kv_t kv,
-                                                           const AttnArgs a, uint32_t* err) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(w / a.n_q_heads), h = static_cast<int>(w % a.n_q_heads);
-  if (t >= kv.T) return;
-  const int s = seq_of_row(kv.q_off, kv.n_seqs, t);
-  if (s < 0) return;
-  const int hk = h / (a.n_q_heads / kv.n_kv_heads);
-  const int64_t cap = static_cast<int64_t>(kv.max_pages) * kv.page_size;
-  int p = kv.kv_len[s] - kv.q_off[s + 1] + t;
-  if (p >= cap) {
-    flag_error(err, LORA_DEVERR_BAD_LEN);
-    p = static_cast<int>(cap) - 1;
-  }
-  int shared_row = s, shared = 0;
-  if (a.group_off != nullptr) {
-    int g = seq_of_row(a.group_off, a.n_groups, s);
-    if (g >= 0) {
-      const int before = kv.kv_len[s] - (kv.q_off[s + 1] - kv.q_off[s]);
-      shared = a.prefix_len[g];
-      shared_row = a.group_off[g];
-      if (shared > before) flag_error(err, LORA_DEVERR_BAD_LEN);
-    }
-  }
-  float q[kPer], acc[kPer];
-  const bf16* qp = static_cast<const bf16*>(a.q) + t * a.q_stride + h * D + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = __bfloat162float(qp[i]) * a.scale;
-    acc[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int lo = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-  for (int j = lo > 0 && a.n_sink > 0 ? 0 : lo; j <= p; ++j) {
-    if (j < lo && j >= a.n_sink) j = lo;
-    const int row = j < shared ? shared_row : s;
-    const int page = kv.block_table[static_cast<int64_t>(row) * kv.max_pages + j / kv.page_size];
-    float dot = 0.f, v[kPer];
-    const bool ok = page >= 0 && page < kv.n_pages;
-    if (!ok) flag_error(err, LORA_DEVERR_BAD_PAGE);
-    const int64_t at =
-        ok ? ((static_cast<int64_t>(page) * kv.n_kv_heads + hk) * kv.page_size + j % kv.page_size) * D +
-                 lane * kPer
-           : 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      dot += ok ? q[i] * __bfloat162float(static_cast<const bf16*>(kv.k_cache)[at + i]) : 0.f;
-      v[i] = ok ? __bfloat162float(static_cast<const bf16*>(kv.v_cache)[at + i]) : 0.f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float m2 = fmaxf(m, dot), c = expf(m - m2), e = expf(dot - m2);
-    l = l * c + e;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * c + e * v[i];
-    m = m2;
-  }
-  bf16* o = static_cast<bf16*>(a.out) + t * a.out_stride + h * D + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = __float2bfloat16(l > 0.f ? acc[i] / l : 0.f);
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  size_t count, part, part_ml, prior, prior_lse, bytes;
+  int max_row_tiles[2];  // sequences, groups
+  int rows[2];
+};
+
+Layout layout(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
+  Layout w;
+  const int group = n_q_heads / kv.n_kv_heads;
+  const int64_t total = static_cast<int64_t>(kv.T) * group;
+  w.rows[0] = tile_rows(rows_of(kv.max_q_len < kv.T ? kv.max_q_len : kv.T, group));
+  w.rows[1] = tile_rows(rows_of(kv.T, group));
+  const int64_t t0 = total / w.rows[0] + kv.n_seqs, t1 = total / w.rows[1] + n_groups;
+  w.max_row_tiles[0] = static_cast<int>(t0);
+  w.max_row_tiles[1] = static_cast<int>(t1);
+  const int64_t tiles = n_groups > 0 && t1 > t0 ? t1 : t0;
+  const int rows = n_groups > 0 && w.rows[1] > w.rows[0] ? w.rows[1] : w.rows[0];
+  const size_t slots = static_cast<size_t>(kDecodeScheduleCtas) * 2 * rows;
+  w.count = 256;
+  w.part = up256(w.count + static_cast<size_t>(tiles) * kv.n_kv_heads * 4);
+  w.part_ml = w.part + slots * kv.head_dim * 4;
+  w.prior = up256(w.part_ml + slots * 8);
+  const size_t rows_all = n_groups > 0 ? static_cast<size_t>(kv.T) * n_q_heads : 0;
+  w.prior_lse = w.prior + rows_all * kv.head_dim * 4;
+  w.bytes = up256(w.prior_lse + rows_all * 4);
+  return w;
+}
+
+// One cache as [groups of 8 rows][64-value halves of a head][8 rows][64
+// values], the order in which a box lands in shared memory: eight rows of 128
+// bytes are one atom of the 128-byte swizzle, the halves of a head are
+// neighbours, pages and boxes of any height follow one another evenly.
+bool encode_cache_map(CUtensorMap* m, void* base, const lora_paged_kv_t& kv) {
+  const uint64_t d = kv.head_dim;
+  const uint64_t groups =
+      static_cast<uint64_t>(kv.n_pages) * kv.n_kv_heads * (kv.page_size / 8);
+  const uint64_t dims[4] = {64, 8, d / 64, groups};
+  const uint64_t strides[3] = {d * 2, 128, d * 16};
+  const uint32_t box[4] = {64, 8, static_cast<uint32_t>(d / 64),
+                           static_cast<uint32_t>((kv.page_size < kKeys ? kv.page_size : kKeys) / 8)};
+  return encode_tensor_map_bf16_4d(m, base, dims, strides, box);
 }
 
 }  // namespace
 
-size_t attn_ws_bytes(const lora_paged_kv_t&, int, int) { return 16; }
+size_t attn_ws_bytes(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
+  return layout(kv, n_q_heads, n_groups).bytes;
+}
 
 cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st,
-                        const DeviceInfo&) {
-  const int64_t warps = static_cast<int64_t>(kv.T) * a.n_q_heads;
-  const dim3 grid(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
-  uint32_t* err = static_cast<uint32_t*>(a.ws);
-  if (kv.head_dim == 64)
-    attn_kernel<64><<<grid, kWarps * 32, 0, st>>>(kv, a, err);
-  else
-    attn_kernel<128><<<grid, kWarps * 32, 0, st>>>(kv, a, err);
-  return cudaGetLastError();
+                        const DeviceInfo& dev) {
+  CUtensorMap tm_k, tm_v;
+  if (!encode_cache_map(&tm_k, kv.k_cache, kv) || !encode_cache_map(&tm_v, kv.v_cache, kv))
+    return cudaErrorInvalidValue;
+  const Layout w = layout(kv, a.n_q_heads, a.n_groups);
+  uint8_t* base = static_cast<uint8_t*>(a.ws);
+  AttnParams P = {};
+  P.kv = kv;
+  P.q = static_cast<const bf16*>(a.q);
+  P.q_stride = a.q_stride;
+  P.out = static_cast<bf16*>(a.out);
+  P.out_stride = a.out_stride;
+  P.group_off = a.group_off;
+  P.prefix_len = a.prefix_len;
+  P.n_groups = a.n_groups;
+  P.group = a.n_q_heads / kv.n_kv_heads;
+  P.n_q_heads = a.n_q_heads;
+  P.scale_log2 = a.scale * 1.4426950408889634f;
+  P.window = a.window;
+  P.n_sink = a.n_sink;
+  P.min_share = 2;
+  P.err = static_cast<uint32_t*>(a.ws);
+  P.count = reinterpret_cast<uint32_t*>(base + w.count);
+  P.part = reinterpret_cast<float*>(base + w.part);
+  P.part_ml = reinterpret_cast<float*>(base + w.part_ml);
+  P.prior = reinterpret_cast<float*>(base + w.prior);
+  P.prior_lse = reinterpret_cast<float*>(base + w.prior_lse);
+  for (int phase = a.n_groups > 0 ? 1 : 0; phase >= 0; --phase) {
+    P.groups_phase = phase == 1;
+    P.max_row_tiles = w.max_row_tiles[phase];
+    const cudaError_t e = launch_attn_decode(tm_k, tm_v, P, w.rows[phase], st, dev);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace lora

@@ -307,9 +307,17 @@ def test_prefix_of_many_rows(L):
 
 
 def test_prefix_longer_than_a_context_is_reported(L):
+    import torch
     groups = ([0, 3], [50])
     c = Case([1, 1, 1], [60, 50, 20], 4, 2, 64, 16, seed=3, groups=groups)
-    prefix_attend(L, c, groups, err=L.DEVERR_BAD_LEN)
+    kv = c.kv(L)
+    ws = L.attn_workspace(kv, c.hq, n_groups=1)
+    off, pl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in groups)
+    got = L.attn_prefix_t(kv, c.q, off, pl, ws, out=c.out).double().cpu().numpy()
+    assert L.get_error_t(ws) == L.DEVERR_BAD_LEN
+    ref, wv = R.attention(c.q_host, [k.double().numpy() for k in c.rows_k],
+                          [v.double().numpy() for v in c.rows_v], c.q_off, c.kv_len, c.d ** -0.5)
+    assert np.all(np.abs(got - ref)[:2] <= U * np.abs(ref[:2]) + (U + 2.0 ** -12) * wv[:2])
 
 
 # ------------------------------------------------------------------ append
