@@ -5,14 +5,14 @@
 // block-table row over the keys [k_lo, k_hi): a sequence, or a prefix group
 // (all its sequences' tokens against the shared prefix).  Its rows, (token,
 // query head of one key head), are packed token-major and cut into row tiles
-// of kRows; a row tile sees some 128-key tiles.  An item is (row tile, key
+// of P.rows; a row tile sees some 128-key tiles.  An item is (row tile, key
 // head); a unit is one key tile of an item.  All units, numbered row tile by
 // row tile, key head by key head, are cut into equal contiguous shares, one
 // per CTA, whatever the lengths are (they live on the device).  An item that
 // several CTAs share is finished by the last of them to arrive, which adds
 // their parts in CTA order: the result is a function of the lengths alone.
-// Each CTA computes the shares itself, from prefix sums of at most kCoarse
-// coarse entries in shared memory.
+// Each CTA computes the shares itself, from prefix sums over kCoarse coarse
+// entries in shared memory.
 #pragma once
 
 #include "attn.h"
@@ -41,7 +41,6 @@ __device__ __forceinline__ int seq_of_row(const int32_t* q_off, int n_seqs, int 
 }
 
 constexpr int kKeys = 128;     // keys of a tile
-constexpr int kCoarse = 512;   // prefix-sum entries
 
 struct AttnParams {
   lora_paged_kv_t kv;
@@ -52,15 +51,17 @@ struct AttnParams {
   int n_groups;
   bool groups_phase;   // problems are the prefix groups (else the sequences)
   int group;           // query heads of a key head
+  int rows;            // rows of a row tile
+  int lg_page;         // log2 of the page size
   int n_q_heads;
   float scale_log2;    // scale * log2(e)
   int window, n_sink;
   int max_row_tiles;   // row tiles that the counters are laid out for
   int min_share;       // units a CTA takes at least
   uint32_t* err;
-  uint32_t* count;     // arrivals per item, zero between calls
-  float* part;         // [CTA][2][kRows][D] partial sums
-  float* part_ml;      // [CTA][2][kRows][2] their maxima (log2 units) and sums
+  uint32_t* count;     // arrivals per item (per half of one: prefill), zero between calls
+  float* part;         // [CTA][2][row tile] partial sums
+  float* part_ml;      // [CTA][2][rows][2] their maxima (log2 units) and sums
   float* prior;        // [T][n_q_heads][D] the prefix phase's result, fp32
   float* prior_lse;    // [T][n_q_heads] its log2-sum-exp
 };
@@ -127,11 +128,10 @@ __device__ __forceinline__ void problem_tokens(const AttnParams& P, int p, int* 
   *t1 = b;
 }
 
-template <int kRows>
 __device__ __forceinline__ int problem_row_tiles(const AttnParams& P, int p) {
   int a, b;
   problem_tokens(P, p, &a, &b);
-  return ((b - a) * P.group + kRows - 1) / kRows;
+  return ((b - a) * P.group + P.rows - 1) / P.rows;
 }
 
 __device__ __forceinline__ Problem load_problem(const AttnParams& P, int p) {
@@ -165,11 +165,10 @@ __device__ __forceinline__ Problem load_problem(const AttnParams& P, int p) {
   return r;
 }
 
-template <int kRows>
 __device__ __forceinline__ RowTile row_tile(const AttnParams& P, const Problem& pr, int rt) {
   RowTile t;
-  t.row0 = rt * kRows;
-  t.n_rows = min(kRows, pr.n_rows - t.row0);
+  t.row0 = rt * P.rows;
+  t.n_rows = min(P.rows, pr.n_rows - t.row0);
   if (P.groups_phase) {
     t.vis_lo = 0;
     t.vis_hi = pr.k_hi - 1;
@@ -194,7 +193,9 @@ __device__ __forceinline__ int key_tile(const RowTile& t, int i) {
 }
 
 // The prefix sums in shared memory.
+template <int C>
 struct Schedule {
+  static constexpr int kCoarse = C;  // a multiple of 32
   int64_t units[kCoarse + 1];  // key tiles before coarse entry e of row tiles
   int tiles[kCoarse + 1];      // row tiles before coarse entry e of problems
   int n_prob, per_prob;        // problems, problems of a coarse entry
@@ -204,7 +205,7 @@ struct Schedule {
 
 // Exclusive prefix sums of v[0 .. kCoarse) in place by one warp, the sum in
 // v[kCoarse].
-template <typename T>
+template <int kCoarse, typename T>
 __device__ __forceinline__ void warp_scan_coarse(T* v) {
   constexpr int kPer = kCoarse / 32;
   const int lane = threadIdx.x & 31;
@@ -236,9 +237,9 @@ struct Cursor {
   Problem pr;
 };
 
-template <int kRows>
-__device__ __forceinline__ Cursor seek_tile(const AttnParams& P, const Schedule& S, int tile) {
-  int lo = 0, hi = kCoarse;  // tiles[lo] <= tile < tiles[hi]
+template <int C>
+__device__ __forceinline__ Cursor seek_tile(const AttnParams& P, const Schedule<C>& S, int tile) {
+  int lo = 0, hi = C;  // tiles[lo] <= tile < tiles[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (S.tiles[mid] <= tile) lo = mid; else hi = mid;
@@ -248,7 +249,7 @@ __device__ __forceinline__ Cursor seek_tile(const AttnParams& P, const Schedule&
   c.prob = lo * S.per_prob;
   c.rt = tile - S.tiles[lo];
   for (;;) {
-    const int n = problem_row_tiles<kRows>(P, c.prob);
+    const int n = problem_row_tiles(P, c.prob);
     if (c.rt < n || c.prob + 1 >= S.n_prob) break;
     c.rt -= n;
     ++c.prob;
@@ -258,37 +259,37 @@ __device__ __forceinline__ Cursor seek_tile(const AttnParams& P, const Schedule&
 }
 
 // The next row tile; the caller knows that there is one.
-template <int kRows>
-__device__ __forceinline__ void next_tile(const AttnParams& P, const Schedule& S, Cursor* c) {
+template <int C>
+__device__ __forceinline__ void next_tile(const AttnParams& P, const Schedule<C>& S, Cursor* c) {
   ++c->tile;
   ++c->rt;
-  if (static_cast<int64_t>(c->rt) * kRows < c->pr.n_rows) return;
+  if (static_cast<int64_t>(c->rt) * P.rows < c->pr.n_rows) return;
   c->rt = 0;
   while (c->prob + 1 < S.n_prob) {
     ++c->prob;
-    if (problem_row_tiles<kRows>(P, c->prob) > 0) break;
+    if (problem_row_tiles(P, c->prob) > 0) break;
   }
   c->pr = load_problem(P, c->prob);
 }
 
 // All threads of the CTA; ends with a barrier.
-template <int kRows>
-__device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule& S) {
+template <int C>
+__device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule<C>& S) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
-  const int per_prob = (n_prob + kCoarse - 1) / kCoarse;
-  for (int e = tid; e < kCoarse; e += nt) {
+  const int per_prob = (n_prob + C - 1) / C;
+  for (int e = tid; e < C; e += nt) {
     int n = 0;
     for (int p = e * per_prob; p < min(n_prob, (e + 1) * per_prob); ++p)
-      n += problem_row_tiles<kRows>(P, p);
+      n += problem_row_tiles(P, p);
     S.tiles[e] = n;
   }
   __syncthreads();
   if (tid < 32) {
-    warp_scan_coarse(S.tiles);
+    warp_scan_coarse<C>(S.tiles);
     if (tid == 31) {
       // more rows than T allows (lengths out of order): the rest is dropped
-      int n = S.tiles[kCoarse];
+      int n = S.tiles[C];
       if (n > P.max_row_tiles) {
         flag_error(P.err, LORA_DEVERR_BAD_LEN);
         n = P.max_row_tiles;
@@ -296,29 +297,29 @@ __device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule& S)
       S.n_prob = n_prob;
       S.per_prob = per_prob;
       S.n_tiles = n;
-      S.per_tile = (n + kCoarse - 1) / kCoarse;
+      S.per_tile = (n + C - 1) / C;
     }
   }
   __syncthreads();
   const int per_tile = S.per_tile, n_tiles = S.n_tiles;
-  for (int e = tid; e < kCoarse; e += nt) {
+  for (int e = tid; e < C; e += nt) {
     int64_t n = 0;
     const int j0 = e * per_tile, j1 = min(n_tiles, j0 + per_tile);
     if (j0 < j1) {
-      Cursor c = seek_tile<kRows>(P, S, j0);
+      Cursor c = seek_tile(P, S, j0);
       for (;;) {
-        n += row_tile<kRows>(P, c.pr, c.rt).n_tiles;
+        n += row_tile(P, c.pr, c.rt).n_tiles;
         if (c.tile + 1 >= j1) break;
-        next_tile<kRows>(P, S, &c);
+        next_tile(P, S, &c);
       }
     }
     S.units[e] = n;
   }
   __syncthreads();
   if (tid < 32) {
-    warp_scan_coarse(S.units);
+    warp_scan_coarse<C>(S.units);
     if (tid == 31) {
-      S.total = S.units[kCoarse] * P.kv.n_kv_heads;
+      S.total = S.units[C] * P.kv.n_kv_heads;
       const int64_t even = (S.total + gridDim.x - 1) / gridDim.x;
       S.share = even > P.min_share ? even : P.min_share;
     }
@@ -340,34 +341,34 @@ struct Segment {
 };
 
 // Walks a CTA's share (one warp, all lanes alike).
-template <int kRows>
+template <int C>
 struct Walker {
   Cursor c;
   RowTile t;
   int64_t u, end;    // next unit, end of the share
   int64_t tile_unit; // first unit of the row tile
 
-  __device__ __forceinline__ void start(const AttnParams& P, const Schedule& S) {
+  __device__ __forceinline__ void start(const AttnParams& P, const Schedule<C>& S) {
     u = S.share * blockIdx.x;
     end = u + S.share < S.total ? u + S.share : S.total;
     if (u >= end) return;
     const int hk = P.kv.n_kv_heads;
-    int lo = 0, hi = kCoarse;  // units[lo] * hk <= u < units[hi] * hk
+    int lo = 0, hi = C;  // units[lo] * hk <= u < units[hi] * hk
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (S.units[mid] * hk <= u) lo = mid; else hi = mid;
     }
-    c = seek_tile<kRows>(P, S, lo * S.per_tile);
+    c = seek_tile(P, S, lo * S.per_tile);
     tile_unit = S.units[lo] * hk;
-    t = row_tile<kRows>(P, c.pr, c.rt);
+    t = row_tile(P, c.pr, c.rt);
     while (tile_unit + static_cast<int64_t>(t.n_tiles) * hk <= u) advance(P, S);
   }
-  __device__ __forceinline__ void advance(const AttnParams& P, const Schedule& S) {
+  __device__ __forceinline__ void advance(const AttnParams& P, const Schedule<C>& S) {
     tile_unit += static_cast<int64_t>(t.n_tiles) * P.kv.n_kv_heads;
-    next_tile<kRows>(P, S, &c);
-    t = row_tile<kRows>(P, c.pr, c.rt);
+    next_tile(P, S, &c);
+    t = row_tile(P, c.pr, c.rt);
   }
-  __device__ __forceinline__ Segment next(const AttnParams& P, const Schedule& S) {
+  __device__ __forceinline__ Segment next(const AttnParams& P, const Schedule<C>& S) {
     Segment g;
     g.n = 0;
     if (u >= end) return g;

@@ -36,7 +36,7 @@ lora_status_t check_kv(const lora_paged_kv_t* kv) {
 // rows that do not overlap.
 lora_status_t check_rows(const void* p, int64_t stride, const lora_paged_kv_t& kv, int heads) {
   if (p == nullptr || !aligned16(p)) return LORA_ERR_INVALID_ARG;
-  if (stride % 8 != 0 || stride > (int64_t{1} << 40) ||
+  if (stride % 8 != 0 || stride > (int64_t{1} << 38) ||
       stride < static_cast<int64_t>(heads) * kv.head_dim)
     return LORA_ERR_SHAPE;
   return LORA_OK;

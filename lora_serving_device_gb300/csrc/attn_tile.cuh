@@ -101,81 +101,54 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, ui
       : "memory");
 }
 
-// The producer warp: walks the CTA's share, publishes its segments in the
-// ring and brings in K and V of their key tiles, a box per page (or per 128
-// rows of a larger one), page ids looked up by a lane each, a tile ahead.
-// Pages that no row sees are not touched.  A page that is missing is asked for
-// past the cache's end, where the tensor map reads zeros.
-// M: full_k, full_v, empty [kStages], ring, seg_full, seg_empty [kRing].
-template <int kRows, int D, int kStages, int kRing, class Mi>
-__device__ __forceinline__ void produce_tiles(const AttnParams& P, Mi& M, uint8_t* smem,
-                                              uint32_t stage_bytes, uint32_t v_offset,
-                                              const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                              volatile int* abort) {
-  const int lane = threadIdx.x & 31;
-  const int page = P.kv.page_size, box = page < kKeys ? page : kKeys;
-  const int lg_page = 31 - __clz(page);
-  const int boxes = kKeys / box;
-  const uint32_t box_bytes = static_cast<uint32_t>(box) * D * 2;
-  Walker<kRows> walk;
-  walk.start(P, M.sched);
-  int tile = 0;
-  bool ok = true;
-  for (int sg = 0; ok; ++sg) {
-    const Segment g = walk.next(P, M.sched);
-    if (sg >= kRing)
-      ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort);
-    if (!ok) break;
-    if (lane == 0) {
-      M.ring[sg % kRing] = g;
-      ptx::mbar_arrive(&M.seg_full[sg % kRing]);
-    }
-    __syncwarp();
-    if (g.n == 0) break;
-    const int32_t* row = P.kv.block_table + static_cast<int64_t>(g.table_row) * P.kv.max_pages;
-    // this lane's box of the segment's i-th tile: where it starts in the
-    // cache, in groups of eight rows; -1: not needed
-    auto lookup = [&](int i) {
-      const int key0 = key_tile(g.t, g.first + i) * kKeys + lane * box;
-      if (lane >= boxes || !((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) ||
-                             key0 < g.t.n_sink))
-        return -1;
-      const int id = row[key0 >> lg_page];
-      if (id < 0 || id >= P.kv.n_pages) {
-        flag_error(P.err, LORA_DEVERR_BAD_PAGE);
-        return P.kv.n_pages * P.kv.n_kv_heads * (page / 8);
-      }
-      return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (key0 & (page - 1)) / 8;
-    };
-    int at = lookup(0);
-    for (int i = 0; i < g.n; ++i, ++tile) {
-      const int here = at;
-      if (i + 1 < g.n) at = lookup(i + 1);
-      const int st = tile % kStages;
-      if (tile >= kStages) ok = wait_all(&M.empty[st], ((tile / kStages) & 1) ^ 1, abort);
-      if (!ok) break;
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here >= 0)) * box_bytes;
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&M.full_k[st], bytes);
-        ptx::mbar_arrive_expect_tx(&M.full_v[st], bytes);
-      }
-      __syncwarp();
-      if (here >= 0) {
-        uint8_t* K = smem + st * stage_bytes + lane * box_bytes;
-        tma_load_4d(K, tm_k, &M.full_k[st], here);
-        tma_load_4d(K + v_offset, tm_v, &M.full_v[st], here);
-      }
-    }
-  }
-  if (!ok) {
-    // gave up: what is on its way into shared memory has to land first
-    int none = 0;
-    for (int k = tile > kStages ? tile - kStages : 0; k < tile; ++k) {
-      ptx::mbar_wait_bounded(&M.full_k[k % kStages], (k / kStages) & 1, &none, kAttnWaitNs);
-      ptx::mbar_wait_bounded(&M.full_v[k % kStages], (k / kStages) & 1, &none, kAttnWaitNs);
-    }
-  }
+// c1 is the head, c2 the token, c3 the 64-value half of the head.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, uint64_t* bar,
+                                              int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(ptx::smem_u32(dst)),
+      "l"(tm), "r"(ptx::smem_u32(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
+
+// Brings in the K or V rows of a key tile: a box per page (or per 128 rows of a
+// larger one), each box in the hands of a lane, which looks its page up.
+// Pages that no row sees are not touched.  A page that is missing is asked for
+// past the cache's end, where the tensor map reads zeros.  One warp.
+template <int D>
+struct TileLoader {
+  int page, lg_page, box, boxes;
+  __device__ __forceinline__ explicit TileLoader(const AttnParams& P)
+      : page(P.kv.page_size),
+        lg_page(P.lg_page),
+        box(page < kKeys ? page : kKeys),
+        boxes(kKeys / box) {}
+  // Where this lane's box of the segment's i-th tile starts in the cache, in
+  // groups of eight rows; -1: not needed.
+  __device__ __forceinline__ int lookup(const AttnParams& P, const Segment& g, int i) const {
+    const int lane = threadIdx.x & 31;
+    const int key0 = key_tile(g.t, g.first + i) * kKeys + lane * box;
+    if (lane >= boxes || !((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) ||
+                           key0 < g.t.n_sink))
+      return -1;
+    const int id =
+        P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages + (key0 >> lg_page)];
+    if (id < 0 || id >= P.kv.n_pages) {
+      flag_error(P.err, LORA_DEVERR_BAD_PAGE);
+      return P.kv.n_pages * P.kv.n_kv_heads * (page / 8);
+    }
+    return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (key0 & (page - 1)) / 8;
+  }
+  __device__ __forceinline__ void load(const CUtensorMap* tm, uint64_t* full, uint8_t* dst,
+                                       int at) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t bytes = static_cast<uint32_t>(box) * D * 2;
+    const uint32_t all = __popc(__ballot_sync(0xffffffffu, at >= 0)) * bytes;
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full, all);
+    __syncwarp();
+    if (at >= 0) tma_load_4d(dst + lane * bytes, tm, full, at);
+  }
+};
 
 // Value d of row n of a finished item: o / sum.  The prefix phase keeps it in
 // fp32 with its log-sum-exp (log2 units, m + log2 sum); otherwise it is joined
@@ -204,24 +177,76 @@ __device__ __forceinline__ void write_row(const AttnParams& P, const Segment& g,
   P.out[t * P.out_stride + h * D + d] = __float2bfloat16_rn(x);
 }
 
+// The same for a thread that holds a whole row, eight values at a time.
+template <int D>
+struct RowWriter {
+  float own, other;  // factors of this result and of the prior part
+  bf16* out;
+  float* prior;
+  bool to_prior, join;
+  __device__ __forceinline__ RowWriter(const AttnParams& P, const Segment& g, int n, float m,
+                                       float sum) {
+    const int r = g.t.row0 + n;
+    const int64_t t = g.tok0 + r / P.group;
+    const int h = g.head * P.group + r % P.group;
+    to_prior = P.groups_phase;
+    join = !to_prior && g.shared;
+    own = sum > 0.f ? 1.f / sum : 0.f;
+    other = 0.f;
+    out = P.out + t * P.out_stride + h * D;
+    const int64_t at = t * P.n_q_heads + h;
+    prior = P.prior + at * D;
+    if ((to_prior || join) && n < g.t.n_rows) {
+      const float lse = sum > 0.f ? m + log2f(sum) : -INFINITY;
+      if (to_prior) {
+        P.prior_lse[at] = lse;
+      } else {
+        const float lp = P.prior_lse[at], top = fmaxf(lse, lp);
+        if (top > -INFINITY) {
+          const float a = exp2f(lse - top), b = exp2f(lp - top);
+          own *= a / (a + b);
+          other = b / (a + b);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void write8(int d, const float* x) const {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * own;
+    if (to_prior) {
+      store8(prior + d, y);
+      return;
+    }
+    if (join) {
+      float z[8];
+      load8(prior + d, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += other * z[i];
+    }
+    store8(out + d, y);
+  }
+};
+
 // The slot of the item's c-th part.
 __device__ __forceinline__ int64_t part_slot(const Segment& g, int c) {
   return static_cast<int64_t>(g.cta0 + c) * 2 + (c == 0 ? 1 : 0);
 }
 
 // Threads of named barrier `bar` (cnt of them) have written this CTA's part:
-// is it the item's last?  Leaves the item's counter at zero.
-__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, bool leader,
-                                               int* flag, int bar, int cnt) {
+// is it the last of the item (or of its half)?  Leaves the counter at zero.
+__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, int counter,
+                                               bool leader, int* flag, int bar, int cnt) {
   __threadfence();
   named_bar(bar, cnt);
   if (leader) {
-    const uint32_t before = atomicAdd(&P.count[g.item], 1u);
+    const uint32_t before = atomicAdd(&P.count[counter], 1u);
     *flag = before + 1 == static_cast<uint32_t>(g.parts) ? 1 : 0;
-    if (*flag) P.count[g.item] = 0;
+    if (*flag) P.count[counter] = 0;
     __threadfence();
   }
   named_bar(bar, cnt);
+  __threadfence();
   return *flag != 0;
 }
 

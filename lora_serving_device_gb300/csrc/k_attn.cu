@@ -8,38 +8,54 @@
 namespace lora {
 
 cudaError_t launch_attn_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                               const AttnParams& P, int rows, cudaStream_t st,
-                               const DeviceInfo& dev);
+                               const AttnParams& P, cudaStream_t st, const DeviceInfo& dev);
+cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                const CUtensorMap& tm_v, const AttnParams& P, cudaStream_t st,
+                                const DeviceInfo& dev);
 
 namespace {
 
-// Rows of a key head that the longest run of new tokens has.
-int64_t rows_of(int64_t tokens, int group) { return (tokens > 1 ? tokens : 1) * group; }
-// Row-tile size for that many rows.
-int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// The kernel of a phase, by the rows of a key head that the longest run of
+// new tokens has: up to 64 the keys stand in the MMA's M and the rows (16, 32
+// or 64 of them) in N; above, the rows stand in M, in two halves of whole
+// tokens.
+struct Shape {
+  bool prefill;
+  int rows;   // of a row tile
+  int space;  // rows that a part of one has room for
+};
+Shape shape_of(int64_t tokens, int group) {
+  const int64_t rows = (tokens > 1 ? tokens : 1) * group;
+  if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256};
+  const int n = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return {false, n, n};
+}
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
   size_t count, part, part_ml, prior, prior_lse, bytes;
   int max_row_tiles[2];  // sequences, groups
-  int rows[2];
+  Shape shape[2];
 };
 
 Layout layout(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
   Layout w;
   const int group = n_q_heads / kv.n_kv_heads;
   const int64_t total = static_cast<int64_t>(kv.T) * group;
-  w.rows[0] = tile_rows(rows_of(kv.max_q_len < kv.T ? kv.max_q_len : kv.T, group));
-  w.rows[1] = tile_rows(rows_of(kv.T, group));
-  const int64_t t0 = total / w.rows[0] + kv.n_seqs, t1 = total / w.rows[1] + n_groups;
-  w.max_row_tiles[0] = static_cast<int>(t0);
-  w.max_row_tiles[1] = static_cast<int>(t1);
-  const int64_t tiles = n_groups > 0 && t1 > t0 ? t1 : t0;
-  const int rows = n_groups > 0 && w.rows[1] > w.rows[0] ? w.rows[1] : w.rows[0];
-  const size_t slots = static_cast<size_t>(kDecodeScheduleCtas) * 2 * rows;
+  w.shape[0] = shape_of(kv.max_q_len < kv.T ? kv.max_q_len : kv.T, group);
+  w.shape[1] = shape_of(kv.T, group);
+  int64_t items = 0;
+  int space = 0;
+  for (int i = 0; i < (n_groups > 0 ? 2 : 1); ++i) {
+    const int64_t tiles = total / w.shape[i].rows + (i == 0 ? kv.n_seqs : n_groups);
+    w.max_row_tiles[i] = static_cast<int>(tiles);
+    if (2 * tiles > items) items = 2 * tiles;
+    if (w.shape[i].space > space) space = w.shape[i].space;
+  }
+  const size_t slots = static_cast<size_t>(kDecodeScheduleCtas) * 2 * space;
   w.count = 256;
-  w.part = up256(w.count + static_cast<size_t>(tiles) * kv.n_kv_heads * 4);
+  w.part = up256(w.count + static_cast<size_t>(items) * kv.n_kv_heads * 4);
   w.part_ml = w.part + slots * kv.head_dim * 4;
   w.prior = up256(w.part_ml + slots * 8);
   const size_t rows_all = n_groups > 0 ? static_cast<size_t>(kv.T) * n_q_heads : 0;
@@ -63,6 +79,17 @@ bool encode_cache_map(CUtensorMap* m, void* base, const lora_paged_kv_t& kv) {
   return encode_tensor_map_bf16_4d(m, base, dims, strides, box);
 }
 
+// q as [64-value halves][tokens][heads][64 values]: a box is whole tokens' query
+// heads of one key head, rows of 128 bytes.
+bool encode_q_map(CUtensorMap* m, const AttnArgs& a, const lora_paged_kv_t& kv, int group) {
+  const uint64_t d = kv.head_dim;
+  const uint64_t dims[4] = {64, static_cast<uint64_t>(a.n_q_heads), static_cast<uint64_t>(kv.T),
+                            d / 64};
+  const uint64_t strides[3] = {d * 2, static_cast<uint64_t>(a.q_stride) * 2, 128};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(group), static_cast<uint32_t>(128 / group), 1};
+  return encode_tensor_map_bf16_4d(m, a.q, dims, strides, box);
+}
+
 }  // namespace
 
 size_t attn_ws_bytes(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
@@ -71,7 +98,7 @@ size_t attn_ws_bytes(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
 
 cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st,
                         const DeviceInfo& dev) {
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_q, tm_k, tm_v;
   if (!encode_cache_map(&tm_k, kv.k_cache, kv) || !encode_cache_map(&tm_v, kv.v_cache, kv))
     return cudaErrorInvalidValue;
   const Layout w = layout(kv, a.n_q_heads, a.n_groups);
@@ -87,10 +114,10 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.n_groups = a.n_groups;
   P.group = a.n_q_heads / kv.n_kv_heads;
   P.n_q_heads = a.n_q_heads;
+  P.lg_page = 31 - __builtin_clz(static_cast<unsigned>(kv.page_size));
   P.scale_log2 = a.scale * 1.4426950408889634f;
   P.window = a.window;
   P.n_sink = a.n_sink;
-  P.min_share = 2;
   P.err = static_cast<uint32_t*>(a.ws);
   P.count = reinterpret_cast<uint32_t*>(base + w.count);
   P.part = reinterpret_cast<float*>(base + w.part);
@@ -100,7 +127,15 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   for (int phase = a.n_groups > 0 ? 1 : 0; phase >= 0; --phase) {
     P.groups_phase = phase == 1;
     P.max_row_tiles = w.max_row_tiles[phase];
-    const cudaError_t e = launch_attn_decode(tm_k, tm_v, P, w.rows[phase], st, dev);
+    P.rows = w.shape[phase].rows;
+    P.min_share = 2;
+    cudaError_t e;
+    if (w.shape[phase].prefill) {
+      if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;
+      e = launch_attn_prefill(tm_q, tm_k, tm_v, P, st, dev);
+    } else {
+      e = launch_attn_decode(tm_k, tm_v, P, st, dev);
+    }
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -32,6 +32,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 192;
+constexpr int kCoarse = 512;  // entries of the schedule's prefix sums
 constexpr int kRing = 4;  // segments that the producer may run ahead
 
 template <int D, int N>
@@ -49,7 +50,7 @@ struct Lay {
 
 template <int N, int kStages>
 struct Misc {
-  Schedule sched;
+  Schedule<kCoarse> sched;
   Segment ring[kRing];
   float red[4][N];       // per warp maxima or sums
   float m[N], fac[N];    // reference maxima (log2 units), rescale factors
@@ -112,14 +113,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  build_schedule<N>(P, M.sched);  // ends with a barrier
+  build_schedule(P, M.sched);  // ends with a barrier
   ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;
   const uint32_t tmem_o = tmem + 2 * N;
 
   if (warp == 0) {
     // ---------------- schedule and TMA ----------------------------------
-    produce_tiles<N, D, kStages, kRing>(P, M, smem, La::kStage, La::kTile, &tm_k, &tm_v, abort_f);
+    Walker<kCoarse> walk;
+    walk.start(P, M.sched);
+    const TileLoader<D> load(P);
+    int tile = 0;
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      const Segment g = walk.next(P, M.sched);
+      if (sg >= kRing)
+        ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
+      if (!ok) break;
+      if (lane == 0) {
+        M.ring[sg % kRing] = g;
+        ptx::mbar_arrive(&M.seg_full[sg % kRing]);
+      }
+      __syncwarp();
+      if (g.n == 0) break;
+      int at = load.lookup(P, g, 0);  // page ids a tile ahead
+      for (int i = 0; i < g.n; ++i, ++tile) {
+        const int here = at;
+        if (i + 1 < g.n) at = load.lookup(P, g, i + 1);
+        const int st = tile % kStages;
+        if (tile >= kStages) ok = wait_all(&M.empty[st], ((tile / kStages) & 1) ^ 1, abort_f);
+        if (!ok) break;
+        uint8_t* K = smem + st * La::kStage;
+        load.load(&tm_k, &M.full_k[st], K, here);
+        load.load(&tm_v, &M.full_v[st], K + La::kTile, here);
+      }
+    }
+    if (!ok) {
+      // gave up: what is on its way into shared memory has to land first
+      int none = 0;
+      for (int k = tile > kStages ? tile - kStages : 0; k < tile; ++k) {
+        ptx::mbar_wait_bounded(&M.full_k[k % kStages], (k / kStages) & 1, &none, kAttnWaitNs / 8);
+        ptx::mbar_wait_bounded(&M.full_v[k % kStages], (k / kStages) & 1, &none, kAttnWaitNs / 8);
+      }
+    }
   } else if (warp == 1) {
     // ---------------- MMA issue ------------------------------------------
     // Two cursors over the same tiles: S of tile qk as soon as its K is
@@ -404,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ml[0] = M.m[n];
           ml[1] = M.red[0][n] + M.red[1][n] + M.red[2][n] + M.red[3][n];
         }
-        if (last_to_arrive(P, g, st_tid == 0, &M.last, kBar, 128)) {
+        if (last_to_arrive(P, g, g.item, st_tid == 0, &M.last, kBar, 128)) {
           for (int n = st_tid; n < g.t.n_rows; n += 128)
             merged_max<N>(P, g, n, &M.m[n], &M.red[0][n]);
           named_bar(kBar, 128);
@@ -431,7 +467,8 @@ template <int D, int N>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, AttnParams P, cudaStream_t st,
                    const DeviceInfo& dev) {
   using La = Lay<D, N>;
-  const size_t smem = 1024 + La::oMisc + sizeof(Misc<N, La::kStages>);
+  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<N, La::kStages>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
   if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
   auto kern = attn_decode_kernel<D, N>;
   cudaError_t e =
@@ -453,15 +490,14 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, AttnParams 
 }  // namespace
 
 cudaError_t launch_attn_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                               const AttnParams& P, int rows, cudaStream_t st,
-                               const DeviceInfo& dev) {
+                               const AttnParams& P, cudaStream_t st, const DeviceInfo& dev) {
   if (P.kv.head_dim == 64) {
-    if (rows == 16) return launch<64, 16>(tm_k, tm_v, P, st, dev);
-    if (rows == 32) return launch<64, 32>(tm_k, tm_v, P, st, dev);
+    if (P.rows == 16) return launch<64, 16>(tm_k, tm_v, P, st, dev);
+    if (P.rows == 32) return launch<64, 32>(tm_k, tm_v, P, st, dev);
     return launch<64, 64>(tm_k, tm_v, P, st, dev);
   }
-  if (rows == 16) return launch<128, 16>(tm_k, tm_v, P, st, dev);
-  if (rows == 32) return launch<128, 32>(tm_k, tm_v, P, st, dev);
+  if (P.rows == 16) return launch<128, 16>(tm_k, tm_v, P, st, dev);
+  if (P.rows == 32) return launch<128, 32>(tm_k, tm_v, P, st, dev);
   return launch<128, 64>(tm_k, tm_v, P, st, dev);
 }
 

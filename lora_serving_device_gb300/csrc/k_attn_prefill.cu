@@ -1,0 +1,502 @@
+// Attention over the paged cache for many rows per key head: prompts, chunks
+// of prompts and the tokens of a prefix group (lora_attn_paged and the prefix
+// phase of lora_attn_prefix).
+//
+// Mathematics, per item (two halves of up to 128 rows of one key head) and
+// key tile of 128 keys, for each half:
+//   S  = Q K^T             [128 rows, 128 keys]   tcgen05, fp32 in tensor memory
+//   P  = 2^(S c - m)       c = scale log2(e), m the row's reference maximum
+//   l += row sums of P
+//   O += P V               [128 rows, D]          tcgen05, P bf16 from tensor memory
+// m is moved (and l, O scaled) only where a score exceeds it by more than 8 in
+// log2 units, so the usual tile leaves O alone.  P is rounded to bf16, the type
+// the MMA takes beside V; l sums the unrounded values in fp32.
+//
+// Bound by the tensor cores: 4 x 128 x 128 x D operations a half and tile.
+// The two halves alternate: while one half's softmax runs on its warpgroup,
+// the tensor cores work for the other.  A softmax thread owns one row (a
+// tensor-memory lane), so maximum and sum need no exchange; P overwrites S in
+// tensor memory and never passes through shared memory.  Rows are (token,
+// query head of the key head), so all query heads of a key head share each
+// K and V tile; a half holds whole tokens, which lets TMA fetch Q too.
+//
+// Warps: 0-3 softmax of half 0, 4-7 of half 1 (and their results), 8 schedule
+// and TMA, 9 MMA issue.  Every wait is bounded; on timeout the kernel raises
+// LORA_DEVERR_TIMEOUT.
+#include <cudaTypedefs.h>
+
+#include "attn.cuh"
+#include "attn_tile.cuh"
+#include "ptx.cuh"
+
+namespace lora {
+namespace {
+
+// Three warpgroups: the softmax threads hold a row of 128 scores each and take
+// registers from the third, of which two warps work.  208 x 256 + 88 x 128 is
+// within the launch's 168 x 384.
+constexpr int kThreads = 384;
+constexpr int kRegsMost = 208, kRegsLeast = 88;
+constexpr int kCoarse = 96;  // entries of the schedule's prefix sums
+constexpr int kRing = 4;     // segments that the producer may run ahead
+constexpr int kHalf = 128;   // rows of a half in the MMA
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t kTile = kKeys * D * 2;  // K or V of a tile, Q of a half
+  static constexpr int kSlots = D == 128 ? 5 : 10;  // K and V tiles in flight
+  static constexpr uint32_t oQ = kSlots * kTile;
+  static constexpr uint32_t oMisc = oQ + 2 * kTile;
+};
+
+template <int kSlots>
+struct Misc {
+  Schedule<kCoarse> sched;
+  Segment ring[kRing];
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
+  uint64_t seg_full[kRing], seg_empty[kRing];
+  uint32_t tmem;
+  int abort;
+  int last[2];
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Part of a row tile, [slot][half][D / 4][128 rows][4]: neighbouring threads
+// (rows) write neighbouring vectors.
+template <int D>
+__device__ __forceinline__ float4* part_row(const AttnParams& P, int64_t slot, int half, int row) {
+  return reinterpret_cast<float4*>(P.part) + (slot * 2 + half) * (D / 4) * kHalf + row;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
+  using La = Lay<D>;
+  constexpr int kSlots = La::kSlots;
+  using Mi = Misc<kSlots>;
+  constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kHalf, kKeys, false, false);
+  constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kHalf, D, false, true);
+  constexpr uint32_t kGroupBytes = (D / 64) * 1024;  // eight keys
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Mi& M = *reinterpret_cast<Mi*>(smem + La::oMisc);
+  volatile int* abort_f = &M.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int half_rows = P.rows / 2;  // rows of a half that are in use
+
+  if (tid == 0) {
+    ptx::prefetch_tmap(&tm_q);
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(&M.full[i], 1);
+      ptx::mbar_init(&M.empty[i], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      ptx::mbar_init(&M.q_full[h], 1);
+      ptx::mbar_init(&M.q_empty[h], 1);
+      ptx::mbar_init(&M.s_full[h], 1);
+      ptx::mbar_init(&M.p_full[h], 4);
+      ptx::mbar_init(&M.o_done[h], 1);
+      ptx::mbar_init(&M.o_empty[h], 4);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      ptx::mbar_init(&M.seg_full[i], 1);
+      ptx::mbar_init(&M.seg_empty[i], 9);
+    }
+    M.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&M.tmem, 512);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  build_schedule(P, M.sched);  // ends with a barrier
+  ptx::tc_fence_after();
+  const uint32_t tmem = M.tmem;  // S (and P) of half h at h * 128, O at 256 + h * 128
+
+  // (each role's branch begins with its own split, so that the compiler knows
+  // the number of registers on every path)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLeast));
+  if (warp == 8) {
+    // ---------------- schedule and TMA ----------------------------------
+    Walker<kCoarse> walk;
+    walk.start(P, M.sched);
+    const TileLoader<D> load(P);
+    int n = 0;              // tiles brought in: K in slot 2n, V in slot 2n + 1
+    int q_use[2] = {0, 0};  // segments of each half
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      const Segment g = walk.next(P, M.sched);
+      if (sg >= kRing)
+        ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
+      if (!ok) break;
+      if (lane == 0) {
+        M.ring[sg % kRing] = g;
+        ptx::mbar_arrive(&M.seg_full[sg % kRing]);
+      }
+      __syncwarp();
+      if (g.n == 0) break;
+      int at = load.lookup(P, g, 0);
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (g.t.n_rows <= h * half_rows) break;
+        if (q_use[h] > 0) ok = wait_all(&M.q_empty[h], (q_use[h] - 1) & 1, abort_f);
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&M.q_full[h], half_rows * D * 2);
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_rows(smem + La::oQ + h * La::kTile + x * (kHalf * 128), &tm_q, &M.q_full[h],
+                          g.head * P.group, g.tok0 + (g.t.row0 + h * half_rows) / P.group, x);
+        }
+        ++q_use[h];
+      }
+      __syncwarp();
+      for (int i = 0; i < g.n && ok; ++i, ++n) {
+        const int here = at;
+        if (i + 1 < g.n) at = load.lookup(P, g, i + 1);
+        for (int v = 0; v < 2; ++v) {
+          const int k = 2 * n + v, st = k % kSlots;
+          if (k >= kSlots) ok = wait_all(&M.empty[st], ((k / kSlots) & 1) ^ 1, abort_f);
+          if (!ok) break;
+          load.load(v ? &tm_v : &tm_k, &M.full[st], smem + st * La::kTile, here);
+        }
+      }
+    }
+    if (!ok) {
+      // gave up: what is on its way into shared memory has to land first
+      int none = 0;
+      for (int h = 0; h < 2; ++h)
+        if (q_use[h] > 0)
+          ptx::mbar_wait_bounded(&M.q_full[h], (q_use[h] - 1) & 1, &none, kAttnWaitNs / 8);
+      for (int k = 2 * n > kSlots ? 2 * n - kSlots : 0; k < 2 * n; ++k)
+        ptx::mbar_wait_bounded(&M.full[k % kSlots], (k / kSlots) & 1, &none, kAttnWaitNs / 8);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issue ------------------------------------------
+    // P V of tile n and Q K^T of tile n + 1, half by half
+    int segs[2] = {0, 0};   // segments of each half so far
+    int tiles[2] = {0, 0};  // tiles of each half whose P V was issued
+    bool ok = true;
+    auto issue_qk = [&](const Segment& g, int i, int n, int h) {
+      if (i == 0) {
+        ok &= wait_all(&M.q_full[h], segs[h] & 1, abort_f);
+        ++segs[h];
+      }
+      const int k = 2 * n, st = k % kSlots;
+      ok &= wait_all(&M.full[st], (k / kSlots) & 1, abort_f);
+      ptx::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t qa = ptx::smem_u32(smem + La::oQ + h * La::kTile);
+        const uint32_t ka = ptx::smem_u32(smem + st * La::kTile);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          // Q: [64-value half of a head][128 rows][64]
+          const uint64_t qd = ptx::sdesc_sw128(
+              qa + (ks / 4) * (kHalf * 128) + (ks % 4) * 32, 16, 1024);
+          const uint64_t kd =
+              ptx::sdesc_sw128(ka + (ks / 4) * 1024 + (ks % 4) * 32, 16, kGroupBytes);
+          ptx::mma_bf16(tmem + h * 128, qd, kd, kIdescQK, ks > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(&M.s_full[h]);
+        if (i == g.n - 1) ptx::mma_commit(&M.q_empty[h]);
+        if (h == 1 || g.t.n_rows <= half_rows) ptx::mma_commit(&M.empty[st]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](const Segment& g, int i, int n, int h) {
+      const int k = 2 * n + 1, st = k % kSlots;
+      uint8_t* V = smem + st * La::kTile;
+      if (h == 0) {
+        ok &= wait_all(&M.full[st], (k / kSlots) & 1, abort_f);
+        if (ok) zero_unseen_values<D>(g.t, key_tile(g.t, g.first + i), V);
+      }
+      ok &= wait_all(&M.p_full[h], tiles[h] & 1, abort_f);
+      // the half's previous segment has been read out of O
+      if (i == 0 && segs[h] > 1) ok &= wait_all(&M.o_empty[h], segs[h] & 1, abort_f);
+      ptx::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t va = ptx::smem_u32(V);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks) {
+          const uint64_t vd = ptx::sdesc_sw128(va + ks * 2 * kGroupBytes, 1024, kGroupBytes);
+          ptx::mma_bf16_ta(tmem + 256 + h * 128, tmem + h * 128 + ks * 8, vd, kIdescPV,
+                           i > 0 || ks > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(&M.o_done[h]);
+        if (h == 1 || g.t.n_rows <= half_rows) ptx::mma_commit(&M.empty[st]);
+      }
+      __syncwarp();
+      ++tiles[h];
+    };
+    ok = wait_all(&M.seg_full[0], 0, abort_f);
+    int sg = 0, n = 0;
+    if (ok && M.ring[0].n > 0) {
+      for (int h = 0; h < 2; ++h)
+        if (M.ring[0].t.n_rows > h * half_rows) issue_qk(M.ring[0], 0, 0, h);
+    }
+    for (int i = 0; ok; ++n) {
+      const Segment& g = M.ring[sg % kRing];
+      if (g.n == 0) break;
+      const bool turn = i == g.n - 1;  // the next tile is of the next segment
+      if (turn) ok = wait_all(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
+      if (!ok) break;
+      const Segment& x = M.ring[(turn ? sg + 1 : sg) % kRing];
+      const int xi = turn ? 0 : i + 1;
+      for (int h = 0; h < 2 && ok; ++h) {
+        // (the count of segments that issue_pv looks at is this segment's)
+        if (g.t.n_rows > h * half_rows) issue_pv(g, i, n, h);
+        if (ok && x.n > 0 && x.t.n_rows > h * half_rows) issue_qk(x, xi, n + 1, h);
+      }
+      if (turn) {
+        if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+        ++sg;
+      }
+      i = xi;
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMost));
+    // ---------------- softmax and results ---------------------------------
+    const int h = warp >> 2, w = warp & 3;
+    const int row = w * 32 + lane;  // of the half, and the TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const uint32_t tm_s = tmem + lanes + h * 128, tm_o = tmem + lanes + 256 + h * 128;
+    const float c = P.scale_log2;
+    const int bar = 1 + h;
+    int tile = 0;  // tiles of this half so far
+    bool ok = true;
+    // the warpgroup's four warps meet at barriers: after a wait that gave up
+    // they run on (every later wait returns at once) to the vote
+    for (int sg = 0;; ++sg) {
+      ok &= wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (named_any(bar, 128, !ok)) break;
+      const Segment g = M.ring[sg % kRing];
+      if (g.n == 0) break;
+      const int n_rows = min(g.t.n_rows - h * half_rows, half_rows);  // of this half
+      if (n_rows <= 0) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+        continue;
+      }
+      // rows past the last copy the first one's limits
+      const int pos =
+          g.base + (g.t.row0 + h * half_rows + (row < n_rows ? row : 0)) / P.group;
+      const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
+      const int lo =
+          P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < g.n; ++i, ++tile) {
+        const int key0 = key_tile(g.t, g.first + i) * kKeys;
+        ok &= wait_all(&M.s_full[h], tile & 1, abort_f);
+        ptx::tc_fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int k = 0; k < kKeys; k += 32)
+          ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
+        ptx::tmem_ld_wait();
+        if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) {
+          const int top = hi - key0, bottom = lo - key0, sink = g.t.n_sink - key0;
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k)
+            if (k > top || (k < bottom && k >= sink)) s[k] = -INFINITY;
+        }
+        float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
+#pragma unroll
+        for (int k = 6; k + 3 < kKeys; k += 4) {
+          mx = max3(mx, s[k], s[k + 1]);
+          my = max3(my, s[k + 2], s[k + 3]);
+        }
+        mx = max3(mx, s[kKeys - 2], s[kKeys - 1]);
+        mx = fmaxf(mx, my) * c;
+        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+          const float now = fmaxf(m, mx);
+          const float f = m == -INFINITY ? 0.f : exp2_fast(m - now);
+          m = now;
+          l *= f;
+          if (i > 0) {
+            ok &= wait_all(&M.o_done[h], (tile - 1) & 1, abort_f);
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+              uint32_t o[32];
+              ptx::tmem_ld32(tm_o + k, o);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              ptx::tmem_st32(tm_o + k, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const uint64_t c2 = pack2(c, c), neg2 = pack2(neg, neg);
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int k = 0; k < kKeys; k += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float a, b;
+            unpack2(fma2(pack2(s[k + 2 * x], s[k + 2 * x + 1]), c2, neg2), &a, &b);
+            a = exp2_fast(a);
+            b = exp2_fast(b);
+            if (x & 1)
+              sum1 = add2(sum1, pack2(a, b));
+            else
+              sum0 = add2(sum0, pack2(a, b));
+            p[x] = pack_bf16x2(a, b);
+          }
+          ptx::tmem_st16(tm_s + k / 2, p);
+        }
+        float a, b;
+        unpack2(add2(sum0, sum1), &a, &b);
+        l += a + b;
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&M.p_full[h]);
+      }
+
+      // ---- the item, or this CTA's part of it, is done
+      ok &= wait_all(&M.o_done[h], (tile - 1) & 1, abort_f);
+      ptx::tc_fence_after();
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
+      const bool mine = row < n_rows;
+      RowWriter<D> out(P, g, h * half_rows + row, m, l);
+      float4* part = part_row<D>(P, slot, h, row);
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tm_o + k, o);
+        ptx::tmem_ld_wait();
+        if (!mine) continue;
+        const float* x = reinterpret_cast<const float*>(o);
+        if (g.parts > 1) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            part[(k / 4 + q) * kHalf] =
+                make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) out.write8(k + 8 * q, x + 8 * q);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&M.o_empty[h]);
+        ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+      }
+      if (g.parts > 1) {
+        float2* ml = reinterpret_cast<float2*>(P.part_ml);
+        if (mine) ml[slot * 2 * kHalf + h * kHalf + row] = make_float2(m, l);
+        if (last_to_arrive(P, g, g.item * 2 + h, row == 0, &M.last[h], bar, 128) && mine) {
+          float top = -INFINITY, sum = 0.f;
+          for (int q = 0; q < g.parts; ++q)
+            top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf + h * kHalf + row].x));
+          for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
+            const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf + h * kHalf + row]);
+            sum += exp2f(v.x - top) * v.y;
+          }
+          RowWriter<D> joined(P, g, h * half_rows + row, top, sum);
+#pragma unroll 1
+          for (int k = 0; k < D; k += 32) {
+            float o[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = 0.f;
+            for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
+              const float f =
+                  exp2f(__ldcg(&ml[part_slot(g, q) * 2 * kHalf + h * kHalf + row].x) - top);
+              const float4* from = part_row<D>(P, part_slot(g, q), h, row);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float4 v = __ldcg(from + (k / 4 + x) * kHalf);
+                o[4 * x] += f * v.x;
+                o[4 * x + 1] += f * v.y;
+                o[4 * x + 2] += f * v.z;
+                o[4 * x + 3] += f * v.w;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) joined.write8(k + 8 * q, o + 8 * q);
+          }
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_f) flag_error(P.err, LORA_DEVERR_TIMEOUT);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                   const AttnParams& P, cudaStream_t st, const DeviceInfo& dev) {
+  using La = Lay<D>;
+  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<La::kSlots>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
+  auto kern = attn_prefill_kernel<D>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kDecodeScheduleCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                const CUtensorMap& tm_v, const AttnParams& P, cudaStream_t st,
+                                const DeviceInfo& dev) {
+  return P.kv.head_dim == 64 ? launch<64>(tm_q, tm_k, tm_v, P, st, dev)
+                             : launch<128>(tm_q, tm_k, tm_v, P, st, dev);
+}
+
+}  // namespace lora
