@@ -6,9 +6,10 @@
 // (all its sequences' tokens against the shared prefix).  Its rows, (token,
 // query head of one key head), are packed token-major and cut into row tiles
 // of P.rows; a row tile sees some 128-key tiles.  An item is (row tile, key
-// head); a unit is one key tile of an item.  All units, numbered row tile by
-// row tile, key head by key head, are cut into equal contiguous shares, one
-// per CTA, whatever the lengths are (they live on the device).  An item that
+// head); its units are its key tiles, after P.over units that stand for the
+// cost of taking it up and finishing it.  All units, numbered row tile by row
+// tile, key head by key head, are cut into equal contiguous shares, one per
+// CTA, whatever the lengths are (they live on the device).  An item that
 // several CTAs share is finished by the last of them to arrive, which adds
 // their parts in CTA order: the result is a function of the lengths alone.
 // Each CTA computes the shares itself, from prefix sums over kCoarse coarse
@@ -53,6 +54,7 @@ struct AttnParams {
   int group;           // query heads of a key head
   int rows;            // rows of a row tile
   int lg_page;         // log2 of the page size
+  int over;            // units that an item costs beside its key tiles
   int n_q_heads;
   float scale_log2;    // scale * log2(e)
   int window, n_sink;
@@ -308,7 +310,7 @@ __device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule<C>&
     if (j0 < j1) {
       Cursor c = seek_tile(P, S, j0);
       for (;;) {
-        n += row_tile(P, c.pr, c.rt).n_tiles;
+        n += row_tile(P, c.pr, c.rt).n_tiles + P.over;
         if (c.tile + 1 >= j1) break;
         next_tile(P, S, &c);
       }
@@ -361,10 +363,13 @@ struct Walker {
     c = seek_tile(P, S, lo * S.per_tile);
     tile_unit = S.units[lo] * hk;
     t = row_tile(P, c.pr, c.rt);
-    while (tile_unit + static_cast<int64_t>(t.n_tiles) * hk <= u) advance(P, S);
+    while (tile_unit + units(P) <= u) advance(P, S);
+  }
+  __device__ __forceinline__ int64_t units(const AttnParams& P) const {  // of the row tile
+    return static_cast<int64_t>(t.n_tiles + P.over) * P.kv.n_kv_heads;
   }
   __device__ __forceinline__ void advance(const AttnParams& P, const Schedule<C>& S) {
-    tile_unit += static_cast<int64_t>(t.n_tiles) * P.kv.n_kv_heads;
+    tile_unit += units(P);
     next_tile(P, S, &c);
     t = row_tile(P, c.pr, c.rt);
   }
@@ -372,9 +377,13 @@ struct Walker {
     Segment g;
     g.n = 0;
     if (u >= end) return g;
-    while (tile_unit + static_cast<int64_t>(t.n_tiles) * P.kv.n_kv_heads <= u) advance(P, S);
-    g.head = static_cast<int>((u - tile_unit) / t.n_tiles);
-    const int64_t a = tile_unit + static_cast<int64_t>(g.head) * t.n_tiles, b = a + t.n_tiles;
+    while (tile_unit + units(P) <= u) advance(P, S);
+    const int span = t.n_tiles + P.over;
+    g.head = static_cast<int>((u - tile_unit) / span);
+    const int64_t a = tile_unit + static_cast<int64_t>(g.head) * span + P.over;
+    const int64_t b = a + t.n_tiles;
+    if (u < a) u = a;
+    if (u >= end) return g;  // the share ends in front of the item's key tiles
     g.first = static_cast<int>(u - a);
     g.n = static_cast<int>((end < b ? end : b) - u);
     g.table_row = c.pr.table_row;
@@ -384,8 +393,15 @@ struct Walker {
     g.shared = c.pr.k_lo > 0 ? 1 : 0;
     g.t = t;
     g.item = c.tile * P.kv.n_kv_heads + g.head;
-    g.cta0 = static_cast<int>(a / S.share);
-    g.parts = static_cast<int>((b - 1) / S.share) - g.cta0 + 1;
+    // (only key tiles make a CTA one of the item's)
+    const int64_t mine = S.share * blockIdx.x;
+    if (a >= mine && b <= mine + S.share) {
+      g.cta0 = blockIdx.x;
+      g.parts = 1;
+    } else {
+      g.cta0 = static_cast<int>(a / S.share);
+      g.parts = static_cast<int>((b - 1) / S.share) - g.cta0 + 1;
+    }
     g.slot = blockIdx.x == g.cta0 ? 1 : 0;
     u += g.n;
     return g;

@@ -48,7 +48,55 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
                   (!*abort && ptx::mbar_wait_bounded(bar, parity, abort, kAttnWaitNs));
   return __all_sync(0xffffffffu, ok);
 }
-// Bounds a polling loop in time: out() after each fruitless round.
+// One lane of a converged warp, in a form the compiler knows to be one thread.
+// A loop that runs wholly inside such a branch issues an MMA in ~20 cycles; in
+// one that lane 0 runs, or that a warp runs with a branch around the MMAs, each
+// takes ~55 (8 MMAs of 128 x 128 x 16 on an idle pipe: 175 against 435 to 470).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// Shared-memory matrix descriptors in halves: the low words hold the address
+// and the leading offset, the high words the stride and the 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | (((lbo_bytes >> 4) & 0x3FFFu) << 16);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes) {
+  return ((sbo_bytes >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29);
+}
+// D[tmem] (+)= A[smem] B[smem] and A[tmem] B[smem], descriptors in halves.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                       uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same without a vote, where no lane acts on the answer: once a wait of the
+// CTA gave up it returns at once.
+__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (!ptx::mbar_try_wait(bar, parity) && !*abort)
+    ptx::mbar_wait_bounded(bar, parity, abort, kAttnWaitNs);
+}
+// Bounds one thread's polling loop in time: out() after each fruitless round.
 struct Patience {
   uint32_t n = 0;
   uint64_t t0 = 0;
@@ -56,12 +104,10 @@ struct Patience {
   __device__ __forceinline__ bool out(volatile int* abort) {
     if (++n < 4096u) return false;
     if (n == 4096u) t0 = ptx::globaltimer_ns();
-    int stop = 0;
-    if ((n & 255u) == 0u) {
-      stop = *abort || ptx::globaltimer_ns() - t0 > kAttnWaitNs ? 1 : 0;
-      if (stop) *abort = 1;
-    }
-    return __any_sync(0xffffffffu, stop);
+    if ((n & 255u) != 0u) return false;
+    if (!*abort && ptx::globaltimer_ns() - t0 <= kAttnWaitNs) return false;
+    *abort = 1;
+    return true;
   }
 };
 
@@ -69,26 +115,23 @@ __device__ __forceinline__ bool tile_key_seen(const RowTile& t, int key) {
   return (key >= t.vis_lo && key <= t.vis_hi) || key < t.n_sink;
 }
 
-// The values of keys that no row of the tile sees are made zero in shared
-// memory (their weights are zero, but 0 * NaN is not); what was not loaded
-// too.  One warp, all lanes; V as the tensor map lays it out.
+// Whether a key tile holds keys that no row of the row tile sees.
+__device__ __forceinline__ bool tile_has_unseen(const RowTile& t, int key0) {
+  return key0 < t.vis_lo || key0 + kKeys - 1 > t.vis_hi;
+}
+// The values of key `j` of such a tile are made zero in shared memory if no row
+// sees the key (its weights are zero, but 0 * NaN is not): rows of the cache
+// past the length or before the window, and what was not loaded at all.  V as
+// the tensor map lays it out; the caller fences before the MMA reads it.
 template <int D>
-__device__ __forceinline__ void zero_unseen_values(const RowTile& t, int tile, uint8_t* V) {
-  const int key0 = tile * kKeys;
-  if (key0 >= t.vis_lo && key0 + kKeys - 1 <= t.vis_hi) return;
-  __syncwarp();
-  const int lane = threadIdx.x & 31;
-  for (int r = lane; r < kKeys; r += 32) {
-    if (tile_key_seen(t, key0 + r)) continue;
-    uint8_t* row = V + (r / 8) * (D / 64) * 1024 + (r % 8) * 128;
+__device__ __forceinline__ void zero_unseen_value(const RowTile& t, int key0, int j, uint8_t* V) {
+  if (tile_key_seen(t, key0 + j)) return;
+  uint8_t* row = V + (j / 8) * (D / 64) * 1024 + (j % 8) * 128;
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h)
+  for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        *reinterpret_cast<uint4*>(row + h * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
-  }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
+    for (int x = 0; x < 8; ++x)
+      *reinterpret_cast<uint4*>(row + h * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // 4-D tiled load (c0 innermost), completion counted in bytes on `bar`.
@@ -150,15 +193,12 @@ struct TileLoader {
   }
 };
 
-// Value d of row n of a finished item: o / sum.  The prefix phase keeps it in
-// fp32 with its log-sum-exp (log2 units, m + log2 sum); otherwise it is joined
-// with that part, if there is one, and rounded to out.
+// Value d of a finished row (token t, query head h): o / sum.  The prefix phase
+// keeps it in fp32 with its log-sum-exp (log2 units, m + log2 sum); otherwise
+// it is joined with that part, if there is one, and rounded to out.
 template <int D>
-__device__ __forceinline__ void write_row(const AttnParams& P, const Segment& g, int n, int d,
-                                          float o, float sum, float m) {
-  const int r = g.t.row0 + n;
-  const int64_t t = g.tok0 + r / P.group;
-  const int h = g.head * P.group + r % P.group;
+__device__ __forceinline__ void write_row(const AttnParams& P, const Segment& g, int64_t t, int h,
+                                          int d, float o, float sum, float m) {
   float x = sum > 0.f ? o / sum : 0.f;
   if (P.groups_phase || g.shared) {
     const float lse = sum > 0.f ? m + log2f(sum) : -INFINITY;
@@ -184,11 +224,8 @@ struct RowWriter {
   bf16* out;
   float* prior;
   bool to_prior, join;
-  __device__ __forceinline__ RowWriter(const AttnParams& P, const Segment& g, int n, float m,
-                                       float sum) {
-    const int r = g.t.row0 + n;
-    const int64_t t = g.tok0 + r / P.group;
-    const int h = g.head * P.group + r % P.group;
+  __device__ __forceinline__ RowWriter(const AttnParams& P, const Segment& g, int64_t t, int h,
+                                       bool in_use, float m, float sum) {
     to_prior = P.groups_phase;
     join = !to_prior && g.shared;
     own = sum > 0.f ? 1.f / sum : 0.f;
@@ -196,7 +233,7 @@ struct RowWriter {
     out = P.out + t * P.out_stride + h * D;
     const int64_t at = t * P.n_q_heads + h;
     prior = P.prior + at * D;
-    if ((to_prior || join) && n < g.t.n_rows) {
+    if ((to_prior || join) && in_use) {
       const float lse = sum > 0.f ? m + log2f(sum) : -INFINITY;
       if (to_prior) {
         P.prior_lse[at] = lse;
@@ -248,40 +285,6 @@ __device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segmen
   named_bar(bar, cnt);
   __threadfence();
   return *flag != 0;
-}
-
-// Maximum and sum of row n over the item's parts.
-template <int kRows>
-__device__ __forceinline__ void merged_max(const AttnParams& P, const Segment& g, int n, float* m,
-                                           float* sum) {
-  float top = -INFINITY, s = 0.f;
-  for (int c = 0; c < g.parts; ++c)
-    top = fmaxf(top, __ldcg(P.part_ml + (part_slot(g, c) * kRows + n) * 2));
-  if (top > -INFINITY) {
-    for (int c = 0; c < g.parts; ++c) {
-      const float2 ml =
-          __ldcg(reinterpret_cast<const float2*>(P.part_ml + (part_slot(g, c) * kRows + n) * 2));
-      s += exp2f(ml.x - top) * ml.y;
-    }
-  }
-  *m = top;
-  *sum = s;
-}
-
-// Value d of row n summed over the item's parts, in their order.
-template <int kRows, int D>
-__device__ __forceinline__ float merged_value(const AttnParams& P, const Segment& g, int n, int d,
-                                              float top) {
-  float o = 0.f;
-  if (top == -INFINITY) return o;
-#pragma unroll 4
-  for (int c = 0; c < g.parts; ++c) {
-    const int64_t row = part_slot(g, c) * kRows + n;
-    const float f = exp2f(__ldcg(P.part_ml + row * 2) - top);
-    // a part that saw nothing of this row holds 0 at most
-    o += f * __ldcg(P.part + row * D + d);
-  }
-  return o;
 }
 
 }  // namespace lora

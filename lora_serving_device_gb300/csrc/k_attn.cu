@@ -16,8 +16,8 @@ cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k
 namespace {
 
 // The kernel of a phase, by the rows of a key head that the longest run of
-// new tokens has: up to 64 the keys stand in the MMA's M and the rows (16, 32
-// or 64 of them) in N; above, the rows stand in M, in two halves of whole
+// new tokens has: up to 32 the keys stand in the MMA's M and the rows (4, 8,
+// 16 or 32 of them) in N; above, the rows stand in M, in two halves of whole
 // tokens.
 struct Shape {
   bool prefill;
@@ -26,8 +26,8 @@ struct Shape {
 };
 Shape shape_of(int64_t tokens, int group) {
   const int64_t rows = (tokens > 1 ? tokens : 1) * group;
-  if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256};
-  const int n = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  if (rows > 32 && group <= 128) return {true, 2 * (128 / group) * group, 256};
+  const int n = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   return {false, n, n};
 }
 
@@ -129,6 +129,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.max_row_tiles = w.max_row_tiles[phase];
     P.rows = w.shape[phase].rows;
     P.min_share = 2;
+    P.over = w.shape[phase].prefill ? 2 : 1;
     cudaError_t e;
     if (w.shape[phase].prefill) {
       if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;

@@ -2,11 +2,11 @@
 // and short runs of them (lora_attn_paged and both phases of
 // lora_attn_prefix).
 //
-// Mathematics, per item (kN rows of one key head) and key tile of 128 keys:
-//   S^T = K Q^T                     [128 keys, kN]   tcgen05, M = the keys
+// Mathematics, per item (up to A rows of one key head) and key tile of 128 keys:
+//   S^T = K Q^T                     [128 keys, A]    tcgen05, M = the keys
 //   P   = 2^(S c - m)               c = scale log2(e), m the reference maximum
 //   l  += column sums of P
-//   O^T += V^T [P_hi | P_lo]        [D, 2 kN]        tcgen05, M = head_dim
+//   O^T += V^T [P_hi | P_lo]        [D, 2 A]         tcgen05, M = head_dim
 // m is a row's maximum when it was last moved; it is moved (and l, O scaled)
 // only when a score exceeds it by more than 8 in log2 units, so P stays
 // below 2^8 and the usual tile costs no reduction over the keys at all, only
@@ -33,28 +33,32 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kCoarse = 512;  // entries of the schedule's prefix sums
-constexpr int kRing = 4;  // segments that the producer may run ahead
+constexpr int kRing = 4;      // segments that the producer may run ahead
 
-template <int D, int N>
+// A rows of a row tile: 4, 8, 16 or 32.  N is their number in Q K^T and kPV
+// the columns of P and O (A for the high halves from 0, A for the rest from
+// kPV / 2); the MMA wants at least 16.
+template <int D, int A>
 struct Lay {
+  static constexpr int N = A < 16 ? 16 : A;
+  static constexpr int kPV = A < 16 ? 16 : 2 * A;
   static constexpr uint32_t kTile = kKeys * D * 2;  // K or V of a tile
   static constexpr uint32_t kStage = 2 * kTile;
   static constexpr uint32_t kQ = N * D * 2;
-  static constexpr uint32_t kP = 2 * N * kKeys * 2;
-  static constexpr int kPBufs = N <= 16 ? 2 : 1;
-  static constexpr int kStages = (N <= 32 ? 196608u : 131072u) / kStage;
+  static constexpr uint32_t kP = kPV * kKeys * 2;
+  static constexpr int kPBufs = A <= 16 ? 2 : 1;
+  static constexpr int kStages = 196608u / kStage;
   static constexpr uint32_t oQ = kStages * kStage;
   static constexpr uint32_t oP = oQ + kQ;
   static constexpr uint32_t oMisc = oP + kPBufs * kP;
 };
 
-template <int N, int kStages>
+template <int A, int kStages>
 struct Misc {
   Schedule<kCoarse> sched;
   Segment ring[kRing];
-  float red[4][N];       // per warp maxima or sums
-  float m[N], fac[N];    // reference maxima (log2 units), rescale factors
-  int row_hi[N], row_lo[N];
+  float4 red[A];  // of a row: the four warps' maxima or sums
+  int row_hi[A], row_lo[A];
   uint64_t full_k[kStages], full_v[kStages], empty[kStages];
   uint64_t s_full[2], s_empty[2], p_full[2], p_done[2];
   uint64_t q_full, o_empty;
@@ -64,16 +68,17 @@ struct Misc {
   int last;
 };
 
-template <int D, int N>
+template <int D, int A>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
-  using La = Lay<D, N>;
+  using La = Lay<D, A>;
+  constexpr int N = La::N, kPV = La::kPV;
   constexpr int kStages = La::kStages, PB = La::kPBufs;
-  using Mi = Misc<N, kStages>;
-  constexpr uint32_t kCols = 4 * N < 32 ? 32 : 4 * N;  // S twice, O's two halves
+  using Mi = Misc<A, kStages>;
+  constexpr uint32_t kCols = 2 * N + kPV <= 64 ? 64 : 2 * N + kPV <= 128 ? 128 : 256;
   constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kKeys, N, false, false);
-  constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(D, 2 * N, true, false);
+  constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(D, kPV, true, false);
   constexpr uint32_t kGroupBytes = (D / 64) * 1024;  // eight keys
 
   extern __shared__ uint8_t smem_raw[];
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   build_schedule(P, M.sched);  // ends with a barrier
   ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;
-  const uint32_t tmem_o = tmem + 2 * N;
+  const uint32_t tmem_o = tmem + 2 * N;  // after two buffers of S
 
   if (warp == 0) {
     // ---------------- schedule and TMA ----------------------------------
@@ -158,94 +163,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMA issue ------------------------------------------
-    // Two cursors over the same tiles: S of tile qk as soon as its K is
-    // there, O += of tile pv as soon as its P is.  S runs at most two ahead.
-    int qk = 0, pv = 0;             // tiles issued
-    int qs = 0, ps = 0;             // their segments
-    int qi = 0, pi = 0;             // their numbers in them
-    int q_n = -1, p_n = -1;         // segment sizes, -1: not read yet
-    const uint32_t qa = ptx::smem_u32(smem + La::oQ);
-    Patience wait;
-    while (!(q_n == 0 && pv == qk)) {
-      int did = 0;
-      // segment headers
-      if (q_n < 0 && __all_sync(0xffffffffu, ptx::mbar_test_wait(&M.seg_full[qs % kRing],
-                                                                 (qs / kRing) & 1))) {
-        q_n = M.ring[qs % kRing].n;
-        did = 1;
-      }
-      if (pv < qk && p_n < 0) {
-        p_n = M.ring[ps % kRing].n;  // the other cursor has been here
-        did = 1;
-      }
-      int go = 0;
-      if (lane == 0) {
-        if (pv < qk && ptx::mbar_test_wait(&M.p_full[pv % PB], (pv / PB) & 1) &&
-            ptx::mbar_test_wait(&M.full_v[pv % kStages], (pv / kStages) & 1) &&
-            (pi > 0 || ps == 0 || ptx::mbar_test_wait(&M.o_empty, (ps - 1) & 1)))
-          go = 1;
-        else if (q_n > 0 && qk - pv < 2 &&
-                 ptx::mbar_test_wait(&M.full_k[qk % kStages], (qk / kStages) & 1) &&
-                 (qk < 2 || ptx::mbar_test_wait(&M.s_empty[qk & 1], ((qk >> 1) & 1) ^ 1)) &&
-                 (qi > 0 || ptx::mbar_test_wait(&M.q_full, qs & 1)))
-          go = 2;
-      }
-      go = __shfl_sync(0xffffffffu, go, 0);
-      if (go == 1) {
-        const Segment& g = M.ring[ps % kRing];
-        const int st = pv % kStages;
-        uint8_t* V = smem + st * La::kStage + La::kTile;
-        zero_unseen_values<D>(g.t, key_tile(g.t, g.first + pi), V);
-        ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t va = ptx::smem_u32(V);
-          const uint32_t pa = ptx::smem_u32(smem + La::oP + (pv % PB) * La::kP);
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks) {
-            const uint64_t vd =
-                ptx::sdesc_sw128(va + ks * 2 * kGroupBytes, 1024, kGroupBytes);
-            const uint64_t pd = ptx::sdesc_sw128(
-                pa + (ks / 4) * (2 * N * 128) + (ks % 4) * 32, 16, 1024);
-            ptx::mma_bf16(tmem_o, vd, pd, kIdescPV, pi > 0 || ks > 0 ? 1u : 0u);
+    // One thread with two cursors over the same tiles: O += of tile pv as soon
+    // as its P is there, S of tile qk as soon as its K is; S runs at most two
+    // ahead.
+    if (elect_one()) {
+      const uint32_t stages = desc_lo(ptx::smem_u32(smem), 0);
+      const uint32_t qa = desc_lo(ptx::smem_u32(smem + La::oQ), 16);
+      const uint32_t pa = desc_lo(ptx::smem_u32(smem + La::oP), 16);
+      uint32_t qk = 0, pv = 0;  // tiles issued
+      uint32_t qs = 0, ps = 0;  // their segments
+      int q_left = -1, p_left = 0;  // tiles to go in them; -1: header not read
+      bool q_first = true, p_first = true;
+      Patience wait;
+      for (;;) {
+        if (q_left < 0) {
+          if (ptx::mbar_test_wait(&M.seg_full[qs % kRing], (qs / kRing) & 1)) {
+            q_left = M.ring[qs % kRing].n;
+            q_first = true;
+            wait.reset();
           }
-          ptx::mma_commit(&M.empty[st]);
-          ptx::mma_commit(&M.p_done[pv % PB]);
+        } else if (q_left == 0 && pv == qk) {
+          break;  // the end of the share
         }
-        __syncwarp();
-        ++pv;
-        if (++pi == p_n) {
-          if (lane == 0) ptx::mbar_arrive(&M.seg_empty[ps % kRing]);
-          ++ps;
-          pi = 0;
-          p_n = -1;
-        }
-        did = 1;
-      } else if (go == 2) {
-        ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t ka = ptx::smem_u32(smem + (qk % kStages) * La::kStage);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t kd =
-                ptx::sdesc_sw128(ka + (ks / 4) * 1024 + (ks % 4) * 32, 16, kGroupBytes);
-            const uint64_t qd =
-                ptx::sdesc_sw128(qa + (ks / 4) * (N * 128) + (ks % 4) * 32, 16, 1024);
-            ptx::mma_bf16(tmem + (qk & 1) * N, kd, qd, kIdescQK, ks > 0 ? 1u : 0u);
+        if (pv < qk) {
+          if (p_left == 0) {
+            p_left = M.ring[ps % kRing].n;
+            p_first = true;
           }
+          if (ptx::mbar_test_wait(&M.p_full[pv % PB], (pv / PB) & 1) &&
+              ptx::mbar_test_wait(&M.full_v[pv % kStages], (pv / kStages) & 1) &&
+              (!p_first || ps == 0 || ptx::mbar_test_wait(&M.o_empty, (ps - 1) & 1))) {
+            ptx::tc_fence_after();
+            const uint32_t st = pv % kStages;
+            const uint32_t va = stages + (st * La::kStage + La::kTile) / 16 + ((1024u / 16) << 16);
+            const uint32_t pb = pa + (pv % PB) * (La::kP / 16);
+#pragma unroll
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              mma_ss(tmem_o, va + ks * 2 * kGroupBytes / 16, desc_hi(kGroupBytes),
+                     pb + ((ks / 4) * (kPV * 128) + (ks % 4) * 32) / 16, desc_hi(1024), kIdescPV,
+                     ks > 0 || !p_first ? 1u : 0u);
+            ptx::mma_commit(&M.empty[st]);
+            ptx::mma_commit(&M.p_done[pv % PB]);
+            ++pv;
+            p_first = false;
+            if (--p_left == 0) {
+              ptx::mbar_arrive(&M.seg_empty[ps % kRing]);
+              ++ps;
+            }
+            wait.reset();
+            continue;
+          }
+        }
+        if (q_left > 0 && qk - pv < 2 &&
+            ptx::mbar_test_wait(&M.full_k[qk % kStages], (qk / kStages) & 1) &&
+            (qk < 2 || ptx::mbar_test_wait(&M.s_empty[qk & 1], ((qk >> 1) & 1) ^ 1)) &&
+            (!q_first || ptx::mbar_test_wait(&M.q_full, qs & 1))) {
+          ptx::tc_fence_after();
+          const uint32_t ka = stages + (qk % kStages) * (La::kStage / 16) + (1u << 16);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + (qk & 1) * N, ka + ((ks / 4) * 1024 + (ks % 4) * 32) / 16,
+                   desc_hi(kGroupBytes), qa + ((ks / 4) * (N * 128) + (ks % 4) * 32) / 16,
+                   desc_hi(1024), kIdescQK, ks > 0 ? 1u : 0u);
           ptx::mma_commit(&M.s_full[qk & 1]);
+          ++qk;
+          q_first = false;
+          if (--q_left == 0) {
+            ++qs;
+            q_left = -1;
+          }
+          wait.reset();
+          continue;
         }
-        __syncwarp();
-        ++qk;
-        if (++qi == q_n) {
-          ++qs;
-          qi = 0;
-          q_n = -1;
-        }
-        did = 1;
+        if (wait.out(abort_f)) break;
       }
-      if (!__any_sync(0xffffffffu, did) && wait.out(abort_f)) break;
-      if (did) wait.reset();
     }
+    __syncwarp();
   } else {
     // ---------------- softmax and epilogue --------------------------------
     const int w = warp & 3;                 // TMEM lanes 32w .. 32w + 31
@@ -256,19 +249,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int d = D == 128 ? j : w * 16 + lane;  // this thread's column of O
     const float c = P.scale_log2;
     constexpr int kBar = 1;
-    float l[N];
 
     // Q of a segment into shared memory, rows past the last as zeros
     auto load_q = [&](const Segment& g) {
       uint8_t* Q = smem + La::oQ;
+#pragma unroll
       for (int i = st_tid; i < N * (D / 8); i += 128) {
         const int n = i / (D / 8), ch = i % (D / 8);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (n < g.t.n_rows) {
-          const int r = g.t.row0 + n;
+          const int r = g.t.row0 + n, tok = r / P.group;
           v = *reinterpret_cast<const uint4*>(
-              P.q + (g.tok0 + r / P.group) * P.q_stride +
-              (g.head * P.group + r % P.group) * D + ch * 8);
+              P.q + (g.tok0 + tok) * P.q_stride +
+              (g.head * P.group + r - tok * P.group) * D + ch * 8);
         }
         *reinterpret_cast<uint4*>(Q + (ch / 8) * (N * 128) + n * 128 +
                                   (((ch % 8) ^ (n & 7)) << 4)) = v;
@@ -277,42 +270,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&M.q_full);
     };
-    auto seg_wait = [&](int s) {
-      return wait_all(&M.seg_full[s % kRing], (s / kRing) & 1, abort_f);
-    };
 
     // The four warps meet at barriers, so none leaves on its own: after a
     // wait that gave up they run on (every later wait returns at once) to
-    // the vote at the segment's end.
-    int tile = 0;  // tiles of this CTA so far
-    bool ok = seg_wait(0);
+    // the vote at the next segment.
+    uint32_t tile = 0;  // tiles of this CTA so far
+    bool ok = wait_all(&M.seg_full[0], 0, abort_f);
     if (ok && M.ring[0].n > 0) load_q(M.ring[0]);
-    for (int sg = 0; !named_any(kBar, 128, !ok); ++sg) {
+    for (int sg = 0; !named_any(kBar, 128, !ok || *abort_f); ++sg) {
       const Segment g = M.ring[sg % kRing];
       if (g.n == 0) break;
-      // limits of the rows (rows past the last copy row 0's) and a first m
-      for (int n = st_tid; n < N; n += 128) {
+      // limits of the rows (rows past the last copy row 0's)
+      for (int n = st_tid; n < A; n += 128) {
         const int pos = g.base + (g.t.row0 + (n < g.t.n_rows ? n : 0)) / P.group;
         M.row_hi[n] = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
         M.row_lo[n] =
             P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
-        M.m[n] = -INFINITY;
-        M.fac[n] = 0.f;
       }
       named_bar(kBar, 128);
-      int min_hi = M.row_hi[lane % N], max_lo = M.row_lo[lane % N];
-      if (N > 32) {
-        min_hi = min(min_hi, M.row_hi[(lane + 32) % N]);
-        max_lo = max(max_lo, M.row_lo[(lane + 32) % N]);
-      }
+      int min_hi = M.row_hi[lane % A], max_lo = M.row_lo[lane % A];
       min_hi = __reduce_min_sync(0xffffffffu, min_hi);
       max_lo = __reduce_max_sync(0xffffffffu, max_lo);
+      // of each row: minus the reference maximum (log2 units; +inf: none yet)
+      // and the sum over this thread's keys
+      float neg[A], l[A];
 #pragma unroll
-      for (int n = 0; n < N; ++n) l[n] = 0.f;
+      for (int n = 0; n < A; ++n) {
+        neg[n] = INFINITY;
+        l[n] = 0.f;
+      }
 
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys, key = key0 + j;
-        ok &= wait_all(&M.s_full[tile & 1], (tile >> 1) & 1, abort_f);
+        wait_quiet(&M.s_full[tile & 1], (tile >> 1) & 1, abort_f);
+        __syncwarp();
         ptx::tc_fence_after();
         float s[N];
 #pragma unroll
@@ -325,70 +316,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&M.s_empty[tile & 1]);
         if (i == g.n - 1) {
           // the last S is here, so Q's buffer is free: fetch the next one's
-          ok &= seg_wait(sg + 1);
+          ok = wait_all(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
           if (ok && M.ring[(sg + 1) % kRing].n > 0) load_q(M.ring[(sg + 1) % kRing]);
         }
         if (key0 < max_lo || key0 + kKeys - 1 > min_hi) {
 #pragma unroll
-          for (int n = 0; n < N; ++n)
+          for (int n = 0; n < A; ++n)
             if (key > M.row_hi[n] || (key < M.row_lo[n] && key >= g.t.n_sink)) s[n] = -INFINITY;
         }
         // does a score exceed its reference maximum by more than 8?
         bool up = false;
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (n < g.t.n_rows) up |= fmaf(s[n], c, -M.m[n]) > 8.f;
+        for (int n = 0; n < A; ++n) up |= fmaf(s[n], c, neg[n]) > 8.f;
         if (named_any(kBar, 128, up)) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            if (n < g.t.n_rows) {
-              const float mx = warp_max(s[n]);
-              if (lane == 0) M.red[w][n] = mx;
-            }
+          for (int n = 0; n < A; ++n) {
+            const float mx = warp_max(s[n]);
+            if (lane == 0) reinterpret_cast<float*>(&M.red[n])[w] = mx;
           }
           named_bar(kBar, 128);
-          for (int n = st_tid; n < g.t.n_rows; n += 128) {
-            const float mx =
-                fmaxf(fmaxf(M.red[0][n], M.red[1][n]), fmaxf(M.red[2][n], M.red[3][n])) * c;
-            const float old = M.m[n], now = fmaxf(old, mx);
-            M.fac[n] = old == -INFINITY ? 0.f : exp2_fast(old - now);
-            M.m[n] = now;
-          }
-          named_bar(kBar, 128);
+          float fac[A];
 #pragma unroll
-          for (int n = 0; n < N; ++n) l[n] *= M.fac[n];
+          for (int n = 0; n < A; ++n) {
+            const float4 r = M.red[n];
+            const float mx = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)) * c;
+            const float now = fminf(neg[n], -mx);
+            fac[n] = neg[n] == INFINITY ? 0.f : exp2_fast(now - neg[n]);
+            neg[n] = now;
+            l[n] *= fac[n];
+          }
           if (i > 0) {
-            ok &= wait_all(&M.p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
+            wait_quiet(&M.p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
+            __syncwarp();
             ptx::tc_fence_after();
 #pragma unroll
-            for (int n = 0; n < 2 * N; n += 16) {
+            for (int n = 0; n < kPV; n += 16) {
               uint32_t o[16];
               ptx::tmem_ld16(tmem_o + lanes + n, o);
               ptx::tmem_ld_wait();
 #pragma unroll
               for (int x = 0; x < 16; ++x)
-                o[x] = __float_as_uint(__uint_as_float(o[x]) * M.fac[(n + x) % N]);
+                o[x] = __float_as_uint(__uint_as_float(o[x]) * fac[(n + x) % (kPV / 2) % A]);
               ptx::tmem_st16(tmem_o + lanes + n, o);
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
           }
         }
+        if (tile_has_unseen(g.t, key0)) {
+          wait_quiet(&M.full_v[tile % kStages], (tile / kStages) & 1, abort_f);
+          zero_unseen_value<D>(g.t, key0, j, smem + (tile % kStages) * La::kStage + La::kTile);
+        }
         // P's buffer is free once the product that read it is done
-        if (tile >= PB) ok &= wait_all(&M.p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
-        uint8_t* Pb = smem + La::oP + (tile % PB) * La::kP + (j / 64) * (2 * N * 128) + (j % 8) * 2;
+        if (tile >= PB) wait_quiet(&M.p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
+        uint8_t* Pb = smem + La::oP + (tile % PB) * La::kP + (j / 64) * (kPV * 128) + (j % 8) * 2;
         const int ch = (j % 64) / 8;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (n < g.t.n_rows) {  // the columns of the other rows are never read
-            const float m = M.m[n];
-            const float p = exp2_fast(fmaf(s[n], c, m == -INFINITY ? 0.f : -m));
-            l[n] += p;
-            const bf16 hi = __float2bfloat16_rn(p);
-            const bf16 lo = __float2bfloat16_rn(p - __bfloat162float(hi));
-            *reinterpret_cast<bf16*>(Pb + n * 128 + ((ch ^ (n & 7)) << 4)) = hi;
-            *reinterpret_cast<bf16*>(Pb + (N + n) * 128 + ((ch ^ (n & 7)) << 4)) = lo;
-          }
+        for (int n = 0; n < A; ++n) {
+          const float p = exp2_fast(fmaf(s[n], c, neg[n] == INFINITY ? 0.f : neg[n]));
+          l[n] += p;
+          const bf16 hi = __float2bfloat16_rn(p);
+          const bf16 lo = __float2bfloat16_rn(p - __bfloat162float(hi));
+          *reinterpret_cast<bf16*>(Pb + n * 128 + ((ch ^ (n & 7)) << 4)) = hi;
+          *reinterpret_cast<bf16*>(Pb + (kPV / 2 + n) * 128 + ((ch ^ (n & 7)) << 4)) = lo;
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -397,35 +387,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the item, or this CTA's part of it, is done
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (n < g.t.n_rows) {
-          const float x = warp_sum(l[n]);
-          if (lane == 0) M.red[w][n] = x;
-        }
+      for (int n = 0; n < A; ++n) {
+        const float x = warp_sum(l[n]);
+        if (lane == 0) reinterpret_cast<float*>(&M.red[n])[w] = x;
       }
-      ok &= wait_all(&M.p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
+      wait_quiet(&M.p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
+      __syncwarp();
       ptx::tc_fence_after();
       named_bar(kBar, 128);
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
-      float* part = P.part + slot * N * D;
+      float* part = P.part + slot * A * D + d;
+      int tok = g.t.row0 / P.group, hd = g.t.row0 - tok * P.group;  // of row n
 #pragma unroll
-      for (int n0 = 0; n0 < N; n0 += 16) {
-        if (n0 >= g.t.n_rows) break;
+      for (int n0 = 0; n0 < A; n0 += 16) {
         uint32_t oh[16], ol[16];
         ptx::tmem_ld16(tmem_o + lanes + n0, oh);
-        ptx::tmem_ld16(tmem_o + lanes + N + n0, ol);
+        if (A >= 16) ptx::tmem_ld16(tmem_o + lanes + kPV / 2 + n0, ol);
         ptx::tmem_ld_wait();
-        if (!has_d) continue;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
+        for (int x = 0; x < (A < 16 ? A : 16); ++x) {
           const int n = n0 + x;
-          if (n >= g.t.n_rows) break;
-          const float o = __uint_as_float(oh[x]) + __uint_as_float(ol[x]);
-          const float sum = M.red[0][n] + M.red[1][n] + M.red[2][n] + M.red[3][n];
-          if (g.parts > 1)
-            part[n * D + d] = o;
-          else
-            write_row<D>(P, g, n, d, o, sum, M.m[n]);
+          const float o = __uint_as_float(oh[x]) + __uint_as_float(A >= 16 ? ol[x] : oh[x + 8]);
+          if (n < g.t.n_rows) {
+            const float4 r = M.red[n];
+            if (!has_d)
+              ;
+            else if (g.parts > 1)
+              part[n * D] = o;
+            else
+              write_row<D>(P, g, g.tok0 + tok, g.head * P.group + hd, d, o,
+                           r.x + r.y + r.z + r.w, -neg[n]);
+            if (++hd == P.group) hd = 0, ++tok;
+          }
         }
       }
       ptx::tc_fence_before();
@@ -435,22 +428,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
       }
       if (g.parts > 1) {
-        for (int n = st_tid; n < g.t.n_rows; n += 128) {
-          float* ml = P.part_ml + (slot * N + n) * 2;
-          ml[0] = M.m[n];
-          ml[1] = M.red[0][n] + M.red[1][n] + M.red[2][n] + M.red[3][n];
+        float2* ml = reinterpret_cast<float2*>(P.part_ml);
+#pragma unroll
+        for (int n = 0; n < A; ++n) {
+          if (st_tid == n) {
+            const float4 r = M.red[n];
+            ml[slot * A + n] = make_float2(-neg[n], r.x + r.y + r.z + r.w);
+          }
         }
         if (last_to_arrive(P, g, g.item, st_tid == 0, &M.last, kBar, 128)) {
-          for (int n = st_tid; n < g.t.n_rows; n += 128)
-            merged_max<N>(P, g, n, &M.m[n], &M.red[0][n]);
-          named_bar(kBar, 128);
-          if (has_d) {
-            for (int n = 0; n < g.t.n_rows; ++n)
-              write_row<D>(P, g, n, d, merged_value<N, D>(P, g, n, d, M.m[n]), M.red[0][n], M.m[n]);
+          // all parts' maxima and sums by way of P's buffer, which is free
+          constexpr int kChunk = La::kP / (A * 8);
+          float2* all = reinterpret_cast<float2*>(smem + La::oP);
+          float o[A], top[A], sum[A];
+#pragma unroll
+          for (int n = 0; n < A; ++n) o[n] = sum[n] = 0.f, top[n] = -INFINITY;
+          for (int c0 = 0; c0 < g.parts; c0 += kChunk) {
+            const int cnt = min(kChunk, g.parts - c0);
+            for (int x = st_tid; x < cnt * A; x += 128)
+              all[x] = __ldcg(&ml[part_slot(g, c0 + x / A) * A + x % A]);
+            named_bar(kBar, 128);
+#pragma unroll
+            for (int n = 0; n < A; ++n) {
+              float now = top[n];
+              for (int q = 0; q < cnt; ++q) now = fmaxf(now, all[q * A + n].x);
+              const float f = top[n] == -INFINITY ? 0.f : exp2_fast(top[n] - now);
+              o[n] *= f;
+              sum[n] *= f;
+              top[n] = now;
+            }
+            for (int q = 0; q < cnt; ++q) {
+              const float* from = P.part + part_slot(g, c0 + q) * A * D + (has_d ? d : 0);
+              float v[A];
+#pragma unroll
+              for (int n = 0; n < A; ++n) v[n] = n < g.t.n_rows ? __ldcg(from + n * D) : 0.f;
+#pragma unroll
+              for (int n = 0; n < A; ++n) {
+                const float2 x = all[q * A + n];
+                const float f = top[n] == -INFINITY ? 0.f : exp2_fast(x.x - top[n]);
+                sum[n] += f * x.y;
+                o[n] += f * v[n];
+              }
+            }
+            named_bar(kBar, 128);
+          }
+          tok = g.t.row0 / P.group, hd = g.t.row0 - tok * P.group;
+#pragma unroll
+          for (int n = 0; n < A; ++n) {
+            if (n < g.t.n_rows) {
+              if (has_d)
+                write_row<D>(P, g, g.tok0 + tok, g.head * P.group + hd, d, o[n], sum[n], top[n]);
+              if (++hd == P.group) hd = 0, ++tok;
+            }
           }
         }
       }
-      named_bar(kBar, 128);  // m and red are free
+      named_bar(kBar, 128);  // red and the limits are free
     }
   }
 
@@ -463,14 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_f) flag_error(P.err, LORA_DEVERR_TIMEOUT);
 }
 
-template <int D, int N>
-cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, AttnParams P, cudaStream_t st,
-                   const DeviceInfo& dev) {
-  using La = Lay<D, N>;
-  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<N, La::kStages>);
+template <int D, int A>
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& P,
+                   cudaStream_t st, const DeviceInfo& dev) {
+  using La = Lay<D, A>;
+  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<A, La::kStages>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
-  auto kern = attn_decode_kernel<D, N>;
+  auto kern = attn_decode_kernel<D, A>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -492,13 +525,19 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, AttnParams 
 cudaError_t launch_attn_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                const AttnParams& P, cudaStream_t st, const DeviceInfo& dev) {
   if (P.kv.head_dim == 64) {
-    if (P.rows == 16) return launch<64, 16>(tm_k, tm_v, P, st, dev);
-    if (P.rows == 32) return launch<64, 32>(tm_k, tm_v, P, st, dev);
-    return launch<64, 64>(tm_k, tm_v, P, st, dev);
+    switch (P.rows) {
+      case 4: return launch<64, 4>(tm_k, tm_v, P, st, dev);
+      case 8: return launch<64, 8>(tm_k, tm_v, P, st, dev);
+      case 16: return launch<64, 16>(tm_k, tm_v, P, st, dev);
+      default: return launch<64, 32>(tm_k, tm_v, P, st, dev);
+    }
   }
-  if (P.rows == 16) return launch<128, 16>(tm_k, tm_v, P, st, dev);
-  if (P.rows == 32) return launch<128, 32>(tm_k, tm_v, P, st, dev);
-  return launch<128, 64>(tm_k, tm_v, P, st, dev);
+  switch (P.rows) {
+    case 4: return launch<128, 4>(tm_k, tm_v, P, st, dev);
+    case 8: return launch<128, 8>(tm_k, tm_v, P, st, dev);
+    case 16: return launch<128, 16>(tm_k, tm_v, P, st, dev);
+    default: return launch<128, 32>(tm_k, tm_v, P, st, dev);
+  }
 }
 
 }  // namespace lora

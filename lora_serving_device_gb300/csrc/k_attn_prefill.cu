@@ -55,7 +55,7 @@ struct Misc {
   Segment ring[kRing];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
   uint64_t seg_full[kRing], seg_empty[kRing];
   uint32_t tmem;
   int abort;
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&M.q_full[h], 1);
       ptx::mbar_init(&M.q_empty[h], 1);
       ptx::mbar_init(&M.s_full[h], 1);
+      ptx::mbar_init(&M.p_half[h], 4);
       ptx::mbar_init(&M.p_full[h], 4);
       ptx::mbar_init(&M.o_done[h], 1);
       ptx::mbar_init(&M.o_empty[h], 4);
@@ -206,86 +207,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ---------------- MMA issue ------------------------------------------
-    // P V of tile n and Q K^T of tile n + 1, half by half
-    int segs[2] = {0, 0};   // segments of each half so far
-    int tiles[2] = {0, 0};  // tiles of each half whose P V was issued
-    bool ok = true;
-    auto issue_qk = [&](const Segment& g, int i, int n, int h) {
-      if (i == 0) {
-        ok &= wait_all(&M.q_full[h], segs[h] & 1, abort_f);
-        ++segs[h];
-      }
-      const int k = 2 * n, st = k % kSlots;
-      ok &= wait_all(&M.full[st], (k / kSlots) & 1, abort_f);
-      ptx::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t qa = ptx::smem_u32(smem + La::oQ + h * La::kTile);
-        const uint32_t ka = ptx::smem_u32(smem + st * La::kTile);
+    // One thread: P V of tile n and Q K^T of tile n + 1, half by half, so that
+    // the tensor cores have the other half's work while a softmax runs.
+    if (elect_one()) {
+      const uint32_t slots = desc_lo(ptx::smem_u32(smem), 0);
+      uint32_t segs[2] = {0, 0};   // segments of each half so far
+      uint32_t tiles[2] = {0, 0};  // tiles of each half whose P V was issued
+      auto issue_qk = [&](bool first, bool last, int n, int h, bool frees) {
+        if (first) wait_quiet(&M.q_full[h], segs[h]++ & 1, abort_f);
+        const int k = 2 * n, st = k % kSlots;
+        wait_quiet(&M.full[st], (k / kSlots) & 1, abort_f);
+        ptx::tc_fence_after();
+        const uint32_t qa = desc_lo(ptx::smem_u32(smem + La::oQ + h * La::kTile), 16);
+        const uint32_t ka = slots + st * (La::kTile / 16) + (1u << 16);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          // Q: [64-value half of a head][128 rows][64]
-          const uint64_t qd = ptx::sdesc_sw128(
-              qa + (ks / 4) * (kHalf * 128) + (ks % 4) * 32, 16, 1024);
-          const uint64_t kd =
-              ptx::sdesc_sw128(ka + (ks / 4) * 1024 + (ks % 4) * 32, 16, kGroupBytes);
-          ptx::mma_bf16(tmem + h * 128, qd, kd, kIdescQK, ks > 0 ? 1u : 0u);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)  // Q: [64-value half of a head][128 rows][64]
+          mma_ss(tmem + h * 128, qa + ((ks / 4) * (kHalf * 128) + (ks % 4) * 32) / 16,
+                 desc_hi(1024), ka + ((ks / 4) * 1024 + (ks % 4) * 32) / 16, desc_hi(kGroupBytes),
+                 kIdescQK, ks > 0 ? 1u : 0u);
         ptx::mma_commit(&M.s_full[h]);
-        if (i == g.n - 1) ptx::mma_commit(&M.q_empty[h]);
-        if (h == 1 || g.t.n_rows <= half_rows) ptx::mma_commit(&M.empty[st]);
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](const Segment& g, int i, int n, int h) {
-      const int k = 2 * n + 1, st = k % kSlots;
-      uint8_t* V = smem + st * La::kTile;
-      if (h == 0) {
-        ok &= wait_all(&M.full[st], (k / kSlots) & 1, abort_f);
-        if (ok) zero_unseen_values<D>(g.t, key_tile(g.t, g.first + i), V);
-      }
-      ok &= wait_all(&M.p_full[h], tiles[h] & 1, abort_f);
-      // the half's previous segment has been read out of O
-      if (i == 0 && segs[h] > 1) ok &= wait_all(&M.o_empty[h], segs[h] & 1, abort_f);
-      ptx::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t va = ptx::smem_u32(V);
+        if (frees) ptx::mma_commit(&M.empty[st]);
+        if (last) ptx::mma_commit(&M.q_empty[h]);
+      };
+      auto issue_pv = [&](bool first, int n, int h, bool frees) {
+        const int k = 2 * n + 1, st = k % kSlots;
+        const uint32_t va = slots + st * (La::kTile / 16) + ((1024u / 16) << 16);
+        if (h == 0) wait_quiet(&M.full[st], (k / kSlots) & 1, abort_f);
+        // the half's previous segment has been read out of O
+        if (first && segs[h] > 1) wait_quiet(&M.o_empty[h], segs[h] & 1, abort_f);
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks) {
-          const uint64_t vd = ptx::sdesc_sw128(va + ks * 2 * kGroupBytes, 1024, kGroupBytes);
-          ptx::mma_bf16_ta(tmem + 256 + h * 128, tmem + h * 128 + ks * 8, vd, kIdescPV,
-                           i > 0 || ks > 0 ? 1u : 0u);
+        for (int x = 0; x < 2; ++x) {
+          wait_quiet(x ? &M.p_full[h] : &M.p_half[h], tiles[h] & 1, abort_f);
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int ks = 4 * x; ks < 4 * x + 4; ++ks)
+            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
+                   va + ks * 2 * kGroupBytes / 16, desc_hi(kGroupBytes), kIdescPV,
+                   ks > 0 || !first ? 1u : 0u);
         }
         ptx::mma_commit(&M.o_done[h]);
-        if (h == 1 || g.t.n_rows <= half_rows) ptx::mma_commit(&M.empty[st]);
+        if (frees) ptx::mma_commit(&M.empty[st]);
+        ++tiles[h];
+      };
+      wait_quiet(&M.seg_full[0], 0, abort_f);
+      int sg = 0, left = M.ring[0].n;  // this segment's key tiles to go
+      bool two = M.ring[0].t.n_rows > half_rows, first = true;
+      if (left > 0) {
+        issue_qk(true, left == 1, 0, 0, !two);
+        if (two) issue_qk(true, left == 1, 0, 1, true);
       }
-      __syncwarp();
-      ++tiles[h];
-    };
-    ok = wait_all(&M.seg_full[0], 0, abort_f);
-    int sg = 0, n = 0;
-    if (ok && M.ring[0].n > 0) {
-      for (int h = 0; h < 2; ++h)
-        if (M.ring[0].t.n_rows > h * half_rows) issue_qk(M.ring[0], 0, 0, h);
+      for (int n = 0; left > 0 && !*abort_f; ++n) {
+        int next = left - 1;
+        bool next_two = two, next_first = false;
+        if (next == 0) {  // the next tile is of the next segment
+          wait_quiet(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
+          next = M.ring[(sg + 1) % kRing].n;
+          next_two = M.ring[(sg + 1) % kRing].t.n_rows > half_rows;
+          next_first = true;
+        }
+        issue_pv(first, n, 0, !two);
+        if (next > 0) issue_qk(next_first, next == 1, n + 1, 0, !next_two);
+        if (two) issue_pv(first, n, 1, true);
+        if (next > 0 && next_two) issue_qk(next_first, next == 1, n + 1, 1, true);
+        if (next_first) {
+          ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+          ++sg;
+        }
+        left = next;
+        two = next_two;
+        first = next_first;
+      }
     }
-    for (int i = 0; ok; ++n) {
-      const Segment& g = M.ring[sg % kRing];
-      if (g.n == 0) break;
-      const bool turn = i == g.n - 1;  // the next tile is of the next segment
-      if (turn) ok = wait_all(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
-      if (!ok) break;
-      const Segment& x = M.ring[(turn ? sg + 1 : sg) % kRing];
-      const int xi = turn ? 0 : i + 1;
-      for (int h = 0; h < 2 && ok; ++h) {
-        // (the count of segments that issue_pv looks at is this segment's)
-        if (g.t.n_rows > h * half_rows) issue_pv(g, i, n, h);
-        if (ok && x.n > 0 && x.t.n_rows > h * half_rows) issue_qk(x, xi, n + 1, h);
-      }
-      if (turn) {
-        if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
-        ++sg;
-      }
-      i = xi;
-    }
+    __syncwarp();
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMost));
@@ -297,12 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = P.scale_log2;
     const int bar = 1 + h;
     int tile = 0;  // tiles of this half so far
-    bool ok = true;
-    // the warpgroup's four warps meet at barriers: after a wait that gave up
-    // they run on (every later wait returns at once) to the vote
+    // The warpgroup's four warps meet at barriers: after a wait that gave up
+    // they run on (every later wait returns at once) to the vote.
     for (int sg = 0;; ++sg) {
-      ok &= wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
-      if (named_any(bar, 128, !ok)) break;
+      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (named_any(bar, 128, *abort_f != 0)) break;
       const Segment g = M.ring[sg % kRing];
       if (g.n == 0) break;
       const int n_rows = min(g.t.n_rows - h * half_rows, half_rows);  // of this half
@@ -311,16 +303,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
         continue;
       }
-      // rows past the last copy the first one's limits
-      const int pos =
-          g.base + (g.t.row0 + h * half_rows + (row < n_rows ? row : 0)) / P.group;
+      // rows past the last copy the first one
+      const bool mine = row < n_rows;
+      const int in_prob = g.t.row0 + h * half_rows + (mine ? row : 0);
+      const int tok = in_prob / P.group, head = g.head * P.group + in_prob - tok * P.group;
+      const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo =
           P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys;
-        ok &= wait_all(&M.s_full[h], tile & 1, abort_f);
+        wait_quiet(&M.s_full[h], tile & 1, abort_f);
+        __syncwarp();
         ptx::tc_fence_after();
         float s[kKeys];
 #pragma unroll
@@ -329,25 +324,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_ld_wait();
         if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) {
           const int top = hi - key0, bottom = lo - key0, sink = g.t.n_sink - key0;
+          if (__any_sync(0xffffffffu, key0 < lo)) {
 #pragma unroll
-          for (int k = 0; k < kKeys; ++k)
-            if (k > top || (k < bottom && k >= sink)) s[k] = -INFINITY;
+            for (int k = 0; k < kKeys; ++k)
+              if (k > top || (k < bottom && k >= sink)) s[k] = -INFINITY;
+          } else {
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k)
+              if (k > top) s[k] = -INFINITY;
+          }
         }
         float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
+        float mz = max3(s[6], s[7], s[8]), mw = max3(s[9], s[10], s[11]);
 #pragma unroll
-        for (int k = 6; k + 3 < kKeys; k += 4) {
+        for (int k = 12; k + 7 < kKeys; k += 8) {
           mx = max3(mx, s[k], s[k + 1]);
           my = max3(my, s[k + 2], s[k + 3]);
+          mz = max3(mz, s[k + 4], s[k + 5]);
+          mw = max3(mw, s[k + 6], s[k + 7]);
         }
-        mx = max3(mx, s[kKeys - 2], s[kKeys - 1]);
-        mx = fmaxf(mx, my) * c;
+        mx = max3(mx, s[kKeys - 4], s[kKeys - 3]);
+        my = max3(my, s[kKeys - 2], s[kKeys - 1]);
+        mx = max3(mx, my, fmaxf(mz, mw)) * c;
         if (__any_sync(0xffffffffu, mx > m + 8.f)) {
           const float now = fmaxf(m, mx);
           const float f = m == -INFINITY ? 0.f : exp2_fast(m - now);
           m = now;
           l *= f;
           if (i > 0) {
-            ok &= wait_all(&M.o_done[h], (tile - 1) & 1, abort_f);
+            wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
+            __syncwarp();
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int k = 0; k < D; k += 32) {
@@ -359,6 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tmem_st32(tm_o + k, o);
             }
           }
+        }
+        if (h == 0 && tile_has_unseen(g.t, key0)) {
+          // (half 0 takes part in every tile, and its P V is issued first)
+          const int k = 2 * tile + 1;
+          wait_quiet(&M.full[k % kSlots], (k / kSlots) & 1, abort_f);
+          zero_unseen_value<D>(g.t, key0, row, smem + (k % kSlots) * La::kTile);
+          ptx::fence_proxy_async_smem();
         }
         const float neg = m == -INFINITY ? 0.f : -m;
         const uint64_t c2 = pack2(c, c), neg2 = pack2(neg, neg);
@@ -379,80 +392,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[x] = pack_bf16x2(a, b);
           }
           ptx::tmem_st16(tm_s + k / 2, p);
+          if (k == 32 || k == 96) {
+            // each half of the keys goes to the MMA as soon as it is there
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(k == 32 ? &M.p_half[h] : &M.p_full[h]);
+          }
         }
         float a, b;
         unpack2(add2(sum0, sum1), &a, &b);
         l += a + b;
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.p_full[h]);
       }
 
       // ---- the item, or this CTA's part of it, is done
-      ok &= wait_all(&M.o_done[h], (tile - 1) & 1, abort_f);
-      ptx::tc_fence_after();
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
-      const bool mine = row < n_rows;
-      RowWriter<D> out(P, g, h * half_rows + row, m, l);
-      float4* part = part_row<D>(P, slot, h, row);
-#pragma unroll 1
-      for (int k = 0; k < D; k += 32) {
-        uint32_t o[32];
-        ptx::tmem_ld32(tm_o + k, o);
-        ptx::tmem_ld_wait();
-        if (!mine) continue;
-        const float* x = reinterpret_cast<const float*>(o);
-        if (g.parts > 1) {
+      const RowWriter<D> out(P, g, g.tok0 + tok, head, mine && g.parts == 1, m, l);
+      wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
+      __syncwarp();
+      ptx::tc_fence_after();
+      float o[D];
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            part[(k / 4 + q) * kHalf] =
-                make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) out.write8(k + 8 * q, x + 8 * q);
-        }
-      }
+      for (int k = 0; k < D; k += 32)
+        ptx::tmem_ld32(tm_o + k, *reinterpret_cast<uint32_t(*)[32]>(o + k));
+      ptx::tmem_ld_wait();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         ptx::mbar_arrive(&M.o_empty[h]);
         ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
       }
-      if (g.parts > 1) {
-        float2* ml = reinterpret_cast<float2*>(P.part_ml);
-        if (mine) ml[slot * 2 * kHalf + h * kHalf + row] = make_float2(m, l);
-        if (last_to_arrive(P, g, g.item * 2 + h, row == 0, &M.last[h], bar, 128) && mine) {
-          float top = -INFINITY, sum = 0.f;
-          for (int q = 0; q < g.parts; ++q)
-            top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf + h * kHalf + row].x));
-          for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
-            const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf + h * kHalf + row]);
-            sum += exp2f(v.x - top) * v.y;
-          }
-          RowWriter<D> joined(P, g, h * half_rows + row, top, sum);
-#pragma unroll 1
-          for (int k = 0; k < D; k += 32) {
-            float o[32];
+      if (g.parts == 1) {
+        if (mine) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0.f;
-            for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
-              const float f =
-                  exp2f(__ldcg(&ml[part_slot(g, q) * 2 * kHalf + h * kHalf + row].x) - top);
-              const float4* from = part_row<D>(P, part_slot(g, q), h, row);
+          for (int k = 0; k < D; k += 8) out.write8(k, o + k);
+        }
+        continue;
+      }
+      float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
+      if (mine) {
+        float4* part = part_row<D>(P, slot, h, row);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const float4 v = __ldcg(from + (k / 4 + x) * kHalf);
-                o[4 * x] += f * v.x;
-                o[4 * x + 1] += f * v.y;
-                o[4 * x + 2] += f * v.z;
-                o[4 * x + 3] += f * v.w;
-              }
-            }
+        for (int k = 0; k < D; k += 4)
+          part[(k / 4) * kHalf] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        ml[slot * 2 * kHalf] = make_float2(m, l);
+      }
+      if (last_to_arrive(P, g, g.item * 2 + h, row == 0, &M.last[h], bar, 128) && mine) {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (int q = 0; q < g.parts; ++q)
+          top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) joined.write8(k + 8 * q, o + 8 * q);
+        for (int k = 0; k < D; ++k) o[k] = 0.f;
+        for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
+          const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
+          const float f = exp2f(v.x - top);
+          sum += f * v.y;
+          const float4* from = part_row<D>(P, part_slot(g, q), h, row);
+#pragma unroll
+          for (int k = 0; k < D; k += 4) {
+            const float4 v4 = __ldcg(from + (k / 4) * kHalf);
+            o[k] += f * v4.x;
+            o[k + 1] += f * v4.y;
+            o[k + 2] += f * v4.z;
+            o[k + 3] += f * v4.w;
           }
         }
+        const RowWriter<D> joined(P, g, g.tok0 + tok, head, true, top, sum);
+#pragma unroll
+        for (int k = 0; k < D; k += 8) joined.write8(k, o + k);
       }
     }
   }
