@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (key0 < max_lo || key0 + kKeys - 1 > min_hi) {
 #pragma unroll
           for (int n = 0; n < A; ++n)
-            if (key > M.row_hi[n] || (key < M.row_lo[n] && key >= g.t.n_sink)) s[n] = -INFINITY;
+            s[n] = (key > M.row_hi[n]) | ((key < M.row_lo[n]) & (key >= g.t.n_sink)) ? -INFINITY
+                                                                                 : s[n];
         }
         // does a score exceed its reference maximum by more than 8?
         bool up = false;

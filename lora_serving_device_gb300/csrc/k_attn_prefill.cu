@@ -86,6 +86,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// The lowest n bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // Part of a row tile, [slot][half][D / 4][128 rows][4]: neighbouring threads
 // (rows) write neighbouring vectors.
 template <int D>
@@ -323,15 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
         ptx::tmem_ld_wait();
         if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) {
-          const int top = hi - key0, bottom = lo - key0, sink = g.t.n_sink - key0;
-          if (__any_sync(0xffffffffu, key0 < lo)) {
+          // a bit per key: up to hi, and from lo or below the first tokens' end
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
-              if (k > top || (k < bottom && k >= sink)) s[k] = -INFINITY;
-          } else {
+          for (int k = 0; k < kKeys; k += 32) {
+            const uint32_t seen = low_bits(hi + 1 - key0 - k) &
+                                  (~low_bits(lo - key0 - k) | low_bits(g.t.n_sink - key0 - k));
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
-              if (k > top) s[k] = -INFINITY;
+            for (int x = 0; x < 32; ++x)
+              if (!(seen & (1u << x))) s[k + x] = -INFINITY;
           }
         }
         float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
