@@ -43,6 +43,14 @@ __device__ __forceinline__ int seq_of_row(const int32_t* q_off, int n_seqs, int 
 
 constexpr int kKeys = 128;     // keys of a tile
 
+// An item that several CTAs share, from the one it begins in.
+struct SplitItem {
+  int parts;          // 0: there is none
+  int tok0, row0, n_rows;
+  int head, shared;
+  int pad[2];
+};
+
 struct AttnParams {
   lora_paged_kv_t kv;
   const bf16* q;
@@ -59,11 +67,11 @@ struct AttnParams {
   float scale_log2;    // scale * log2(e)
   int window, n_sink;
   int max_row_tiles;   // row tiles that the counters are laid out for
-  int min_share;       // units a CTA takes at least
   uint32_t* err;
-  uint32_t* count;     // arrivals per item (per half of one: prefill), zero between calls
+  uint32_t* count;     // arrivals per item, zero between calls
   float* part;         // [CTA][2][row tile] partial sums
   float* part_ml;      // [CTA][2][rows][2] their maxima (log2 units) and sums
+  SplitItem* split;    // [CTA] the item that begins there and ends in another (prefill)
   float* prior;        // [T][n_q_heads][D] the prefix phase's result, fp32
   float* prior_lse;    // [T][n_q_heads] its log2-sum-exp
 };
@@ -130,12 +138,6 @@ __device__ __forceinline__ void problem_tokens(const AttnParams& P, int p, int* 
   *t1 = b;
 }
 
-__device__ __forceinline__ int problem_row_tiles(const AttnParams& P, int p) {
-  int a, b;
-  problem_tokens(P, p, &a, &b);
-  return ((b - a) * P.group + P.rows - 1) / P.rows;
-}
-
 __device__ __forceinline__ Problem load_problem(const AttnParams& P, int p) {
   Problem r;
   int b;
@@ -194,22 +196,30 @@ __device__ __forceinline__ int key_tile(const RowTile& t, int i) {
   return i < t.sink_tiles ? i : t.tile_lo + i - t.sink_tiles;
 }
 
-// The prefix sums in shared memory.
+// Units of one key head over all row tiles of a problem: a warp's lanes take a
+// row tile each.
+__device__ __forceinline__ int64_t problem_units(const AttnParams& P, const Problem& pr) {
+  const int n = (pr.n_rows + P.rows - 1) / P.rows;
+  int64_t sum = 0;
+  for (int rt = threadIdx.x & 31; rt < n; rt += 32) sum += row_tile(P, pr, rt).n_tiles + P.over;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// The prefix sums in shared memory.  C is a multiple of 32.
 template <int C>
 struct Schedule {
-  static constexpr int kCoarse = C;  // a multiple of 32
-  int64_t units[kCoarse + 1];  // key tiles before coarse entry e of row tiles
-  int tiles[kCoarse + 1];      // row tiles before coarse entry e of problems
-  int n_prob, per_prob;        // problems, problems of a coarse entry
-  int n_tiles, per_tile;       // row tiles, row tiles of a coarse entry
-  int64_t total, share;        // units of the call, units of a CTA
+  int64_t units[C + 1];   // units of a key head before coarse entry e of problems
+  int tiles[C + 1];       // row tiles before it
+  int n_prob, per_prob;   // problems, problems of a coarse entry
+  int total, share;       // units of the call, units of a CTA
 };
 
-// Exclusive prefix sums of v[0 .. kCoarse) in place by one warp, the sum in
-// v[kCoarse].
-template <int kCoarse, typename T>
+// Exclusive prefix sums of v[0 .. C) in place by one warp, the sum in v[C].
+template <int C, typename T>
 __device__ __forceinline__ void warp_scan_coarse(T* v) {
-  constexpr int kPer = kCoarse / 32;
+  constexpr int kPer = C / 32;
   const int lane = threadIdx.x & 31;
   T x[kPer], sum = 0;
 #pragma unroll
@@ -229,101 +239,65 @@ __device__ __forceinline__ void warp_scan_coarse(T* v) {
     v[lane * kPer + i] = run;
     run += x[i];
   }
-  if (lane == 31) v[kCoarse] = run;
-}
-
-// A place in the list of row tiles.
-struct Cursor {
-  int tile;      // row tile, counted over all problems
-  int prob, rt;  // its problem, and its number in it
-  Problem pr;
-};
-
-template <int C>
-__device__ __forceinline__ Cursor seek_tile(const AttnParams& P, const Schedule<C>& S, int tile) {
-  int lo = 0, hi = C;  // tiles[lo] <= tile < tiles[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (S.tiles[mid] <= tile) lo = mid; else hi = mid;
-  }
-  Cursor c;
-  c.tile = tile;
-  c.prob = lo * S.per_prob;
-  c.rt = tile - S.tiles[lo];
-  for (;;) {
-    const int n = problem_row_tiles(P, c.prob);
-    if (c.rt < n || c.prob + 1 >= S.n_prob) break;
-    c.rt -= n;
-    ++c.prob;
-  }
-  c.pr = load_problem(P, c.prob);
-  return c;
-}
-
-// The next row tile; the caller knows that there is one.
-template <int C>
-__device__ __forceinline__ void next_tile(const AttnParams& P, const Schedule<C>& S, Cursor* c) {
-  ++c->tile;
-  ++c->rt;
-  if (static_cast<int64_t>(c->rt) * P.rows < c->pr.n_rows) return;
-  c->rt = 0;
-  while (c->prob + 1 < S.n_prob) {
-    ++c->prob;
-    if (problem_row_tiles(P, c->prob) > 0) break;
-  }
-  c->pr = load_problem(P, c->prob);
+  if (lane == 31) v[C] = run;
 }
 
 // All threads of the CTA; ends with a barrier.
 template <int C>
 __device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule<C>& S) {
-  const int tid = threadIdx.x, nt = blockDim.x;
   const int n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
   const int per_prob = (n_prob + C - 1) / C;
-  for (int e = tid; e < C; e += nt) {
-    int n = 0;
-    for (int p = e * per_prob; p < min(n_prob, (e + 1) * per_prob); ++p)
-      n += problem_row_tiles(P, p);
-    S.tiles[e] = n;
+  for (int e = threadIdx.x; e < C; e += blockDim.x) {
+    S.units[e] = 0;
+    S.tiles[e] = 0;
   }
   __syncthreads();
-  if (tid < 32) {
+  // a lane takes a problem; those of many row tiles are added up by the warp
+  const int lane = threadIdx.x & 31;
+  for (int p0 = threadIdx.x & ~31; p0 < n_prob; p0 += blockDim.x) {
+    const int p = p0 + lane;
+    Problem pr = {};
+    if (p < n_prob) pr = load_problem(P, p);
+    const int n = (pr.n_rows + P.rows - 1) / P.rows;
+    int64_t units = 0;
+    if (n == 1) units = row_tile(P, pr, 0).n_tiles + P.over;
+    for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many != 0; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      Problem x;
+      x.n_rows = __shfl_sync(0xffffffffu, pr.n_rows, src);
+      x.base = __shfl_sync(0xffffffffu, pr.base, src);
+      x.k_lo = __shfl_sync(0xffffffffu, pr.k_lo, src);
+      x.k_hi = __shfl_sync(0xffffffffu, pr.k_hi, src);
+      const int64_t all = problem_units(P, x);
+      if (lane == src) units = all;
+    }
+    if (n > 0) {
+      const int e = per_prob == 1 ? p : p / per_prob;
+      atomicAdd(reinterpret_cast<unsigned long long*>(&S.units[e]),
+                static_cast<unsigned long long>(units));
+      atomicAdd(&S.tiles[e], n);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    warp_scan_coarse<C>(S.units);
     warp_scan_coarse<C>(S.tiles);
-    if (tid == 31) {
-      // more rows than T allows (lengths out of order): the rest is dropped
-      int n = S.tiles[C];
-      if (n > P.max_row_tiles) {
-        flag_error(P.err, LORA_DEVERR_BAD_LEN);
-        n = P.max_row_tiles;
-      }
+    if (threadIdx.x == 31) {
+      // More row tiles than T allows (lengths out of order), or more units than
+      // a call could ever work off (2^31 of them read 10^14 bytes): refused.
+      const int64_t total = S.units[C] * P.kv.n_kv_heads;
+      const int items = S.tiles[C] * P.kv.n_kv_heads;
+      const bool ok = S.tiles[C] <= P.max_row_tiles && total <= INT32_MAX;
+      if (!ok) flag_error(P.err, LORA_DEVERR_BAD_LEN);
       S.n_prob = n_prob;
       S.per_prob = per_prob;
-      S.n_tiles = n;
-      S.per_tile = (n + C - 1) / C;
-    }
-  }
-  __syncthreads();
-  const int per_tile = S.per_tile, n_tiles = S.n_tiles;
-  for (int e = tid; e < C; e += nt) {
-    int64_t n = 0;
-    const int j0 = e * per_tile, j1 = min(n_tiles, j0 + per_tile);
-    if (j0 < j1) {
-      Cursor c = seek_tile(P, S, j0);
-      for (;;) {
-        n += row_tile(P, c.pr, c.rt).n_tiles + P.over;
-        if (c.tile + 1 >= j1) break;
-        next_tile(P, S, &c);
-      }
-    }
-    S.units[e] = n;
-  }
-  __syncthreads();
-  if (tid < 32) {
-    warp_scan_coarse<C>(S.units);
-    if (tid == 31) {
-      S.total = S.units[C] * P.kv.n_kv_heads;
-      const int64_t even = (S.total + gridDim.x - 1) / gridDim.x;
-      S.share = even > P.min_share ? even : P.min_share;
+      S.total = ok ? static_cast<int>(total) : 0;
+      // Equal shares, but an item of a few key tiles is not worth splitting,
+      // nor is less than four tiles worth a CTA.
+      const int even = (S.total + gridDim.x - 1) / gridDim.x;
+      const int span = items > 0 ? (S.total + items - 1) / items : 1;
+      const int least = span <= 8 ? span : 4;
+      S.share = even > least ? even : least;
     }
   }
   __syncthreads();
@@ -339,70 +313,114 @@ struct Segment {
   RowTile t;
   int item;          // its counter
   int cta0, parts;   // the CTAs that share the item: cta0 .. cta0 + parts - 1
+  int tile0;         // key tiles of this CTA before the segment
   int slot;          // where this CTA's part goes, if parts > 1
 };
 
 // Walks a CTA's share (one warp, all lanes alike).
-template <int C>
 struct Walker {
-  Cursor c;
+  Problem pr;
   RowTile t;
-  int64_t u, end;    // next unit, end of the share
-  int64_t tile_unit; // first unit of the row tile
+  int prob, rt;   // the problem, and the row tile's number in it
+  int tile;       // and over all problems
+  int u, end;     // next unit, end of the share
+  int tile_unit;  // first unit of the row tile
+  int done = 0;   // key tiles of the segments so far
 
+  __device__ __forceinline__ int units(const AttnParams& P) const {  // of the row tile
+    return (t.n_tiles + P.over) * P.kv.n_kv_heads;
+  }
+  template <int C>
   __device__ __forceinline__ void start(const AttnParams& P, const Schedule<C>& S) {
-    u = S.share * blockIdx.x;
-    end = u + S.share < S.total ? u + S.share : S.total;
+    u = min(S.total, S.share * static_cast<int>(blockIdx.x));  // (below 2^31: see build_schedule)
+    if (static_cast<int64_t>(S.share) * blockIdx.x >= S.total) u = S.total;
+    end = S.total - u < S.share ? S.total : u + S.share;
     if (u >= end) return;
-    const int hk = P.kv.n_kv_heads;
+    const int hk = P.kv.n_kv_heads, lane = threadIdx.x & 31;
     int lo = 0, hi = C;  // units[lo] * hk <= u < units[hi] * hk
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (S.units[mid] * hk <= u) lo = mid; else hi = mid;
     }
-    c = seek_tile(P, S, lo * S.per_tile);
-    tile_unit = S.units[lo] * hk;
-    t = row_tile(P, c.pr, c.rt);
-    while (tile_unit + units(P) <= u) advance(P, S);
+    prob = lo * S.per_prob;
+    tile = S.tiles[lo];
+    tile_unit = static_cast<int>(S.units[lo]) * hk;
+    for (;;) {  // the problem in the coarse entry
+      pr = load_problem(P, prob);
+      if (S.per_prob == 1) break;
+      const int span = static_cast<int>(problem_units(P, pr)) * hk;
+      if (tile_unit + span > u || prob + 1 >= S.n_prob) break;
+      tile_unit += span;
+      tile += (pr.n_rows + P.rows - 1) / P.rows;
+      ++prob;
+    }
+    const int n = (pr.n_rows + P.rows - 1) / P.rows;
+    for (rt = 0;; rt += 32) {  // the row tile in the problem, 32 at a time
+      int own = rt + lane < n ? (row_tile(P, pr, rt + lane).n_tiles + P.over) * hk : 0, incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, tile_unit + incl > u);
+      const int k = past != 0 ? __ffs(past) - 1 : 31;
+      const int before = __shfl_sync(0xffffffffu, incl - own, k);
+      if (past != 0 || rt + 32 >= n) {
+        tile_unit += before;
+        rt += k;
+        break;
+      }
+      tile_unit += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    tile += rt;
+    t = row_tile(P, pr, rt);
   }
-  __device__ __forceinline__ int64_t units(const AttnParams& P) const {  // of the row tile
-    return static_cast<int64_t>(t.n_tiles + P.over) * P.kv.n_kv_heads;
-  }
+  // The next row tile; there is one while u is below the total.
+  template <int C>
   __device__ __forceinline__ void advance(const AttnParams& P, const Schedule<C>& S) {
     tile_unit += units(P);
-    next_tile(P, S, &c);
-    t = row_tile(P, c.pr, c.rt);
+    ++tile;
+    ++rt;
+    if (rt * P.rows >= pr.n_rows) {
+      rt = 0;
+      do {
+        ++prob;
+        pr = load_problem(P, prob);
+      } while (pr.n_rows == 0 && prob + 1 < S.n_prob);
+    }
+    t = row_tile(P, pr, rt);
   }
+  template <int C>
   __device__ __forceinline__ Segment next(const AttnParams& P, const Schedule<C>& S) {
     Segment g;
     g.n = 0;
     if (u >= end) return g;
     while (tile_unit + units(P) <= u) advance(P, S);
     const int span = t.n_tiles + P.over;
-    g.head = static_cast<int>((u - tile_unit) / span);
-    const int64_t a = tile_unit + static_cast<int64_t>(g.head) * span + P.over;
-    const int64_t b = a + t.n_tiles;
+    g.head = (u - tile_unit) / span;
+    const int a = tile_unit + g.head * span + P.over;
+    const int b = a + t.n_tiles;
     if (u < a) u = a;
     if (u >= end) return g;  // the share ends in front of the item's key tiles
-    g.first = static_cast<int>(u - a);
-    g.n = static_cast<int>((end < b ? end : b) - u);
-    g.table_row = c.pr.table_row;
-    g.tok0 = c.pr.tok0;
-    g.base = c.pr.base;
-    g.k_lo = c.pr.k_lo;
-    g.shared = c.pr.k_lo > 0 ? 1 : 0;
+    g.first = u - a;
+    g.n = (end < b ? end : b) - u;
+    g.table_row = pr.table_row;
+    g.tok0 = pr.tok0;
+    g.base = pr.base;
+    g.k_lo = pr.k_lo;
+    g.shared = pr.k_lo > 0 ? 1 : 0;
     g.t = t;
-    g.item = c.tile * P.kv.n_kv_heads + g.head;
+    g.item = tile * P.kv.n_kv_heads + g.head;
     // (only key tiles make a CTA one of the item's)
-    const int64_t mine = S.share * blockIdx.x;
-    if (a >= mine && b <= mine + S.share) {
-      g.cta0 = blockIdx.x;
-      g.parts = 1;
-    } else {
-      g.cta0 = static_cast<int>(a / S.share);
-      g.parts = static_cast<int>((b - 1) / S.share) - g.cta0 + 1;
+    g.cta0 = blockIdx.x;
+    g.parts = 1;
+    if (g.n < t.n_tiles) {
+      g.cta0 = a / S.share;
+      g.parts = (b - 1) / S.share - g.cta0 + 1;
     }
     g.slot = blockIdx.x == g.cta0 ? 1 : 0;
+    g.tile0 = done;
+    done += g.n;
     u += g.n;
     return g;
   }

@@ -154,25 +154,26 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, 
       : "memory");
 }
 
-// Brings in the K or V rows of a key tile: a box per page (or per 128 rows of a
-// larger one), each box in the hands of a lane, which looks its page up.
-// Pages that no row sees are not touched.  A page that is missing is asked for
-// past the cache's end, where the tensor map reads zeros.  One warp.
+// Brings in the K and V rows of key tiles: a box per page (or per 128 rows of a
+// larger one).  The page ids of 32 boxes are looked up at once, a lane each, and
+// the next 32 ahead of their use.  Pages that no row sees are not touched.  A
+// page that is missing is asked for past the cache's end, where the tensor map
+// reads zeros.  One warp; the tiles of a segment in their order.
 template <int D>
 struct TileLoader {
-  int page, lg_page, box, boxes;
+  int page, lg_page, box, boxes, per;
+  int now, next;  // where this lane's box starts in the cache, in groups of eight
+                  // rows, for two batches of `per` tiles; -1: not needed
   __device__ __forceinline__ explicit TileLoader(const AttnParams& P)
       : page(P.kv.page_size),
         lg_page(P.lg_page),
         box(page < kKeys ? page : kKeys),
-        boxes(kKeys / box) {}
-  // Where this lane's box of the segment's i-th tile starts in the cache, in
-  // groups of eight rows; -1: not needed.
-  __device__ __forceinline__ int lookup(const AttnParams& P, const Segment& g, int i) const {
-    const int lane = threadIdx.x & 31;
-    const int key0 = key_tile(g.t, g.first + i) * kKeys + lane * box;
-    if (lane >= boxes || !((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) ||
-                           key0 < g.t.n_sink))
+        boxes(kKeys / box),
+        per(32 / boxes) {}
+  __device__ __forceinline__ int lookup(const AttnParams& P, const Segment& g, int i0) const {
+    const int lane = threadIdx.x & 31, i = i0 + lane / boxes;
+    const int key0 = key_tile(g.t, g.first + i) * kKeys + (lane & (boxes - 1)) * box;
+    if (i >= g.n || !((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) || key0 < g.t.n_sink))
       return -1;
     const int id =
         P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages + (key0 >> lg_page)];
@@ -182,14 +183,31 @@ struct TileLoader {
     }
     return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (key0 & (page - 1)) / 8;
   }
-  __device__ __forceinline__ void load(const CUtensorMap* tm, uint64_t* full, uint8_t* dst,
-                                       int at) const {
+  __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
+    now = lookup(P, g, 0);
+    next = g.n > per ? lookup(P, g, per) : -1;
+  }
+  // The place of this lane's box of tile i (lanes below `boxes`).
+  __device__ __forceinline__ int at(const AttnParams& P, const Segment& g, int i) {
+    const int k = i % per;
+    if (k == 0 && i > 0) {
+      now = next;
+      next = i + per < g.n ? lookup(P, g, i + per) : -1;
+    }
     const int lane = threadIdx.x & 31;
-    const uint32_t bytes = static_cast<uint32_t>(box) * D * 2;
-    const uint32_t all = __popc(__ballot_sync(0xffffffffu, at >= 0)) * bytes;
+    const int x = __shfl_sync(0xffffffffu, now, k * boxes + (lane & (boxes - 1)));
+    return lane < boxes ? x : -1;
+  }
+  __device__ __forceinline__ uint32_t bytes(int at) const {  // of all lanes' boxes
+    return __popc(__ballot_sync(0xffffffffu, at >= 0)) * box_bytes();
+  }
+  __device__ __forceinline__ uint32_t box_bytes() const { return static_cast<uint32_t>(box) * D * 2; }
+  __device__ __forceinline__ void load(const CUtensorMap* tm, uint64_t* full, uint8_t* dst, int at,
+                                       uint32_t all) const {
+    const int lane = threadIdx.x & 31;
     if (lane == 0) ptx::mbar_arrive_expect_tx(full, all);
     __syncwarp();
-    if (at >= 0) tma_load_4d(dst + lane * bytes, tm, full, at);
+    if (at >= 0) tma_load_4d(dst + lane * box_bytes(), tm, full, at);
   }
 };
 
@@ -224,10 +242,10 @@ struct RowWriter {
   bf16* out;
   float* prior;
   bool to_prior, join;
-  __device__ __forceinline__ RowWriter(const AttnParams& P, const Segment& g, int64_t t, int h,
+  __device__ __forceinline__ RowWriter(const AttnParams& P, int shared, int64_t t, int h,
                                        bool in_use, float m, float sum) {
     to_prior = P.groups_phase;
-    join = !to_prior && g.shared;
+    join = !to_prior && shared;
     own = sum > 0.f ? 1.f / sum : 0.f;
     other = 0.f;
     out = P.out + t * P.out_stride + h * D;
@@ -271,15 +289,15 @@ __device__ __forceinline__ int64_t part_slot(const Segment& g, int c) {
 }
 
 // Threads of named barrier `bar` (cnt of them) have written this CTA's part:
-// is it the last of the item (or of its half)?  Leaves the counter at zero.
-__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, int counter,
-                                               bool leader, int* flag, int bar, int cnt) {
+// is it the item's last?  Leaves the counter at zero.
+__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, bool leader,
+                                               int* flag, int bar, int cnt) {
   __threadfence();
   named_bar(bar, cnt);
   if (leader) {
-    const uint32_t before = atomicAdd(&P.count[counter], 1u);
+    const uint32_t before = atomicAdd(&P.count[g.item], 1u);
     *flag = before + 1 == static_cast<uint32_t>(g.parts) ? 1 : 0;
-    if (*flag) P.count[counter] = 0;
+    if (*flag) P.count[g.item] = 0;
     __threadfence();
   }
   named_bar(bar, cnt);

@@ -34,7 +34,7 @@ Shape shape_of(int64_t tokens, int group) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t count, part, part_ml, prior, prior_lse, bytes;
+  size_t count, split, part, part_ml, prior, prior_lse, bytes;
   int max_row_tiles[2];  // sequences, groups
   Shape shape[2];
 };
@@ -50,12 +50,13 @@ Layout layout(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
   for (int i = 0; i < (n_groups > 0 ? 2 : 1); ++i) {
     const int64_t tiles = total / w.shape[i].rows + (i == 0 ? kv.n_seqs : n_groups);
     w.max_row_tiles[i] = static_cast<int>(tiles);
-    if (2 * tiles > items) items = 2 * tiles;
+    if (tiles > items) items = tiles;
     if (w.shape[i].space > space) space = w.shape[i].space;
   }
   const size_t slots = static_cast<size_t>(kDecodeScheduleCtas) * 2 * space;
   w.count = 256;
-  w.part = up256(w.count + static_cast<size_t>(items) * kv.n_kv_heads * 4);
+  w.split = up256(w.count + static_cast<size_t>(items) * kv.n_kv_heads * 4);
+  w.part = up256(w.split + kDecodeScheduleCtas * sizeof(SplitItem));
   w.part_ml = w.part + slots * kv.head_dim * 4;
   w.prior = up256(w.part_ml + slots * 8);
   const size_t rows_all = n_groups > 0 ? static_cast<size_t>(kv.T) * n_q_heads : 0;
@@ -120,6 +121,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.n_sink = a.n_sink;
   P.err = static_cast<uint32_t*>(a.ws);
   P.count = reinterpret_cast<uint32_t*>(base + w.count);
+  P.split = reinterpret_cast<SplitItem*>(base + w.split);
   P.part = reinterpret_cast<float*>(base + w.part);
   P.part_ml = reinterpret_cast<float*>(base + w.part_ml);
   P.prior = reinterpret_cast<float*>(base + w.prior);
@@ -128,7 +130,6 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.groups_phase = phase == 1;
     P.max_row_tiles = w.max_row_tiles[phase];
     P.rows = w.shape[phase].rows;
-    P.min_share = 2;
     P.over = w.shape[phase].prefill ? 2 : 1;
     cudaError_t e;
     if (w.shape[phase].prefill) {

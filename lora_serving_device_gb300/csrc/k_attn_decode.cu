@@ -15,12 +15,12 @@
 //
 // Bound by reading the cache: 4 D bytes a key and key head.  A tile's K and V
 // are brought in by TMA, one box per page and tensor, through a ring that takes
-// most of the shared memory; what the tensor cores and the one softmax
-// warpgroup spend on a tile is a fraction of the time its bytes need.  The keys
+// most of the shared memory; what the tensor cores and a softmax warpgroup
+// spend on a tile is a fraction of the time its bytes need.  The keys
 // stand in M, where 128 is the MMA's natural size, and the few rows in N, where
 // 16 is possible: padding costs nothing that is scarce.
 //
-// Warps: 0 = schedule and TMA, 1 = MMA issue, 2-5 = softmax and epilogue.
+// Warps: 0 = schedule and TMA, 1 = MMA issue, 2-5 and 6-9 = softmax and epilogue.
 // Every wait is bounded; on timeout the kernel raises LORA_DEVERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
@@ -31,52 +31,62 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kCoarse = 512;  // entries of the schedule's prefix sums
 constexpr int kRing = 4;      // segments that the producer may run ahead
 
 // A rows of a row tile: 4, 8, 16 or 32.  N is their number in Q K^T and kPV
 // the columns of P and O (A for the high halves from 0, A for the rest from
-// kPV / 2); the MMA wants at least 16.
+// kPV / 2); the MMA wants at least 16.  W softmax warpgroups take the segments
+// in turn, each with its own Q, P and O, so that one's first scores and last
+// results do not keep the next segment's tiles waiting (32 rows take the
+// registers of two).
 template <int D, int A>
 struct Lay {
+  static constexpr int W = A <= 16 ? 2 : 1;
+  static constexpr int kThreads = 64 + 128 * W;
   static constexpr int N = A < 16 ? 16 : A;
   static constexpr int kPV = A < 16 ? 16 : 2 * A;
   static constexpr uint32_t kTile = kKeys * D * 2;  // K or V of a tile
   static constexpr uint32_t kStage = 2 * kTile;
   static constexpr uint32_t kQ = N * D * 2;
   static constexpr uint32_t kP = kPV * kKeys * 2;
-  static constexpr int kPBufs = A <= 16 ? 2 : 1;
+  static constexpr int kPBufs = A <= 8 ? 2 : 1;
+  static constexpr int kSBufs = 2;
   static constexpr int kStages = 196608u / kStage;
   static constexpr uint32_t oQ = kStages * kStage;
-  static constexpr uint32_t oP = oQ + kQ;
-  static constexpr uint32_t oMisc = oP + kPBufs * kP;
-};
-
-template <int A, int kStages>
-struct Misc {
-  Schedule<kCoarse> sched;
-  Segment ring[kRing];
-  float4 red[A];  // of a row: the four warps' maxima or sums
-  int row_hi[A], row_lo[A];
-  uint64_t full_k[kStages], full_v[kStages], empty[kStages];
-  uint64_t s_full[2], s_empty[2], p_full[2], p_done[2];
-  uint64_t q_full, o_empty;
-  uint64_t seg_full[kRing], seg_empty[kRing];
-  uint32_t tmem;
-  int abort;
-  int last;
+  static constexpr uint32_t oP = oQ + W * kQ;
+  static constexpr uint32_t oMisc = oP + W * kPBufs * kP;
 };
 
 template <int D, int A>
-__global__ void __launch_bounds__(kThreads, 1)
+struct Misc {
+  using La = Lay<D, A>;
+  static constexpr int W = La::W, kStages = La::kStages;
+  Schedule<kCoarse> sched;
+  Segment ring[kRing];
+  float4 red[W][A];  // of a row: the four warps' maxima or sums
+  int row_hi[W][A], row_lo[W][A];
+  uint64_t full_k[kStages], full_v[kStages], empty[kStages];
+  uint64_t s_full[W][La::kSBufs], s_empty[W][La::kSBufs];
+  uint64_t p_full[W][La::kPBufs], p_done[W][La::kPBufs];
+  uint64_t q_full[W], o_empty[W];
+  uint64_t seg_full[kRing], seg_empty[kRing];
+  uint32_t tmem;
+  int abort;
+  int last[W];
+};
+
+template <int D, int A>
+__global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
   using La = Lay<D, A>;
   constexpr int N = La::N, kPV = La::kPV;
-  constexpr int kStages = La::kStages, PB = La::kPBufs;
-  using Mi = Misc<A, kStages>;
-  constexpr uint32_t kCols = 2 * N + kPV <= 64 ? 64 : 2 * N + kPV <= 128 ? 128 : 256;
+  constexpr int W = La::W, kStages = La::kStages, PB = La::kPBufs, SB = La::kSBufs;
+  using Mi = Misc<D, A>;
+  constexpr uint32_t kUsed = W * (SB * N + kPV);  // S, then O
+  constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  static_assert(kUsed <= 256, "tensor memory");
   constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kKeys, N, false, false);
   constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(D, kPV, true, false);
   constexpr uint32_t kGroupBytes = (D / 64) * 1024;  // eight keys
@@ -96,14 +106,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&M.full_v[i], 1);
       ptx::mbar_init(&M.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&M.s_full[i], 1);
-      ptx::mbar_init(&M.s_empty[i], 4);
-      ptx::mbar_init(&M.p_full[i], 4);
-      ptx::mbar_init(&M.p_done[i], 1);
+    for (int w = 0; w < W; ++w) {
+      for (int i = 0; i < SB; ++i) {
+        ptx::mbar_init(&M.s_full[w][i], 1);
+        ptx::mbar_init(&M.s_empty[w][i], 4);
+      }
+      for (int i = 0; i < PB; ++i) {
+        ptx::mbar_init(&M.p_full[w][i], 4);
+        ptx::mbar_init(&M.p_done[w][i], 1);
+      }
+      ptx::mbar_init(&M.q_full[w], 4);
+      ptx::mbar_init(&M.o_empty[w], 4);
     }
-    ptx::mbar_init(&M.q_full, 4);
-    ptx::mbar_init(&M.o_empty, 4);
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(&M.seg_full[i], 1);
       ptx::mbar_init(&M.seg_empty[i], 5);
@@ -121,14 +135,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   build_schedule(P, M.sched);  // ends with a barrier
   ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;
-  const uint32_t tmem_o = tmem + 2 * N;  // after two buffers of S
+  const uint32_t tmem_o = tmem + W * SB * N;  // after the buffers of S
 
   if (warp == 0) {
     // ---------------- schedule and TMA ----------------------------------
-    Walker<kCoarse> walk;
+    Walker walk;
     walk.start(P, M.sched);
-    const TileLoader<D> load(P);
-    int tile = 0;
+    TileLoader<D> load(P);
+    int tile = 0, ends = 0;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       const Segment g = walk.next(P, M.sched);
@@ -140,17 +154,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(&M.seg_full[sg % kRing]);
       }
       __syncwarp();
-      if (g.n == 0) break;
-      int at = load.lookup(P, g, 0);  // page ids a tile ahead
+      if (g.n == 0) {
+        if (++ends == W) break;  // each warpgroup finds its own end
+        continue;
+      }
+      load.begin(P, g);
       for (int i = 0; i < g.n; ++i, ++tile) {
-        const int here = at;
-        if (i + 1 < g.n) at = load.lookup(P, g, i + 1);
+        const int at = load.at(P, g, i);
+        const uint32_t bytes = load.bytes(at);
         const int st = tile % kStages;
         if (tile >= kStages) ok = wait_all(&M.empty[st], ((tile / kStages) & 1) ^ 1, abort_f);
         if (!ok) break;
         uint8_t* K = smem + st * La::kStage;
-        load.load(&tm_k, &M.full_k[st], K, here);
-        load.load(&tm_v, &M.full_v[st], K + La::kTile, here);
+        load.load(&tm_k, &M.full_k[st], K, at, bytes);
+        load.load(&tm_v, &M.full_v[st], K + La::kTile, at, bytes);
       }
     }
     if (!ok) {
@@ -164,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------- MMA issue ------------------------------------------
     // One thread with two cursors over the same tiles: O += of tile pv as soon
-    // as its P is there, S of tile qk as soon as its K is; S runs at most two
-    // ahead.
+    // as its P is there, S of tile qk as soon as its K is there and one of its
+    // warpgroup's buffers is free.
     if (elect_one()) {
       const uint32_t stages = desc_lo(ptx::smem_u32(smem), 0);
       const uint32_t qa = desc_lo(ptx::smem_u32(smem + La::oQ), 16);
@@ -173,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t qk = 0, pv = 0;  // tiles issued
       uint32_t qs = 0, ps = 0;  // their segments
       int q_left = -1, p_left = 0;  // tiles to go in them; -1: header not read
+      uint32_t s0 = 0, s1 = 0, p0 = 0, p1 = 0;  // uses of each warpgroup's S and P
       bool q_first = true, p_first = true;
       Patience wait;
       for (;;) {
@@ -190,20 +208,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_left = M.ring[ps % kRing].n;
             p_first = true;
           }
-          if (ptx::mbar_test_wait(&M.p_full[pv % PB], (pv / PB) & 1) &&
+          const uint32_t w = ps % W, use = w ? p1 : p0;
+          if (ptx::mbar_test_wait(&M.p_full[w][use % PB], (use / PB) & 1) &&
               ptx::mbar_test_wait(&M.full_v[pv % kStages], (pv / kStages) & 1) &&
-              (!p_first || ps == 0 || ptx::mbar_test_wait(&M.o_empty, (ps - 1) & 1))) {
+              (!p_first || ps < W || ptx::mbar_test_wait(&M.o_empty[w], (ps / W - 1) & 1))) {
             ptx::tc_fence_after();
             const uint32_t st = pv % kStages;
             const uint32_t va = stages + (st * La::kStage + La::kTile) / 16 + ((1024u / 16) << 16);
-            const uint32_t pb = pa + (pv % PB) * (La::kP / 16);
+            const uint32_t pb = pa + (w * PB + use % PB) * (La::kP / 16);
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks)
-              mma_ss(tmem_o, va + ks * 2 * kGroupBytes / 16, desc_hi(kGroupBytes),
+              mma_ss(tmem_o + w * kPV, va + ks * 2 * kGroupBytes / 16, desc_hi(kGroupBytes),
                      pb + ((ks / 4) * (kPV * 128) + (ks % 4) * 32) / 16, desc_hi(1024), kIdescPV,
                      ks > 0 || !p_first ? 1u : 0u);
             ptx::mma_commit(&M.empty[st]);
-            ptx::mma_commit(&M.p_done[pv % PB]);
+            ptx::mma_commit(&M.p_done[w][use % PB]);
+            if (w) ++p1; else ++p0;
             ++pv;
             p_first = false;
             if (--p_left == 0) {
@@ -214,18 +234,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
         }
-        if (q_left > 0 && qk - pv < 2 &&
+        const uint32_t v = qs % W, s_use = v ? s1 : s0;
+        if (q_left > 0 &&
             ptx::mbar_test_wait(&M.full_k[qk % kStages], (qk / kStages) & 1) &&
-            (qk < 2 || ptx::mbar_test_wait(&M.s_empty[qk & 1], ((qk >> 1) & 1) ^ 1)) &&
-            (!q_first || ptx::mbar_test_wait(&M.q_full, qs & 1))) {
+            (s_use < SB || ptx::mbar_test_wait(&M.s_empty[v][s_use % SB], ((s_use / SB) & 1) ^ 1)) &&
+            (!q_first || ptx::mbar_test_wait(&M.q_full[v], (qs / W) & 1))) {
           ptx::tc_fence_after();
           const uint32_t ka = stages + (qk % kStages) * (La::kStage / 16) + (1u << 16);
+          const uint32_t qd = qa + v * (La::kQ / 16);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss(tmem + (qk & 1) * N, ka + ((ks / 4) * 1024 + (ks % 4) * 32) / 16,
-                   desc_hi(kGroupBytes), qa + ((ks / 4) * (N * 128) + (ks % 4) * 32) / 16,
+            mma_ss(tmem + (v * SB + s_use % SB) * N, ka + ((ks / 4) * 1024 + (ks % 4) * 32) / 16,
+                   desc_hi(kGroupBytes), qd + ((ks / 4) * (N * 128) + (ks % 4) * 32) / 16,
                    desc_hi(1024), kIdescQK, ks > 0 ? 1u : 0u);
-          ptx::mma_commit(&M.s_full[qk & 1]);
+          ptx::mma_commit(&M.s_full[v][s_use % SB]);
+          if (v) ++s1; else ++s0;
           ++qk;
           q_first = false;
           if (--q_left == 0) {
@@ -243,16 +266,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- softmax and epilogue --------------------------------
     const int w = warp & 3;                 // TMEM lanes 32w .. 32w + 31
     const int j = w * 32 + lane;            // this thread's key in a tile
-    const int st_tid = tid - 64;
+    const int wg = (warp - 2) / 4;          // warpgroup
+    const int st_tid = tid - 64 - wg * 128;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const bool has_d = D == 128 || lane < 16;   // M = 64 fills 16 lanes of each warp
     const int d = D == 128 ? j : w * 16 + lane;  // this thread's column of O
     const float c = P.scale_log2;
-    constexpr int kBar = 1;
+    const int kBar = 1 + wg;
+    float4* red = M.red[wg];
+    uint8_t* const Pbase = smem + La::oP + wg * PB * La::kP;
+    const uint32_t tm_o = tmem_o + wg * kPV + lanes;
+    uint64_t* const p_full = M.p_full[wg];
+    uint64_t* const p_done = M.p_done[wg];
 
     // Q of a segment into shared memory, rows past the last as zeros
     auto load_q = [&](const Segment& g) {
-      uint8_t* Q = smem + La::oQ;
+      uint8_t* Q = smem + La::oQ + wg * La::kQ;
 #pragma unroll
       for (int i = st_tid; i < N * (D / 8); i += 128) {
         const int n = i / (D / 8), ch = i % (D / 8);
@@ -268,27 +297,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&M.q_full);
+      if (lane == 0) ptx::mbar_arrive(&M.q_full[wg]);
     };
 
     // The four warps meet at barriers, so none leaves on its own: after a
     // wait that gave up they run on (every later wait returns at once) to
     // the vote at the next segment.
-    uint32_t tile = 0;  // tiles of this CTA so far
-    bool ok = wait_all(&M.seg_full[0], 0, abort_f);
-    if (ok && M.ring[0].n > 0) load_q(M.ring[0]);
-    for (int sg = 0; !named_any(kBar, 128, !ok || *abort_f); ++sg) {
+    uint32_t tile = 0;  // tiles of this warpgroup so far
+    for (int sg = wg;; sg += W) {
+      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (named_any(kBar, 128, *abort_f != 0)) break;
       const Segment g = M.ring[sg % kRing];
       if (g.n == 0) break;
+      load_q(g);  // (the MMAs that read the last one's are done: so are its scores)
       // limits of the rows (rows past the last copy row 0's)
       for (int n = st_tid; n < A; n += 128) {
         const int pos = g.base + (g.t.row0 + (n < g.t.n_rows ? n : 0)) / P.group;
-        M.row_hi[n] = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
-        M.row_lo[n] =
+        M.row_hi[wg][n] = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
+        M.row_lo[wg][n] =
             P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
       }
       named_bar(kBar, 128);
-      int min_hi = M.row_hi[lane % A], max_lo = M.row_lo[lane % A];
+      int min_hi = M.row_hi[wg][lane % A], max_lo = M.row_lo[wg][lane % A];
       min_hi = __reduce_min_sync(0xffffffffu, min_hi);
       max_lo = __reduce_max_sync(0xffffffffu, max_lo);
       // of each row: minus the reference maximum (log2 units; +inf: none yet)
@@ -302,28 +332,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys, key = key0 + j;
-        wait_quiet(&M.s_full[tile & 1], (tile >> 1) & 1, abort_f);
+        const uint32_t in_cta = g.tile0 + i;
+        wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
         float s[N];
 #pragma unroll
         for (int n = 0; n < N; n += 16)
-          ptx::tmem_ld16(tmem + lanes + (tile & 1) * N + n,
+          ptx::tmem_ld16(tmem + lanes + (wg * SB + tile % SB) * N + n,
                          *reinterpret_cast<uint32_t(*)[16]>(s + n));
         ptx::tmem_ld_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.s_empty[tile & 1]);
-        if (i == g.n - 1) {
-          // the last S is here, so Q's buffer is free: fetch the next one's
-          ok = wait_all(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
-          if (ok && M.ring[(sg + 1) % kRing].n > 0) load_q(M.ring[(sg + 1) % kRing]);
-        }
+        if (lane == 0) ptx::mbar_arrive(&M.s_empty[wg][tile % SB]);
         if (key0 < max_lo || key0 + kKeys - 1 > min_hi) {
 #pragma unroll
           for (int n = 0; n < A; ++n)
-            s[n] = (key > M.row_hi[n]) | ((key < M.row_lo[n]) & (key >= g.t.n_sink)) ? -INFINITY
-                                                                                 : s[n];
+            s[n] = (key > M.row_hi[wg][n]) | ((key < M.row_lo[wg][n]) & (key >= g.t.n_sink))
+                       ? -INFINITY
+                       : s[n];
         }
         // does a score exceed its reference maximum by more than 8?
         bool up = false;
@@ -333,13 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int n = 0; n < A; ++n) {
             const float mx = warp_max(s[n]);
-            if (lane == 0) reinterpret_cast<float*>(&M.red[n])[w] = mx;
+            if (lane == 0) reinterpret_cast<float*>(&red[n])[w] = mx;
           }
           named_bar(kBar, 128);
           float fac[A];
 #pragma unroll
           for (int n = 0; n < A; ++n) {
-            const float4 r = M.red[n];
+            const float4 r = red[n];
             const float mx = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)) * c;
             const float now = fminf(neg[n], -mx);
             fac[n] = neg[n] == INFINITY ? 0.f : exp2_fast(now - neg[n]);
@@ -347,30 +374,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[n] *= fac[n];
           }
           if (i > 0) {
-            wait_quiet(&M.p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
+            wait_quiet(&p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
             __syncwarp();
             ptx::tc_fence_after();
 #pragma unroll
             for (int n = 0; n < kPV; n += 16) {
               uint32_t o[16];
-              ptx::tmem_ld16(tmem_o + lanes + n, o);
+              ptx::tmem_ld16(tm_o + n, o);
               ptx::tmem_ld_wait();
 #pragma unroll
               for (int x = 0; x < 16; ++x)
                 o[x] = __float_as_uint(__uint_as_float(o[x]) * fac[(n + x) % (kPV / 2) % A]);
-              ptx::tmem_st16(tmem_o + lanes + n, o);
+              ptx::tmem_st16(tm_o + n, o);
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
           }
         }
         if (tile_has_unseen(g.t, key0)) {
-          wait_quiet(&M.full_v[tile % kStages], (tile / kStages) & 1, abort_f);
-          zero_unseen_value<D>(g.t, key0, j, smem + (tile % kStages) * La::kStage + La::kTile);
+          wait_quiet(&M.full_v[in_cta % kStages], (in_cta / kStages) & 1, abort_f);
+          zero_unseen_value<D>(g.t, key0, j, smem + (in_cta % kStages) * La::kStage + La::kTile);
         }
         // P's buffer is free once the product that read it is done
-        if (tile >= PB) wait_quiet(&M.p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
-        uint8_t* Pb = smem + La::oP + (tile % PB) * La::kP + (j / 64) * (kPV * 128) + (j % 8) * 2;
+        if (tile >= PB) wait_quiet(&p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
+        uint8_t* Pb = Pbase + (tile % PB) * La::kP + (j / 64) * (kPV * 128) + (j % 8) * 2;
         const int ch = (j % 64) / 8;
 #pragma unroll
         for (int n = 0; n < A; ++n) {
@@ -383,16 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.p_full[tile % PB]);
+        if (lane == 0) ptx::mbar_arrive(&p_full[tile % PB]);
       }
 
       // ---- the item, or this CTA's part of it, is done
 #pragma unroll
       for (int n = 0; n < A; ++n) {
         const float x = warp_sum(l[n]);
-        if (lane == 0) reinterpret_cast<float*>(&M.red[n])[w] = x;
+        if (lane == 0) reinterpret_cast<float*>(&red[n])[w] = x;
       }
-      wait_quiet(&M.p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
+      wait_quiet(&p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
       __syncwarp();
       ptx::tc_fence_after();
       named_bar(kBar, 128);
@@ -402,15 +429,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int n0 = 0; n0 < A; n0 += 16) {
         uint32_t oh[16], ol[16];
-        ptx::tmem_ld16(tmem_o + lanes + n0, oh);
-        if (A >= 16) ptx::tmem_ld16(tmem_o + lanes + kPV / 2 + n0, ol);
+        ptx::tmem_ld16(tm_o + n0, oh);
+        if (A >= 16) ptx::tmem_ld16(tm_o + kPV / 2 + n0, ol);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int x = 0; x < (A < 16 ? A : 16); ++x) {
           const int n = n0 + x;
           const float o = __uint_as_float(oh[x]) + __uint_as_float(A >= 16 ? ol[x] : oh[x + 8]);
           if (n < g.t.n_rows) {
-            const float4 r = M.red[n];
+            const float4 r = red[n];
             if (!has_d)
               ;
             else if (g.parts > 1)
@@ -425,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        ptx::mbar_arrive(&M.o_empty);
+        ptx::mbar_arrive(&M.o_empty[wg]);
         ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
       }
       if (g.parts > 1) {
@@ -433,14 +460,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int n = 0; n < A; ++n) {
           if (st_tid == n) {
-            const float4 r = M.red[n];
+            const float4 r = red[n];
             ml[slot * A + n] = make_float2(-neg[n], r.x + r.y + r.z + r.w);
           }
         }
-        if (last_to_arrive(P, g, g.item, st_tid == 0, &M.last, kBar, 128)) {
+        if (last_to_arrive(P, g, st_tid == 0, &M.last[wg], kBar, 128)) {
           // all parts' maxima and sums by way of P's buffer, which is free
           constexpr int kChunk = La::kP / (A * 8);
-          float2* all = reinterpret_cast<float2*>(smem + La::oP);
+          float2* all = reinterpret_cast<float2*>(Pbase);
           float o[A], top[A], sum[A];
 #pragma unroll
           for (int n = 0; n < A; ++n) o[n] = sum[n] = 0.f, top[n] = -INFINITY;
@@ -501,7 +528,7 @@ template <int D, int A>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& P,
                    cudaStream_t st, const DeviceInfo& dev) {
   using La = Lay<D, A>;
-  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<A, La::kStages>);
+  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<D, A>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
   auto kern = attn_decode_kernel<D, A>;
@@ -510,7 +537,7 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnP
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kDecodeScheduleCtas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(La::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

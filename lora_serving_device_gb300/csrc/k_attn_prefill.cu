@@ -59,7 +59,6 @@ struct Misc {
   uint64_t seg_full[kRing], seg_empty[kRing];
   uint32_t tmem;
   int abort;
-  int last[2];
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -159,12 +158,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLeast));
   if (warp == 8) {
     // ---------------- schedule and TMA ----------------------------------
-    Walker<kCoarse> walk;
+    Walker walk;
     walk.start(P, M.sched);
-    const TileLoader<D> load(P);
+    TileLoader<D> load(P);
     int n = 0;              // tiles brought in: K in slot 2n, V in slot 2n + 1
     int q_use[2] = {0, 0};  // segments of each half
     bool ok = true;
+    SplitItem mine = {};
     for (int sg = 0; ok; ++sg) {
       const Segment g = walk.next(P, M.sched);
       if (sg >= kRing)
@@ -176,7 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (g.n == 0) break;
-      int at = load.lookup(P, g, 0);
+      load.begin(P, g);
+      if (g.parts > 1 && g.cta0 == blockIdx.x)
+        mine = {g.parts, g.tok0, g.t.row0, g.t.n_rows, g.head, g.shared, {0, 0}};
       for (int h = 0; h < 2 && ok; ++h) {
         if (g.t.n_rows <= h * half_rows) break;
         if (q_use[h] > 0) ok = wait_all(&M.q_empty[h], (q_use[h] - 1) & 1, abort_f);
@@ -191,16 +193,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       for (int i = 0; i < g.n && ok; ++i, ++n) {
-        const int here = at;
-        if (i + 1 < g.n) at = load.lookup(P, g, i + 1);
+        const int at = load.at(P, g, i);
+        const uint32_t bytes = load.bytes(at);
         for (int v = 0; v < 2; ++v) {
           const int k = 2 * n + v, st = k % kSlots;
           if (k >= kSlots) ok = wait_all(&M.empty[st], ((k / kSlots) & 1) ^ 1, abort_f);
           if (!ok) break;
-          load.load(v ? &tm_v : &tm_k, &M.full[st], smem + st * La::kTile, here);
+          load.load(v ? &tm_v : &tm_k, &M.full[st], smem + st * La::kTile, at, bytes);
         }
       }
     }
+    if (lane == 0) P.split[blockIdx.x] = mine;
     if (!ok) {
       // gave up: what is on its way into shared memory has to land first
       int none = 0;
@@ -350,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = max3(mx, s[kKeys - 4], s[kKeys - 3]);
         my = max3(my, s[kKeys - 2], s[kKeys - 1]);
         mx = max3(mx, my, fmaxf(mz, mw)) * c;
-        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+        // (rows that are not in use hold anything: they have no say)
+        if (__any_sync(0xffffffffu, mine && mx > m + 8.f)) {
           const float now = fmaxf(m, mx);
           const float f = m == -INFINITY ? 0.f : exp2_fast(m - now);
           m = now;
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the item, or this CTA's part of it, is done
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
-      const RowWriter<D> out(P, g, g.tok0 + tok, head, mine && g.parts == 1, m, l);
+      const RowWriter<D> out(P, g.shared, g.tok0 + tok, head, mine && g.parts == 1, m, l);
       wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
       __syncwarp();
       ptx::tc_fence_after();
@@ -441,31 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[(k / 4) * kHalf] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         ml[slot * 2 * kHalf] = make_float2(m, l);
       }
-      if (last_to_arrive(P, g, g.item * 2 + h, row == 0, &M.last[h], bar, 128) && mine) {
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int q = 0; q < g.parts; ++q)
-          top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
-#pragma unroll
-        for (int k = 0; k < D; ++k) o[k] = 0.f;
-        for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
-          const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
-          const float f = exp2f(v.x - top);
-          sum += f * v.y;
-          const float4* from = part_row<D>(P, part_slot(g, q), h, row);
-#pragma unroll
-          for (int k = 0; k < D; k += 4) {
-            const float4 v4 = __ldcg(from + (k / 4) * kHalf);
-            o[k] += f * v4.x;
-            o[k + 1] += f * v4.y;
-            o[k + 2] += f * v4.z;
-            o[k + 3] += f * v4.w;
-          }
-        }
-        const RowWriter<D> joined(P, g, g.tok0 + tok, head, true, top, sum);
-#pragma unroll
-        for (int k = 0; k < D; k += 8) joined.write8(k, o + k);
-      }
     }
   }
 
@@ -476,6 +455,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_dealloc(tmem, 512);
   }
   if (tid == 0 && *abort_f) flag_error(P.err, LORA_DEVERR_TIMEOUT);
+}
+
+// Joins the parts of the items that several CTAs shared: block (c, x) takes 32
+// rows of the item that begins in CTA c and ends in another, if there is one.
+// A lane is a row; the parts' factors come first, then each warp adds up four
+// values a row at a time, so that all reads are whole lines, and the rows are
+// written from shared memory.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
+  __shared__ float fac[kDecodeScheduleCtas][32];
+  __shared__ float4 rows[32][D / 4 + 1];
+  __shared__ float top_s[32], sum_s[32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const SplitItem it = P.split[c];
+  const int half_rows = P.rows / 2;
+  const int h = blockIdx.y / 4, row = blockIdx.y % 4 * 32 + lane;  // half, row of the half
+  const int in_tile = h * half_rows + row;
+  if (it.parts <= 1 || blockIdx.y % 4 * 32 >= half_rows ||
+      h * half_rows + blockIdx.y % 4 * 32 >= it.n_rows)
+    return;
+  const bool used = row < half_rows && in_tile < it.n_rows;
+  auto slot = [&](int q) { return static_cast<int64_t>(c + q) * 2 + (q == 0 ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(P.part_ml) + h * kHalf + row;
+  // warp w looks at parts w, w + 8, ...; the maximum over all by shared memory
+  for (int q = warp; q < it.parts; q += 8) fac[q][lane] = used ? ml[slot(q) * 2 * kHalf].x : 0.f;
+  __syncthreads();
+  if (warp == 0) {
+    float top = -INFINITY, sum = 0.f;
+    for (int q = 0; q < it.parts; ++q) top = fmaxf(top, fac[q][lane]);
+    for (int q = 0; q < it.parts; ++q) {
+      const float f = top == -INFINITY ? 0.f : exp2f(fac[q][lane] - top);
+      fac[q][lane] = f;
+      sum += used ? f * ml[slot(q) * 2 * kHalf].y : 0.f;
+    }
+    top_s[lane] = top;
+    sum_s[lane] = sum;
+  }
+  __syncthreads();
+  for (int k = warp; k < D / 4; k += 8) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int q = 0; q < it.parts; ++q) {
+      const float f = fac[q][lane];
+      const float4 v = part_row<D>(P, slot(q), h, row)[k * kHalf];
+      o.x += f * v.x;
+      o.y += f * v.y;
+      o.z += f * v.z;
+      o.w += f * v.w;
+    }
+    rows[lane][k] = o;
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < 32 * (D / 8); x += 256) {
+    const int r = x / (D / 8), k = x % (D / 8);
+    const int at = blockIdx.y % 4 * 32 + r;
+    if (at >= half_rows || h * half_rows + at >= it.n_rows) continue;
+    const int in_prob = it.row0 + h * half_rows + at, tok = in_prob / P.group;
+    const RowWriter<D> out(P, it.shared, it.tok0 + tok, it.head * P.group + in_prob - tok * P.group,
+                           true, top_s[r], sum_s[r]);
+    float v[8];
+    *reinterpret_cast<float4*>(v) = rows[r][2 * k];
+    *reinterpret_cast<float4*>(v + 4) = rows[r][2 * k + 1];
+    out.write8(8 * k, v);
+  }
 }
 
 template <int D>
@@ -499,7 +544,11 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(kDecodeScheduleCtas, 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, P);
 }
 
 }  // namespace

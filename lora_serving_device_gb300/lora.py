@@ -641,22 +641,24 @@ class PagedKV:
                                     _ptr(kv_len), n_pages, page_size, n_kv_heads, head_dim, n_seqs,
                                     block_table.shape[1], T, T if max_q_len is None else max_q_len)
         self.ref = ctypes.addressof(self.struct)
+        self._device = k_cache.get_device()
+        self._bf16 = torch.bfloat16
+        self._current_stream = torch._C._cuda_getCurrentRawStream
 
-    def rows(self, x, n_heads=None, what="q"):
-        """Checks x [T, heads, head_dim] bf16 and returns its distance between tokens."""
-        import torch
+    def rows(self, x, n_heads, what):
+        """Checks x [T, n_heads, head_dim] bf16 and returns its distance between tokens."""
+        T, heads, d = self.T, n_heads, self.head_dim
         st = x.stride()
-        if x.dtype is not torch.bfloat16:
-            raise TypeError(f"{what}: unsupported dtype {x.dtype}")
-        if x.dim() != 3 or x.shape[0] != self.T or x.shape[2] != self.head_dim or \
-                (n_heads is not None and x.shape[1] != n_heads):
-            raise ValueError(f"{what}: shape {tuple(x.shape)}, need [{self.T}, "
-                             f"{'heads' if n_heads is None else n_heads}, {self.head_dim}]")
-        if st[2] != 1 or (x.shape[1] > 1 and st[1] != self.head_dim):
-            raise ValueError(f"{what}: heads of a token must be contiguous")
-        if x.device != self.k_cache.device:
-            raise ValueError(f"{what}: on {x.device}, the cache on {self.k_cache.device}")
-        return st[0] if self.T > 1 else x.shape[1] * x.shape[2]
+        if x.shape != (T, heads, d) or x.dtype is not self._bf16 or x.get_device() != self._device or \
+                st[2] != 1 or (st[1] != d and heads > 1):
+            if x.dtype is not self._bf16:
+                raise TypeError(f"{what}: unsupported dtype {x.dtype}")
+            raise ValueError(f"{what}: shape {tuple(x.shape)}, strides {st} on {x.device}; need [{T}, {heads}, "
+                             f"{d}] with the heads of a token contiguous, on the cache's device")
+        return st[0] if T > 1 else heads * d
+
+    def stream(self, stream):
+        return self._current_stream(self._device) if stream is None else stream.cuda_stream
 
 
 def attn_workspace(kv, n_q_heads, n_groups=0):
@@ -683,46 +685,52 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
     allowed).  q None: keys and values only.  cos_sin [n_pos, rot_dim] fp32 (rope_table) or
     None for no rotation.  pos: None (the position in the cache), [T], or [n_axes, T] with
     axis_pairs, the rotated pairs of each axis."""
-    import torch
-    n_q = 0
-    q_stride = q_out_stride = 0
+    n_q = q_stride = q_out_stride = 0
     if q is not None:
-        q_stride = kv.rows(q)
         n_q = q.shape[1]
+        q_stride = kv.rows(q, n_q, "q")
         if q_out is None:
-            q_out = torch.empty((kv.T, n_q, kv.head_dim), dtype=torch.bfloat16, device=q.device)
-        q_out_stride = kv.rows(q_out, n_q, "q_out")
-    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    if cos_sin is not None and (cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous()):
-        raise TypeError("cos_sin: contiguous fp32 [n_pos, rot_dim]")
-    n_axes = 1
+            q_out = q.new_empty(q.shape)
+            q_out_stride = n_q * kv.head_dim
+        else:
+            q_out_stride = kv.rows(q_out, n_q, "q_out")
+    n_pos = rot = 0
+    if cos_sin is not None:
+        n_pos, rot = cos_sin.shape
+        if cos_sin.element_size() != 4 or not cos_sin.is_floating_point() or not cos_sin.is_contiguous() or \
+                cos_sin.get_device() != kv._device:
+            raise TypeError("cos_sin: contiguous fp32 [n_pos, rot_dim] on the cache's device")
+    n_axes, pairs = 1, None
     if pos is not None:
-        n_axes = pos.numel() // kv.T if kv.T else 1
-        if pos.dtype is not torch.int32 or not pos.is_contiguous() or pos.shape[-1] != kv.T:
-            raise TypeError(f"pos: contiguous int32 [{kv.T}] or [n_axes, {kv.T}]")
-    pairs = None
+        n_axes = pos.shape[0] if pos.dim() == 2 else 1
+        if pos.element_size() != 4 or pos.is_floating_point() or not pos.is_contiguous() or \
+                pos.shape[-1] != kv.T or pos.get_device() != kv._device:
+            raise TypeError(f"pos: contiguous int32 [{kv.T}] or [n_axes, {kv.T}] on the cache's device")
     if axis_pairs is not None:
         if len(axis_pairs) != n_axes:
             raise ValueError(f"axis_pairs: {len(axis_pairs)} counts for {n_axes} axes")
         pairs = (ctypes.c_int32 * n_axes)(*axis_pairs)
-    check(lora_kv_append(kv.ref, _ptr(q), q_stride, k.data_ptr(), kv.rows(k, kv.n_kv_heads, "k"),
-                         v.data_ptr(), kv.rows(v, kv.n_kv_heads, "v"), n_q, _ptr(cos_sin), n_pos, rot,
-                         _ptr(pos), n_axes, pairs, 1 if interleaved else 0, _ptr(q_out), q_out_stride,
-                         ws.data_ptr(), ws.numel(), _stream(stream)), "lora_kv_append")
+    hk = kv.n_kv_heads
+    check(load().lora_kv_append(kv.ref, _ptr(q), q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(),
+                                kv.rows(v, hk, "v"), n_q, _ptr(cos_sin), n_pos, rot, _ptr(pos), n_axes, pairs,
+                                1 if interleaved else 0, _ptr(q_out), q_out_stride, ws.data_ptr(),
+                                ws.numel(), kv.stream(stream)), "lora_kv_append")
     return q_out
 
 
 def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
     """Causal attention of q [T, n_q_heads, D] over kv's cache (lora_attn_paged); scale
     defaults to D^-0.5, window 0 is none."""
-    import torch
-    q_stride = kv.rows(q)
     n_q = q.shape[1]
+    q_stride = kv.rows(q, n_q, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    check(lora_attn_paged(kv.ref, q.data_ptr(), q_stride, n_q,
-                          kv.head_dim ** -0.5 if scale is None else scale, window, n_sink, out.data_ptr(),
-                          kv.rows(out, n_q, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
+        out = q.new_empty(q.shape)
+        out_stride = n_q * kv.head_dim
+    else:
+        out_stride = kv.rows(out, n_q, "out")
+    check(load().lora_attn_paged(kv.ref, q.data_ptr(), q_stride, n_q,
+                                 kv.head_dim ** -0.5 if scale is None else scale, window, n_sink,
+                                 out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(), kv.stream(stream)),
           "lora_attn_paged")
     return out
 
@@ -730,19 +738,22 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
 def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
     """attn_paged_t for groups of sequences that share a prefix (lora_attn_prefix):
     group_off [n_groups + 1], prefix_len [n_groups] int32 on the device."""
-    import torch
-    q_stride = kv.rows(q)
     n_q = q.shape[1]
+    q_stride = kv.rows(q, n_q, "q")
     n_groups = prefix_len.numel()
-    if group_off.dtype is not torch.int32 or prefix_len.dtype is not torch.int32 or \
-            group_off.numel() != n_groups + 1 or not group_off.is_contiguous() or \
-            not prefix_len.is_contiguous():
-        raise TypeError("group_off [n_groups + 1], prefix_len [n_groups]: contiguous int32")
+    for name, t, n in (("group_off", group_off, n_groups + 1), ("prefix_len", prefix_len, n_groups)):
+        if t.element_size() != 4 or t.is_floating_point() or t.numel() != n or not t.is_contiguous() or \
+                t.get_device() != kv._device:
+            raise TypeError(f"{name}: contiguous int32 [{n}] on the cache's device")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    check(lora_attn_prefix(kv.ref, group_off.data_ptr(), prefix_len.data_ptr(), n_groups, q.data_ptr(),
-                           q_stride, n_q, kv.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
-                           kv.rows(out, n_q, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
+        out = q.new_empty(q.shape)
+        out_stride = n_q * kv.head_dim
+    else:
+        out_stride = kv.rows(out, n_q, "out")
+    check(load().lora_attn_prefix(kv.ref, group_off.data_ptr(), prefix_len.data_ptr(), n_groups,
+                                  q.data_ptr(), q_stride, n_q,
+                                  kv.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                                  out_stride, ws.data_ptr(), ws.numel(), kv.stream(stream)),
           "lora_attn_prefix")
     return out
 
