@@ -12,8 +12,9 @@
 // CTA, whatever the lengths are (they live on the device).  An item that
 // several CTAs share is finished by the last of them to arrive, which adds
 // their parts in CTA order: the result is a function of the lengths alone.
-// Each CTA computes the shares itself, from prefix sums over kCoarse coarse
-// entries in shared memory.
+// Each CTA's producer warp finds its share itself, a problem to a lane: no
+// launch, no barrier and no memory stand between the lengths and the first
+// load.
 #pragma once
 
 #include "attn.h"
@@ -196,113 +197,6 @@ __device__ __forceinline__ int key_tile(const RowTile& t, int i) {
   return i < t.sink_tiles ? i : t.tile_lo + i - t.sink_tiles;
 }
 
-// Units of one key head over all row tiles of a problem: a warp's lanes take a
-// row tile each.
-__device__ __forceinline__ int64_t problem_units(const AttnParams& P, const Problem& pr) {
-  const int n = (pr.n_rows + P.rows - 1) / P.rows;
-  int64_t sum = 0;
-  for (int rt = threadIdx.x & 31; rt < n; rt += 32) sum += row_tile(P, pr, rt).n_tiles + P.over;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
-}
-
-// The prefix sums in shared memory.  C is a multiple of 32.
-template <int C>
-struct Schedule {
-  int64_t units[C + 1];   // units of a key head before coarse entry e of problems
-  int tiles[C + 1];       // row tiles before it
-  int n_prob, per_prob;   // problems, problems of a coarse entry
-  int total, share;       // units of the call, units of a CTA
-};
-
-// Exclusive prefix sums of v[0 .. C) in place by one warp, the sum in v[C].
-template <int C, typename T>
-__device__ __forceinline__ void warp_scan_coarse(T* v) {
-  constexpr int kPer = C / 32;
-  const int lane = threadIdx.x & 31;
-  T x[kPer], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    x[i] = v[lane * kPer + i];
-    sum += x[i];
-  }
-  T incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  T run = incl - sum;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    v[lane * kPer + i] = run;
-    run += x[i];
-  }
-  if (lane == 31) v[C] = run;
-}
-
-// All threads of the CTA; ends with a barrier.
-template <int C>
-__device__ __forceinline__ void build_schedule(const AttnParams& P, Schedule<C>& S) {
-  const int n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
-  const int per_prob = (n_prob + C - 1) / C;
-  for (int e = threadIdx.x; e < C; e += blockDim.x) {
-    S.units[e] = 0;
-    S.tiles[e] = 0;
-  }
-  __syncthreads();
-  // a lane takes a problem; those of many row tiles are added up by the warp
-  const int lane = threadIdx.x & 31;
-  for (int p0 = threadIdx.x & ~31; p0 < n_prob; p0 += blockDim.x) {
-    const int p = p0 + lane;
-    Problem pr = {};
-    if (p < n_prob) pr = load_problem(P, p);
-    const int n = (pr.n_rows + P.rows - 1) / P.rows;
-    int64_t units = 0;
-    if (n == 1) units = row_tile(P, pr, 0).n_tiles + P.over;
-    for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many != 0; many &= many - 1) {
-      const int src = __ffs(many) - 1;
-      Problem x;
-      x.n_rows = __shfl_sync(0xffffffffu, pr.n_rows, src);
-      x.base = __shfl_sync(0xffffffffu, pr.base, src);
-      x.k_lo = __shfl_sync(0xffffffffu, pr.k_lo, src);
-      x.k_hi = __shfl_sync(0xffffffffu, pr.k_hi, src);
-      const int64_t all = problem_units(P, x);
-      if (lane == src) units = all;
-    }
-    if (n > 0) {
-      const int e = per_prob == 1 ? p : p / per_prob;
-      atomicAdd(reinterpret_cast<unsigned long long*>(&S.units[e]),
-                static_cast<unsigned long long>(units));
-      atomicAdd(&S.tiles[e], n);
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    warp_scan_coarse<C>(S.units);
-    warp_scan_coarse<C>(S.tiles);
-    if (threadIdx.x == 31) {
-      // More row tiles than T allows (lengths out of order), or more units than
-      // a call could ever work off (2^31 of them read 10^14 bytes): refused.
-      const int64_t total = S.units[C] * P.kv.n_kv_heads;
-      const int items = S.tiles[C] * P.kv.n_kv_heads;
-      const bool ok = S.tiles[C] <= P.max_row_tiles && total <= INT32_MAX;
-      if (!ok) flag_error(P.err, LORA_DEVERR_BAD_LEN);
-      S.n_prob = n_prob;
-      S.per_prob = per_prob;
-      S.total = ok ? static_cast<int>(total) : 0;
-      // Equal shares, but an item of a few key tiles is not worth splitting,
-      // nor is less than four tiles worth a CTA.
-      const int even = (S.total + gridDim.x - 1) / gridDim.x;
-      const int span = items > 0 ? (S.total + items - 1) / items : 1;
-      const int least = span <= 8 ? span : 4;
-      S.share = even > least ? even : least;
-    }
-  }
-  __syncthreads();
-}
-
 // What a CTA does next: key tiles [tile0, tile0 + n) of an item.
 struct Segment {
   int n;             // key tiles; 0: the CTA is done
@@ -317,67 +211,153 @@ struct Segment {
   int slot;          // where this CTA's part goes, if parts > 1
 };
 
+// Units of one key head over all row tiles of a problem: a warp's lanes take a
+// row tile each.
+__device__ __forceinline__ int64_t problem_units(const AttnParams& P, const Problem& pr) {
+  const int n = (pr.n_rows + P.rows - 1) / P.rows;
+  int64_t sum = 0;
+  for (int rt = threadIdx.x & 31; rt < n; rt += 32) sum += row_tile(P, pr, rt).n_tiles + P.over;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// 32 consecutive problems, one to a lane: the lane's problem, its row tiles and
+// its units of one key head.  Problems of many row tiles (prompts) are added up
+// by the whole warp.
+struct ProblemLane {
+  Problem pr;
+  int tiles;
+  int64_t units;
+};
+__device__ __forceinline__ ProblemLane load_problems(const AttnParams& P, int p0, int n_prob) {
+  const int lane = threadIdx.x & 31;
+  ProblemLane r;
+  r.pr = {};
+  if (p0 + lane < n_prob) r.pr = load_problem(P, p0 + lane);
+  r.tiles = (r.pr.n_rows + P.rows - 1) / P.rows;
+  r.units = 0;
+  if (r.tiles == 1) r.units = row_tile(P, r.pr, 0).n_tiles + P.over;
+  for (uint32_t many = __ballot_sync(0xffffffffu, r.tiles > 1); many != 0; many &= many - 1) {
+    const int src = __ffs(many) - 1;
+    Problem x;
+    x.n_rows = __shfl_sync(0xffffffffu, r.pr.n_rows, src);
+    x.base = __shfl_sync(0xffffffffu, r.pr.base, src);
+    x.k_lo = __shfl_sync(0xffffffffu, r.pr.k_lo, src);
+    x.k_hi = __shfl_sync(0xffffffffu, r.pr.k_hi, src);
+    const int64_t all = problem_units(P, x);
+    if (lane == src) r.units = all;
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ T warp_total(T x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T up = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += up;
+  }
+  return x;
+}
+
 // Walks a CTA's share (one warp, all lanes alike).
 struct Walker {
   Problem pr;
   RowTile t;
-  int prob, rt;   // the problem, and the row tile's number in it
-  int tile;       // and over all problems
-  int u, end;     // next unit, end of the share
-  int tile_unit;  // first unit of the row tile
-  int done = 0;   // key tiles of the segments so far
+  int prob, rt;      // the problem, and the row tile's number in it
+  int tile;          // and over all problems
+  int u, end;        // next unit, end of the share
+  int total, share;  // units of the call, units of a CTA
+  int tile_unit;     // first unit of the row tile
+  int done;          // key tiles of the segments so far
+  int n_prob;
 
   __device__ __forceinline__ int units(const AttnParams& P) const {  // of the row tile
     return (t.n_tiles + P.over) * P.kv.n_kv_heads;
   }
-  template <int C>
-  __device__ __forceinline__ void start(const AttnParams& P, const Schedule<C>& S) {
-    u = min(S.total, S.share * static_cast<int>(blockIdx.x));  // (below 2^31: see build_schedule)
-    if (static_cast<int64_t>(S.share) * blockIdx.x >= S.total) u = S.total;
-    end = S.total - u < S.share ? S.total : u + S.share;
-    if (u >= end) return;
+  __device__ __forceinline__ void start(const AttnParams& P) {
     const int hk = P.kv.n_kv_heads, lane = threadIdx.x & 31;
-    int lo = 0, hi = C;  // units[lo] * hk <= u < units[hi] * hk
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (S.units[mid] * hk <= u) lo = mid; else hi = mid;
+    n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
+    done = 0;
+    // the sizes of all problems, then the equal share of a CTA
+    ProblemLane x = load_problems(P, 0, n_prob);
+    int64_t units = x.units, tiles = x.tiles;
+#pragma unroll 2
+    for (int p0 = 32; p0 < n_prob; p0 += 32) {
+      const ProblemLane y = load_problems(P, p0, n_prob);
+      units += y.units;
+      tiles += y.tiles;
     }
-    prob = lo * S.per_prob;
-    tile = S.tiles[lo];
-    tile_unit = static_cast<int>(S.units[lo]) * hk;
-    for (;;) {  // the problem in the coarse entry
-      pr = load_problem(P, prob);
-      if (S.per_prob == 1) break;
-      const int span = static_cast<int>(problem_units(P, pr)) * hk;
-      if (tile_unit + span > u || prob + 1 >= S.n_prob) break;
-      tile_unit += span;
-      tile += (pr.n_rows + P.rows - 1) / P.rows;
-      ++prob;
-    }
-    const int n = (pr.n_rows + P.rows - 1) / P.rows;
-    for (rt = 0;; rt += 32) {  // the row tile in the problem, 32 at a time
-      int own = rt + lane < n ? (row_tile(P, pr, rt + lane).n_tiles + P.over) * hk : 0, incl = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-      }
+    units = warp_total(units) * hk;
+    tiles = warp_total(tiles);
+    // More row tiles than T allows (lengths out of order), or more units than a
+    // call could ever work off (2^31 of them read 10^14 bytes): refused.
+    const bool ok = tiles <= P.max_row_tiles && units <= INT32_MAX;
+    if (!ok) flag_error(P.err, LORA_DEVERR_BAD_LEN);
+    total = ok ? static_cast<int>(units) : 0;
+    // Equal shares, but an item of a few key tiles is not worth splitting, nor
+    // is less than four tiles worth a CTA.
+    const int items = ok ? static_cast<int>(tiles) * hk : 0;
+    const int even = (total + gridDim.x - 1) / gridDim.x;
+    const int span = items > 0 ? (total + items - 1) / items : 1;
+    const int least = span <= 8 ? span : 4;
+    share = even > least ? even : least;
+    const int64_t first = static_cast<int64_t>(share) * blockIdx.x;
+    u = first < total ? static_cast<int>(first) : total;
+    end = total - u < share ? total : u + share;
+    if (u >= end) return;
+    // the problem that unit u belongs to
+    tile = tile_unit = 0;
+    for (int p0 = 0;; p0 += 32) {
+      if (p0 > 0) x = load_problems(P, p0, n_prob);
+      const int own = static_cast<int>(x.units) * hk, incl = warp_scan(own);
+      const int t_incl = warp_scan(x.tiles);
       const uint32_t past = __ballot_sync(0xffffffffu, tile_unit + incl > u);
-      const int k = past != 0 ? __ffs(past) - 1 : 31;
-      const int before = __shfl_sync(0xffffffffu, incl - own, k);
-      if (past != 0 || rt + 32 >= n) {
-        tile_unit += before;
-        rt += k;
+      if (past != 0) {
+        const int k = __ffs(past) - 1;
+        prob = p0 + k;
+        tile_unit += __shfl_sync(0xffffffffu, incl - own, k);
+        tile += __shfl_sync(0xffffffffu, t_incl - x.tiles, k);
+        pr.tok0 = __shfl_sync(0xffffffffu, x.pr.tok0, k);
+        pr.n_rows = __shfl_sync(0xffffffffu, x.pr.n_rows, k);
+        pr.base = __shfl_sync(0xffffffffu, x.pr.base, k);
+        pr.k_lo = __shfl_sync(0xffffffffu, x.pr.k_lo, k);
+        pr.k_hi = __shfl_sync(0xffffffffu, x.pr.k_hi, k);
+        pr.table_row = __shfl_sync(0xffffffffu, x.pr.table_row, k);
         break;
       }
       tile_unit += __shfl_sync(0xffffffffu, incl, 31);
+      tile += __shfl_sync(0xffffffffu, t_incl, 31);
+    }
+    // the row tile in it, 32 at a time
+    const int n = (pr.n_rows + P.rows - 1) / P.rows;
+    rt = 0;
+    if (n > 1) {
+      for (;; rt += 32) {
+        const int own = rt + lane < n ? (row_tile(P, pr, rt + lane).n_tiles + P.over) * hk : 0;
+        const int incl = warp_scan(own);
+        const uint32_t past = __ballot_sync(0xffffffffu, tile_unit + incl > u);
+        if (past != 0) {
+          const int k = __ffs(past) - 1;
+          tile_unit += __shfl_sync(0xffffffffu, incl - own, k);
+          rt += k;
+          break;
+        }
+        tile_unit += __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
     tile += rt;
     t = row_tile(P, pr, rt);
   }
   // The next row tile; there is one while u is below the total.
-  template <int C>
-  __device__ __forceinline__ void advance(const AttnParams& P, const Schedule<C>& S) {
+  __device__ __forceinline__ void advance(const AttnParams& P) {
     tile_unit += units(P);
     ++tile;
     ++rt;
@@ -386,16 +366,15 @@ struct Walker {
       do {
         ++prob;
         pr = load_problem(P, prob);
-      } while (pr.n_rows == 0 && prob + 1 < S.n_prob);
+      } while (pr.n_rows == 0 && prob + 1 < n_prob);
     }
     t = row_tile(P, pr, rt);
   }
-  template <int C>
-  __device__ __forceinline__ Segment next(const AttnParams& P, const Schedule<C>& S) {
+  __device__ __forceinline__ Segment next(const AttnParams& P) {
     Segment g;
     g.n = 0;
     if (u >= end) return g;
-    while (tile_unit + units(P) <= u) advance(P, S);
+    while (tile_unit + units(P) <= u) advance(P);
     const int span = t.n_tiles + P.over;
     g.head = (u - tile_unit) / span;
     const int a = tile_unit + g.head * span + P.over;
@@ -415,8 +394,8 @@ struct Walker {
     g.cta0 = blockIdx.x;
     g.parts = 1;
     if (g.n < t.n_tiles) {
-      g.cta0 = a / S.share;
-      g.parts = (b - 1) / S.share - g.cta0 + 1;
+      g.cta0 = a / share;
+      g.parts = (b - 1) / share - g.cta0 + 1;
     }
     g.slot = blockIdx.x == g.cta0 ? 1 : 0;
     g.tile0 = done;

@@ -130,7 +130,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.groups_phase = phase == 1;
     P.max_row_tiles = w.max_row_tiles[phase];
     P.rows = w.shape[phase].rows;
-    P.over = w.shape[phase].prefill ? 2 : 1;
+    P.over = w.shape[phase].prefill ? 4 : 1;
     cudaError_t e;
     if (w.shape[phase].prefill) {
       if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;

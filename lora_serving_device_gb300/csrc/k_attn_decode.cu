@@ -31,7 +31,6 @@
 namespace lora {
 namespace {
 
-constexpr int kCoarse = 512;  // entries of the schedule's prefix sums
 constexpr int kRing = 4;      // segments that the producer may run ahead
 
 // A rows of a row tile: 4, 8, 16 or 32.  N is their number in Q K^T and kPV
@@ -62,7 +61,6 @@ template <int D, int A>
 struct Misc {
   using La = Lay<D, A>;
   static constexpr int W = La::W, kStages = La::kStages;
-  Schedule<kCoarse> sched;
   Segment ring[kRing];
   float4 red[W][A];  // of a row: the four warps' maxima or sums
   int row_hi[W][A], row_lo[W][A];
@@ -130,22 +128,22 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
+  __syncthreads();
+  ptx::tc_fence_after();
   pdl_wait();
   pdl_launch_dependents();
-  build_schedule(P, M.sched);  // ends with a barrier
-  ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;
   const uint32_t tmem_o = tmem + W * SB * N;  // after the buffers of S
 
   if (warp == 0) {
     // ---------------- schedule and TMA ----------------------------------
     Walker walk;
-    walk.start(P, M.sched);
+    walk.start(P);
     TileLoader<D> load(P);
     int tile = 0, ends = 0;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
-      const Segment g = walk.next(P, M.sched);
+      const Segment g = walk.next(P);
       if (sg >= kRing)
         ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
       if (!ok) break;

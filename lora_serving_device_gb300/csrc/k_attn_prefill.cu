@@ -37,7 +37,6 @@ namespace {
 // within the launch's 168 x 384.
 constexpr int kThreads = 384;
 constexpr int kRegsMost = 208, kRegsLeast = 88;
-constexpr int kCoarse = 96;  // entries of the schedule's prefix sums
 constexpr int kRing = 4;     // segments that the producer may run ahead
 constexpr int kHalf = 128;   // rows of a half in the MMA
 
@@ -51,7 +50,6 @@ struct Lay {
 
 template <int kSlots>
 struct Misc {
-  Schedule<kCoarse> sched;
   Segment ring[kRing];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full[2], q_empty[2];
@@ -146,10 +144,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
+  __syncthreads();
+  ptx::tc_fence_after();
   pdl_wait();
   pdl_launch_dependents();
-  build_schedule(P, M.sched);  // ends with a barrier
-  ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;  // S (and P) of half h at h * 128, O at 256 + h * 128
 
   // (each role's branch begins with its own split, so that the compiler knows
@@ -159,14 +157,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ---------------- schedule and TMA ----------------------------------
     Walker walk;
-    walk.start(P, M.sched);
+    walk.start(P);
     TileLoader<D> load(P);
     int n = 0;              // tiles brought in: K in slot 2n, V in slot 2n + 1
     int q_use[2] = {0, 0};  // segments of each half
     bool ok = true;
     SplitItem mine = {};
     for (int sg = 0; ok; ++sg) {
-      const Segment g = walk.next(P, M.sched);
+      const Segment g = walk.next(P);
       if (sg >= kRing)
         ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
       if (!ok) break;
@@ -457,69 +455,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_f) flag_error(P.err, LORA_DEVERR_TIMEOUT);
 }
 
-// Joins the parts of the items that several CTAs shared: block (c, x) takes 32
-// rows of the item that begins in CTA c and ends in another, if there is one.
-// A lane is a row; the parts' factors come first, then each warp adds up four
-// values a row at a time, so that all reads are whole lines, and the rows are
-// written from shared memory.
+// Joins the parts of the items that several CTAs shared: block (c, y, z) takes 32
+// rows (y) and half the columns (z) of the item that begins in CTA c and ends
+// in another, if there is one.  A lane is a row; the parts' factors come first,
+// then each warp adds up its columns, so that all reads are whole lines, and
+// the rows are written from shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
+  constexpr int kCols = D / 2, kPer = kCols / 4 / 8;  // vectors of a warp
   __shared__ float fac[kDecodeScheduleCtas][32];
-  __shared__ float4 rows[32][D / 4 + 1];
+  __shared__ float4 rows[32][kCols / 4 + 1];
   __shared__ float top_s[32], sum_s[32];
   pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const SplitItem it = P.split[c];
   const int half_rows = P.rows / 2;
-  const int h = blockIdx.y / 4, row = blockIdx.y % 4 * 32 + lane;  // half, row of the half
-  const int in_tile = h * half_rows + row;
-  if (it.parts <= 1 || blockIdx.y % 4 * 32 >= half_rows ||
-      h * half_rows + blockIdx.y % 4 * 32 >= it.n_rows)
-    return;
-  const bool used = row < half_rows && in_tile < it.n_rows;
+  const int h = blockIdx.y / 4, row0 = blockIdx.y % 4 * 32, row = row0 + lane;  // in the half
+  if (it.parts <= 1 || row0 >= half_rows || h * half_rows + row0 >= it.n_rows) return;
+  const bool used = row < half_rows && h * half_rows + row < it.n_rows;
   auto slot = [&](int q) { return static_cast<int64_t>(c + q) * 2 + (q == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(P.part_ml) + h * kHalf + row;
-  // warp w looks at parts w, w + 8, ...; the maximum over all by shared memory
-  for (int q = warp; q < it.parts; q += 8) fac[q][lane] = used ? ml[slot(q) * 2 * kHalf].x : 0.f;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+  for (int q = 0; q < it.parts; ++q) top = fmaxf(top, used ? ml[slot(q) * 2 * kHalf].x : 0.f);
+  for (int q = warp; q < it.parts; q += 8)
+    fac[q][lane] =
+        !used || top == -INFINITY ? 0.f : exp2f(ml[slot(q) * 2 * kHalf].x - top);
   __syncthreads();
   if (warp == 0) {
-    float top = -INFINITY, sum = 0.f;
-    for (int q = 0; q < it.parts; ++q) top = fmaxf(top, fac[q][lane]);
-    for (int q = 0; q < it.parts; ++q) {
-      const float f = top == -INFINITY ? 0.f : exp2f(fac[q][lane] - top);
-      fac[q][lane] = f;
-      sum += used ? f * ml[slot(q) * 2 * kHalf].y : 0.f;
-    }
+#pragma unroll 8
+    for (int q = 0; q < it.parts; ++q) sum += used ? fac[q][lane] * ml[slot(q) * 2 * kHalf].y : 0.f;
     top_s[lane] = top;
     sum_s[lane] = sum;
   }
-  __syncthreads();
-  for (int k = warp; k < D / 4; k += 8) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int q = 0; q < it.parts; ++q) {
-      const float f = fac[q][lane];
-      const float4 v = part_row<D>(P, slot(q), h, row)[k * kHalf];
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
+  const int k0 = blockIdx.z * (kCols / 4) + warp * kPer;
+  float4 o[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int q = 0; q < it.parts; ++q) {
+    const float f = fac[q][lane];
+    const float4* from = part_row<D>(P, slot(q), h, row) + k0 * kHalf;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const float4 v = from[x * kHalf];
+      o[x].x += f * v.x;
+      o[x].y += f * v.y;
+      o[x].z += f * v.z;
+      o[x].w += f * v.w;
     }
-    rows[lane][k] = o;
   }
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) rows[lane][warp * kPer + x] = o[x];
   __syncthreads();
-  for (int x = threadIdx.x; x < 32 * (D / 8); x += 256) {
-    const int r = x / (D / 8), k = x % (D / 8);
-    const int at = blockIdx.y % 4 * 32 + r;
-    if (at >= half_rows || h * half_rows + at >= it.n_rows) continue;
-    const int in_prob = it.row0 + h * half_rows + at, tok = in_prob / P.group;
+  for (int x = threadIdx.x; x < 32 * (kCols / 8); x += 256) {
+    const int r = x / (kCols / 8), k = x % (kCols / 8);
+    if (row0 + r >= half_rows || h * half_rows + row0 + r >= it.n_rows) continue;
+    const int in_prob = it.row0 + h * half_rows + row0 + r, tok = in_prob / P.group;
     const RowWriter<D> out(P, it.shared, it.tok0 + tok, it.head * P.group + in_prob - tok * P.group,
                            true, top_s[r], sum_s[r]);
     float v[8];
     *reinterpret_cast<float4*>(v) = rows[r][2 * k];
     *reinterpret_cast<float4*>(v + 4) = rows[r][2 * k + 1];
-    out.write8(8 * k, v);
+    out.write8(blockIdx.z * kCols + 8 * k, v);
   }
 }
 
@@ -545,7 +544,7 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(kDecodeScheduleCtas, 8);
+  cfg.gridDim = dim3(kDecodeScheduleCtas, 8, 2);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, P);

@@ -642,7 +642,7 @@ class PagedKV:
                                     block_table.shape[1], T, T if max_q_len is None else max_q_len)
         self.ref = ctypes.addressof(self.struct)
         self._device = k_cache.get_device()
-        self._bf16 = torch.bfloat16
+        self._bf16, self._empty, self._torch_device = torch.bfloat16, torch.empty, k_cache.device
         self._current_stream = torch._C._cuda_getCurrentRawStream
 
     def rows(self, x, n_heads, what):
@@ -656,6 +656,9 @@ class PagedKV:
             raise ValueError(f"{what}: shape {tuple(x.shape)}, strides {st} on {x.device}; need [{T}, {heads}, "
                              f"{d}] with the heads of a token contiguous, on the cache's device")
         return st[0] if T > 1 else heads * d
+
+    def empty_like(self, x):
+        return self._empty(x.shape, dtype=self._bf16, device=self._torch_device)
 
     def stream(self, stream):
         return self._current_stream(self._device) if stream is None else stream.cuda_stream
@@ -690,7 +693,7 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
         n_q = q.shape[1]
         q_stride = kv.rows(q, n_q, "q")
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = kv.empty_like(q)
             q_out_stride = n_q * kv.head_dim
         else:
             q_out_stride = kv.rows(q_out, n_q, "q_out")
@@ -724,7 +727,7 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
     n_q = q.shape[1]
     q_stride = kv.rows(q, n_q, "q")
     if out is None:
-        out = q.new_empty(q.shape)
+        out = kv.empty_like(q)
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")
@@ -746,7 +749,7 @@ def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream
                 t.get_device() != kv._device:
             raise TypeError(f"{name}: contiguous int32 [{n}] on the cache's device")
     if out is None:
-        out = q.new_empty(q.shape)
+        out = kv.empty_like(q)
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")

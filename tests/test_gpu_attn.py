@@ -233,6 +233,49 @@ def test_long_context_of_few_rows(L):
         assert (got - ref).norm() <= 5e-3 * ref.norm()
 
 
+@pytest.mark.parametrize("hq,hkv,d,window", [(64, 8, 64, 1024), (32, 8, 128, 0), (12, 12, 64, 0), (32, 2, 128, 300),
+                                             (24, 1, 64, 0)])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_ordinary_batches(L, hq, hkv, d, window, rows):
+    """Shares of many segments and tiles, on every SM: 60 sequences of 1 or up to 70 new rows,
+    against fp64 on the GPU."""
+    import torch
+    rng = np.random.default_rng(hq + window + rows)
+    n, page, n_sink = 60, 32, 4
+    ctx = rng.integers(0, 4000, n)
+    q_lens = rng.integers(1, rows + 1, n)
+    kv_len = ctx + q_lens
+    max_pages = -(-int(kv_len.max()) // page)
+    table = torch.randperm(n * max_pages, device="cuda").to(torch.int32).view(n, max_pages)
+    torch.manual_seed(hq)
+    kc, vc = (torch.randn(n * max_pages, hkv, page, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    off = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    T = int(off[-1])
+    q = torch.randn(T, hq, d, device="cuda").to(torch.bfloat16)
+    kv = L.PagedKV(kc, vc, table, torch.from_numpy(off).cuda(), torch.from_numpy(kv_len.astype(np.int32)).cuda(), T,
+                   max_q_len=int(q_lens.max()))
+    ws = L.attn_workspace(kv, hq)
+    got = L.attn_paged_t(kv, q, ws, window=window, n_sink=n_sink)
+    assert L.get_error_t(ws) == 0
+    for s in range(n):
+        m = int(kv_len[s])
+        k, v = (c[table[s].long()].transpose(1, 2).reshape(-1, hkv, d)[:m].double().repeat_interleave(hq // hkv, 1)
+                for c in (kc, vc))
+        a, b = int(off[s]), int(off[s + 1])
+        x = torch.einsum("thd,nhd->htn", q[a:b].double(), k) * d ** -0.5
+        pos = torch.arange(m - (b - a), m, device="cuda")[:, None]
+        key = torch.arange(m, device="cuda")
+        seen = key <= pos
+        if window:
+            seen &= (key > pos - window) | (key < n_sink)
+        w = x.masked_fill(~seen, -float("inf")).softmax(-1)
+        ref, wv = (torch.einsum("htn,nhd->thd", w, y) for y in (v, v.abs()))
+        err = (got[a:b].double() - ref).abs()
+        assert (err <= U * ref.abs() + (U + 2.0 ** -12) * wv).all(), s
+        assert err.norm() <= 5e-3 * ref.norm()
+    assert torch.equal(got, L.attn_paged_t(kv, q, ws, window=window, n_sink=n_sink))
+
+
 def test_cache_past_32_bit_offsets(L):
     """A cache of more than 2^32 elements, used at its end."""
     import torch
