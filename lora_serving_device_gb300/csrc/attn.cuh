@@ -12,9 +12,8 @@
 // CTA, whatever the lengths are (they live on the device).  An item that
 // several CTAs share is finished by the last of them to arrive, which adds
 // their parts in CTA order: the result is a function of the lengths alone.
-// Each CTA's producer warp finds its share itself, a problem to a lane: no
-// launch, no barrier and no memory stand between the lengths and the first
-// load.
+// Each CTA finds its share itself: its threads size a problem each, and one
+// warp adds the sizes up and looks for its place.
 #pragma once
 
 #include "attn.h"
@@ -44,6 +43,22 @@ __device__ __forceinline__ int seq_of_row(const int32_t* q_off, int n_seqs, int 
 
 constexpr int kKeys = 128;     // keys of a tile
 
+// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and mul =
+// floor(2^(31+s) / d) + 1 the product exceeds n 2^(31+s) / d by less than
+// 2^(31+s) / d.
+struct FastDiv {
+  uint32_t mul;
+  int shift;
+  static FastDiv of(int d) {
+    int s = 0;
+    while ((int64_t{1} << s) < d) ++s;
+    return {static_cast<uint32_t>((uint64_t{1} << (31 + s)) / d + 1), 31 + s};
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul >> shift);
+  }
+};
+
 // An item that several CTAs share, from the one it begins in.
 struct SplitItem {
   int parts;          // 0: there is none
@@ -62,6 +77,7 @@ struct AttnParams {
   bool groups_phase;   // problems are the prefix groups (else the sequences)
   int group;           // query heads of a key head
   int rows;            // rows of a row tile
+  FastDiv by_group, by_rows;
   int lg_page;         // log2 of the page size
   int over;            // units that an item costs beside its key tiles
   int n_q_heads;
@@ -100,7 +116,14 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
 
 // The group of sequence s (0 .. n_groups - 1), or -1.
 __device__ __forceinline__ int group_of_seq(const AttnParams& P, int s) {
-  int lo = 0, hi = P.n_groups;  // group_off[lo] <= s < group_off[hi], if in any
+  const int n = P.n_groups;
+  if (n <= 16) {  // loads that do not wait for one another
+    int g = -1;
+#pragma unroll 4
+    for (int i = 0; i <= n; ++i) g += P.group_off[i] <= s ? 1 : 0;
+    return g < n ? g : -1;
+  }
+  int lo = 0, hi = n;  // group_off[lo] <= s < group_off[hi], if in any
   if (s >= P.group_off[hi]) return -1;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -181,8 +204,8 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams& P, const Problem& 
     t.n_tiles = (pr.k_hi + kKeys - 1) / kKeys;
     return t;
   }
-  const int first = pr.base + t.row0 / P.group;
-  t.vis_hi = min(pr.base + (t.row0 + t.n_rows - 1) / P.group, pr.k_hi - 1);
+  const int first = pr.base + P.by_group(t.row0);
+  t.vis_hi = min(pr.base + P.by_group(t.row0 + t.n_rows - 1), pr.k_hi - 1);
   t.vis_lo = P.window > 0 ? max(first - P.window + 1, 0) : 0;
   t.vis_lo = max(t.vis_lo, pr.k_lo);
   t.n_sink = P.window > 0 ? max(min(P.n_sink, t.vis_hi + 1), 0) : 0;
@@ -208,13 +231,14 @@ struct Segment {
   int item;          // its counter
   int cta0, parts;   // the CTAs that share the item: cta0 .. cta0 + parts - 1
   int tile0;         // key tiles of this CTA before the segment
+  int once;          // no other CTA reads these key tiles
   int slot;          // where this CTA's part goes, if parts > 1
 };
 
 // Units of one key head over all row tiles of a problem: a warp's lanes take a
 // row tile each.
 __device__ __forceinline__ int64_t problem_units(const AttnParams& P, const Problem& pr) {
-  const int n = (pr.n_rows + P.rows - 1) / P.rows;
+  const int n = P.by_rows(pr.n_rows + P.rows - 1);
   int64_t sum = 0;
   for (int rt = threadIdx.x & 31; rt < n; rt += 32) sum += row_tile(P, pr, rt).n_tiles + P.over;
 #pragma unroll
@@ -222,31 +246,46 @@ __device__ __forceinline__ int64_t problem_units(const AttnParams& P, const Prob
   return sum;
 }
 
-// 32 consecutive problems, one to a lane: the lane's problem, its row tiles and
-// its units of one key head.  Problems of many row tiles (prompts) are added up
-// by the whole warp.
-struct ProblemLane {
-  Problem pr;
+// Sizes of the first kSized problems: row tiles and units of one key head (-1
+// units: not added up yet, many row tiles).  All threads of the CTA compute
+// them, into shared memory that the first tiles will overwrite.
+constexpr int kSized = 2048;
+struct ProblemSize {
+  int tiles, units;
+};
+__device__ __forceinline__ ProblemSize problem_size(const AttnParams& P, const Problem& pr) {
+  ProblemSize z;
+  z.tiles = P.by_rows(pr.n_rows + P.rows - 1);
+  z.units = z.tiles > 4 ? -1 : 0;
+  if (z.tiles <= 4)
+    for (int rt = 0; rt < z.tiles; ++rt) z.units += row_tile(P, pr, rt).n_tiles + P.over;
+  return z;
+}
+// All threads; the caller follows it with a barrier.
+__device__ __forceinline__ void size_problems(const AttnParams& P, ProblemSize* sizes) {
+  const int n = min(P.groups_phase ? P.n_groups : P.kv.n_seqs, kSized);
+  for (int p = threadIdx.x; p < n; p += blockDim.x) sizes[p] = problem_size(P, load_problem(P, p));
+}
+
+// 32 consecutive problems, one to a lane.  Those of many row tiles (prompts)
+// are added up by the whole warp.
+struct LaneSize {
   int tiles;
   int64_t units;
 };
-__device__ __forceinline__ ProblemLane load_problems(const AttnParams& P, int p0, int n_prob) {
-  const int lane = threadIdx.x & 31;
-  ProblemLane r;
-  r.pr = {};
-  if (p0 + lane < n_prob) r.pr = load_problem(P, p0 + lane);
-  r.tiles = (r.pr.n_rows + P.rows - 1) / P.rows;
-  r.units = 0;
-  if (r.tiles == 1) r.units = row_tile(P, r.pr, 0).n_tiles + P.over;
-  for (uint32_t many = __ballot_sync(0xffffffffu, r.tiles > 1); many != 0; many &= many - 1) {
+__device__ __forceinline__ LaneSize lane_sizes(const AttnParams& P, ProblemSize* sizes, int p0,
+                                               int n_prob) {
+  const int lane = threadIdx.x & 31, p = p0 + lane;
+  ProblemSize z = {0, 0};
+  if (p < n_prob) z = p0 < kSized ? sizes[p] : problem_size(P, load_problem(P, p));
+  LaneSize r = {z.tiles, z.units};
+  for (uint32_t many = __ballot_sync(0xffffffffu, z.units < 0); many != 0; many &= many - 1) {
     const int src = __ffs(many) - 1;
-    Problem x;
-    x.n_rows = __shfl_sync(0xffffffffu, r.pr.n_rows, src);
-    x.base = __shfl_sync(0xffffffffu, r.pr.base, src);
-    x.k_lo = __shfl_sync(0xffffffffu, r.pr.k_lo, src);
-    x.k_hi = __shfl_sync(0xffffffffu, r.pr.k_hi, src);
-    const int64_t all = problem_units(P, x);
-    if (lane == src) r.units = all;
+    const int64_t all = problem_units(P, load_problem(P, p0 + src));
+    if (lane == src) {
+      r.units = all;
+      if (p0 < kSized && all <= INT32_MAX) sizes[p].units = static_cast<int>(all);
+    }
   }
   return r;
 }
@@ -282,19 +321,19 @@ struct Walker {
   __device__ __forceinline__ int units(const AttnParams& P) const {  // of the row tile
     return (t.n_tiles + P.over) * P.kv.n_kv_heads;
   }
-  __device__ __forceinline__ void start(const AttnParams& P) {
+  // `sizes`: see size_problems; not used after this.
+  __device__ __forceinline__ void start(const AttnParams& P, ProblemSize* sizes) {
     const int hk = P.kv.n_kv_heads, lane = threadIdx.x & 31;
     n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
     done = 0;
     // the sizes of all problems, then the equal share of a CTA
-    ProblemLane x = load_problems(P, 0, n_prob);
-    int64_t units = x.units, tiles = x.tiles;
-#pragma unroll 2
-    for (int p0 = 32; p0 < n_prob; p0 += 32) {
-      const ProblemLane y = load_problems(P, p0, n_prob);
-      units += y.units;
-      tiles += y.tiles;
+    int64_t units = 0, tiles = 0;
+    for (int p0 = 0; p0 < n_prob; p0 += 32) {
+      const LaneSize x = lane_sizes(P, sizes, p0, n_prob);
+      units += x.units;
+      tiles += x.tiles;
     }
+    __syncwarp();
     units = warp_total(units) * hk;
     tiles = warp_total(tiles);
     // More row tiles than T allows (lengths out of order), or more units than a
@@ -316,7 +355,7 @@ struct Walker {
     // the problem that unit u belongs to
     tile = tile_unit = 0;
     for (int p0 = 0;; p0 += 32) {
-      if (p0 > 0) x = load_problems(P, p0, n_prob);
+      const LaneSize x = lane_sizes(P, sizes, p0, n_prob);
       const int own = static_cast<int>(x.units) * hk, incl = warp_scan(own);
       const int t_incl = warp_scan(x.tiles);
       const uint32_t past = __ballot_sync(0xffffffffu, tile_unit + incl > u);
@@ -325,19 +364,14 @@ struct Walker {
         prob = p0 + k;
         tile_unit += __shfl_sync(0xffffffffu, incl - own, k);
         tile += __shfl_sync(0xffffffffu, t_incl - x.tiles, k);
-        pr.tok0 = __shfl_sync(0xffffffffu, x.pr.tok0, k);
-        pr.n_rows = __shfl_sync(0xffffffffu, x.pr.n_rows, k);
-        pr.base = __shfl_sync(0xffffffffu, x.pr.base, k);
-        pr.k_lo = __shfl_sync(0xffffffffu, x.pr.k_lo, k);
-        pr.k_hi = __shfl_sync(0xffffffffu, x.pr.k_hi, k);
-        pr.table_row = __shfl_sync(0xffffffffu, x.pr.table_row, k);
         break;
       }
       tile_unit += __shfl_sync(0xffffffffu, incl, 31);
       tile += __shfl_sync(0xffffffffu, t_incl, 31);
     }
+    pr = load_problem(P, prob);
     // the row tile in it, 32 at a time
-    const int n = (pr.n_rows + P.rows - 1) / P.rows;
+    const int n = P.by_rows(pr.n_rows + P.rows - 1);
     rt = 0;
     if (n > 1) {
       for (;; rt += 32) {
@@ -399,6 +433,7 @@ struct Walker {
     }
     g.slot = blockIdx.x == g.cta0 ? 1 : 0;
     g.tile0 = done;
+    g.once = pr.n_rows <= P.rows ? 1 : 0;
     done += g.n;
     u += g.n;
     return g;

@@ -134,16 +134,25 @@ __device__ __forceinline__ void zero_unseen_value(const RowTile& t, int key0, in
       *reinterpret_cast<uint4*>(row + h * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// L2 policies: what one CTA alone reads leaves first, so that a step's block
+// tables, lengths and instructions stay.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+  uint64_t p;
+  if (once)
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // 4-D tiled load (c0 innermost), completion counted in bytes on `bar`.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, uint64_t* bar,
-                                            int c3) {
+                                            int c3, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %3, %3, %4}], [%2];" ::"r"(ptx::smem_u32(dst)),
-      "l"(tm), "r"(ptx::smem_u32(bar)), "r"(0), "r"(c3)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %3, %3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
+      "l"(tm), "r"(ptx::smem_u32(bar)), "r"(0), "r"(c3), "l"(policy)
       : "memory");
 }
-
 // c1 is the head, c2 the token, c3 the 64-value half of the head.
 __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, uint64_t* bar,
                                               int c1, int c2, int c3) {
@@ -162,6 +171,7 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, 
 template <int D>
 struct TileLoader {
   int page, lg_page, box, boxes, per;
+  uint64_t policy;
   int now, next;  // where this lane's box starts in the cache, in groups of eight
                   // rows, for two batches of `per` tiles; -1: not needed
   __device__ __forceinline__ explicit TileLoader(const AttnParams& P)
@@ -184,6 +194,7 @@ struct TileLoader {
     return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (key0 & (page - 1)) / 8;
   }
   __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
+    policy = l2_policy(g.once != 0);
     now = lookup(P, g, 0);
     next = g.n > per ? lookup(P, g, per) : -1;
   }
@@ -207,35 +218,14 @@ struct TileLoader {
     const int lane = threadIdx.x & 31;
     if (lane == 0) ptx::mbar_arrive_expect_tx(full, all);
     __syncwarp();
-    if (at >= 0) tma_load_4d(dst + lane * box_bytes(), tm, full, at);
+    if (at >= 0) tma_load_4d(dst + lane * box_bytes(), tm, full, at, policy);
   }
 };
 
-// Value d of a finished row (token t, query head h): o / sum.  The prefix phase
-// keeps it in fp32 with its log-sum-exp (log2 units, m + log2 sum); otherwise
-// it is joined with that part, if there is one, and rounded to out.
-template <int D>
-__device__ __forceinline__ void write_row(const AttnParams& P, const Segment& g, int64_t t, int h,
-                                          int d, float o, float sum, float m) {
-  float x = sum > 0.f ? o / sum : 0.f;
-  if (P.groups_phase || g.shared) {
-    const float lse = sum > 0.f ? m + log2f(sum) : -INFINITY;
-    const int64_t at = t * P.n_q_heads + h;
-    if (P.groups_phase) {
-      P.prior[at * D + d] = x;
-      if (d == 0) P.prior_lse[at] = lse;
-      return;
-    }
-    const float other = P.prior_lse[at], top = fmaxf(lse, other);
-    if (top > -INFINITY) {
-      const float a = exp2f(lse - top), b = exp2f(other - top);
-      x = (a * x + b * P.prior[at * D + d]) / (a + b);
-    }
-  }
-  P.out[t * P.out_stride + h * D + d] = __float2bfloat16_rn(x);
-}
-
-// The same for a thread that holds a whole row, eight values at a time.
+// Writes a finished row (token t, query head h; sums of exponentials `sum` at the
+// maximum m, log2 units), eight values at a time: x / sum.  The prefix phase
+// keeps it in fp32 with its log-sum-exp; otherwise it is joined with that part,
+// if there is one, and rounded to out.
 template <int D>
 struct RowWriter {
   float own, other;  // factors of this result and of the prior part

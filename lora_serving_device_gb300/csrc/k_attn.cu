@@ -114,6 +114,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.prefix_len = a.prefix_len;
   P.n_groups = a.n_groups;
   P.group = a.n_q_heads / kv.n_kv_heads;
+  P.by_group = FastDiv::of(P.group);
   P.n_q_heads = a.n_q_heads;
   P.lg_page = 31 - __builtin_clz(static_cast<unsigned>(kv.page_size));
   P.scale_log2 = a.scale * 1.4426950408889634f;
@@ -130,6 +131,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.groups_phase = phase == 1;
     P.max_row_tiles = w.max_row_tiles[phase];
     P.rows = w.shape[phase].rows;
+    P.by_rows = FastDiv::of(P.rows);
     P.over = w.shape[phase].prefill ? 4 : 1;
     cudaError_t e;
     if (w.shape[phase].prefill) {

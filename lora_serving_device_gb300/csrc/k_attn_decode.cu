@@ -63,6 +63,7 @@ struct Misc {
   static constexpr int W = La::W, kStages = La::kStages;
   Segment ring[kRing];
   float4 red[W][A];  // of a row: the four warps' maxima or sums
+  float m[W][A];
   int row_hi[W][A], row_lo[W][A];
   uint64_t full_k[kStages], full_v[kStages], empty[kStages];
   uint64_t s_full[W][La::kSBufs], s_empty[W][La::kSBufs];
@@ -128,17 +129,22 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
-  __syncthreads();
-  ptx::tc_fence_after();
   pdl_wait();
   pdl_launch_dependents();
+  // the tiles' memory holds the problems' sizes until the first load
+  size_problems(P, reinterpret_cast<ProblemSize*>(smem));
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+  ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;
   const uint32_t tmem_o = tmem + W * SB * N;  // after the buffers of S
 
   if (warp == 0) {
     // ---------------- schedule and TMA ----------------------------------
     Walker walk;
-    walk.start(P);
+    walk.start(P, reinterpret_cast<ProblemSize*>(smem));
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
     TileLoader<D> load(P);
     int tile = 0, ends = 0;
     bool ok = true;
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         const int n = i / (D / 8), ch = i % (D / 8);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (n < g.t.n_rows) {
-          const int r = g.t.row0 + n, tok = r / P.group;
+          const int r = g.t.row0 + n, tok = P.by_group(r);
           v = *reinterpret_cast<const uint4*>(
               P.q + (g.tok0 + tok) * P.q_stride +
               (g.head * P.group + r - tok * P.group) * D + ch * 8);
@@ -302,15 +308,23 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     // wait that gave up they run on (every later wait returns at once) to
     // the vote at the next segment.
     uint32_t tile = 0;  // tiles of this warpgroup so far
-    for (int sg = wg;; sg += W) {
-      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
-      if (named_any(kBar, 128, *abort_f != 0)) break;
-      const Segment g = M.ring[sg % kRing];
-      if (g.n == 0) break;
-      load_q(g);  // (the MMAs that read the last one's are done: so are its scores)
+    // A first segment with nothing in it: its one tile, without waits and
+    // effects, brings the loop's instructions in while the first real segment
+    // is looked for.
+    for (int sg = P.kv.T < 0 ? wg : wg - W;; sg += W) {
+      const bool dry = sg < 0;
+      Segment g = {};
+      g.n = g.parts = 1;
+      if (!dry) {
+        wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+        if (named_any(kBar, 128, *abort_f != 0)) break;
+        g = M.ring[sg % kRing];
+        if (g.n == 0) break;
+        load_q(g);  // (the MMAs that read the last one's are done: so are its scores)
+      }
       // limits of the rows (rows past the last copy row 0's)
       for (int n = st_tid; n < A; n += 128) {
-        const int pos = g.base + (g.t.row0 + (n < g.t.n_rows ? n : 0)) / P.group;
+        const int pos = g.base + P.by_group(g.t.row0 + (n < g.t.n_rows ? n : 0));
         M.row_hi[wg][n] = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
         M.row_lo[wg][n] =
             P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
@@ -328,10 +342,11 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         l[n] = 0.f;
       }
 
-      for (int i = 0; i < g.n; ++i, ++tile) {
+#pragma unroll 1
+      for (int i = 0; i < g.n; ++i, tile += dry ? 0 : 1) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys, key = key0 + j;
         const uint32_t in_cta = g.tile0 + i;
-        wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
+        if (!dry) wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
         float s[N];
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         ptx::tmem_ld_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.s_empty[wg][tile % SB]);
+        if (lane == 0 && !dry) ptx::mbar_arrive(&M.s_empty[wg][tile % SB]);
         if (key0 < max_lo || key0 + kKeys - 1 > min_hi) {
 #pragma unroll
           for (int n = 0; n < A; ++n)
@@ -351,7 +366,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
                        : s[n];
         }
         // does a score exceed its reference maximum by more than 8?
-        bool up = false;
+        bool up = dry;
 #pragma unroll
         for (int n = 0; n < A; ++n) up |= fmaf(s[n], c, neg[n]) > 8.f;
         if (named_any(kBar, 128, up)) {
@@ -389,12 +404,12 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
             ptx::tc_fence_before();
           }
         }
-        if (tile_has_unseen(g.t, key0)) {
+        if (!dry && tile_has_unseen(g.t, key0)) {
           wait_quiet(&M.full_v[in_cta % kStages], (in_cta / kStages) & 1, abort_f);
           zero_unseen_value<D>(g.t, key0, j, smem + (in_cta % kStages) * La::kStage + La::kTile);
         }
         // P's buffer is free once the product that read it is done
-        if (tile >= PB) wait_quiet(&p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
+        if (tile >= PB && !dry) wait_quiet(&p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
         uint8_t* Pb = Pbase + (tile % PB) * La::kP + (j / 64) * (kPV * 128) + (j % 8) * 2;
         const int ch = (j % 64) / 8;
 #pragma unroll
@@ -408,43 +423,33 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_full[tile % PB]);
+        if (lane == 0 && !dry) ptx::mbar_arrive(&p_full[tile % PB]);
       }
 
-      // ---- the item, or this CTA's part of it, is done
+      // ---- the item, or this CTA's part of it, is done: O by way of P's
+      // buffer to threads that hold eight values of a row each
+      if (dry) continue;
 #pragma unroll
       for (int n = 0; n < A; ++n) {
         const float x = warp_sum(l[n]);
         if (lane == 0) reinterpret_cast<float*>(&red[n])[w] = x;
+        if (st_tid == 0) M.m[wg][n] = -neg[n];
       }
       wait_quiet(&p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
       __syncwarp();
       ptx::tc_fence_after();
-      named_bar(kBar, 128);
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
-      float* part = P.part + slot * A * D + d;
-      int tok = g.t.row0 / P.group, hd = g.t.row0 - tok * P.group;  // of row n
+      float* stage = reinterpret_cast<float*>(Pbase);
 #pragma unroll
       for (int n0 = 0; n0 < A; n0 += 16) {
         uint32_t oh[16], ol[16];
         ptx::tmem_ld16(tm_o + n0, oh);
         if (A >= 16) ptx::tmem_ld16(tm_o + kPV / 2 + n0, ol);
         ptx::tmem_ld_wait();
+        if (has_d) {
 #pragma unroll
-        for (int x = 0; x < (A < 16 ? A : 16); ++x) {
-          const int n = n0 + x;
-          const float o = __uint_as_float(oh[x]) + __uint_as_float(A >= 16 ? ol[x] : oh[x + 8]);
-          if (n < g.t.n_rows) {
-            const float4 r = red[n];
-            if (!has_d)
-              ;
-            else if (g.parts > 1)
-              part[n * D] = o;
-            else
-              write_row<D>(P, g, g.tok0 + tok, g.head * P.group + hd, d, o,
-                           r.x + r.y + r.z + r.w, -neg[n]);
-            if (++hd == P.group) hd = 0, ++tok;
-          }
+          for (int x = 0; x < (A < 16 ? A : 16); ++x)
+            stage[(n0 + x) * D + d] = __uint_as_float(oh[x]) +
+                                      __uint_as_float(A >= 16 ? ol[x] : oh[x + 8]);
         }
       }
       ptx::tc_fence_before();
@@ -453,61 +458,55 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         ptx::mbar_arrive(&M.o_empty[wg]);
         ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
       }
+      named_bar(kBar, 128);
+      float2* ml = reinterpret_cast<float2*>(P.part_ml);
+      const int vectors = g.t.n_rows * (D / 8);
+      bool write = true;
       if (g.parts > 1) {
-        float2* ml = reinterpret_cast<float2*>(P.part_ml);
+        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
+#pragma unroll 1
+        for (int x = st_tid; x < vectors; x += 128) {
+          const int n = x / (D / 8), k = x % (D / 8) * 8;
+          store8(P.part + (slot * A + n) * D + k,
+                 *reinterpret_cast<const float(*)[8]>(stage + n * D + k));
+          const float4 r = red[n];
+          if (k == 0) ml[slot * A + n] = make_float2(M.m[wg][n], r.x + r.y + r.z + r.w);
+        }
+        write = last_to_arrive(P, g, st_tid == 0, &M.last[wg], kBar, 128);
+      }
+#pragma unroll 1
+      for (int x = write ? st_tid : vectors; x < vectors; x += 128) {
+        const int n = x / (D / 8), k = x % (D / 8) * 8;
+        float o[8], top, sum;
+        if (g.parts == 1) {
+          const float4 r = red[n];
+          top = M.m[wg][n];
+          sum = r.x + r.y + r.z + r.w;
+          load8(stage + n * D + k, o);
+        } else {
+          // all parts, in their order
+          top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+          for (int q = 0; q < g.parts; ++q)
+            top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * A + n].x));
 #pragma unroll
-        for (int n = 0; n < A; ++n) {
-          if (st_tid == n) {
-            const float4 r = red[n];
-            ml[slot * A + n] = make_float2(-neg[n], r.x + r.y + r.z + r.w);
+          for (int y = 0; y < 8; ++y) o[y] = 0.f;
+#pragma unroll 4
+          for (int q = 0; q < g.parts; ++q) {
+            const float2 v = __ldcg(&ml[part_slot(g, q) * A + n]);
+            const float4* from =
+                reinterpret_cast<const float4*>(P.part + (part_slot(g, q) * A + n) * D + k);
+            const float4 a = __ldcg(from), b = __ldcg(from + 1);
+            const float f = top == -INFINITY ? 0.f : exp2_fast(v.x - top);
+            sum += f * v.y;
+            o[0] += f * a.x; o[1] += f * a.y; o[2] += f * a.z; o[3] += f * a.w;
+            o[4] += f * b.x; o[5] += f * b.y; o[6] += f * b.z; o[7] += f * b.w;
           }
         }
-        if (last_to_arrive(P, g, st_tid == 0, &M.last[wg], kBar, 128)) {
-          // all parts' maxima and sums by way of P's buffer, which is free
-          constexpr int kChunk = La::kP / (A * 8);
-          float2* all = reinterpret_cast<float2*>(Pbase);
-          float o[A], top[A], sum[A];
-#pragma unroll
-          for (int n = 0; n < A; ++n) o[n] = sum[n] = 0.f, top[n] = -INFINITY;
-          for (int c0 = 0; c0 < g.parts; c0 += kChunk) {
-            const int cnt = min(kChunk, g.parts - c0);
-            for (int x = st_tid; x < cnt * A; x += 128)
-              all[x] = __ldcg(&ml[part_slot(g, c0 + x / A) * A + x % A]);
-            named_bar(kBar, 128);
-#pragma unroll
-            for (int n = 0; n < A; ++n) {
-              float now = top[n];
-              for (int q = 0; q < cnt; ++q) now = fmaxf(now, all[q * A + n].x);
-              const float f = top[n] == -INFINITY ? 0.f : exp2_fast(top[n] - now);
-              o[n] *= f;
-              sum[n] *= f;
-              top[n] = now;
-            }
-            for (int q = 0; q < cnt; ++q) {
-              const float* from = P.part + part_slot(g, c0 + q) * A * D + (has_d ? d : 0);
-              float v[A];
-#pragma unroll
-              for (int n = 0; n < A; ++n) v[n] = n < g.t.n_rows ? __ldcg(from + n * D) : 0.f;
-#pragma unroll
-              for (int n = 0; n < A; ++n) {
-                const float2 x = all[q * A + n];
-                const float f = top[n] == -INFINITY ? 0.f : exp2_fast(x.x - top[n]);
-                sum[n] += f * x.y;
-                o[n] += f * v[n];
-              }
-            }
-            named_bar(kBar, 128);
-          }
-          tok = g.t.row0 / P.group, hd = g.t.row0 - tok * P.group;
-#pragma unroll
-          for (int n = 0; n < A; ++n) {
-            if (n < g.t.n_rows) {
-              if (has_d)
-                write_row<D>(P, g, g.tok0 + tok, g.head * P.group + hd, d, o[n], sum[n], top[n]);
-              if (++hd == P.group) hd = 0, ++tok;
-            }
-          }
-        }
+        const int r = g.t.row0 + n, tok = P.by_group(r);
+        const RowWriter<D> out(P, g.shared, g.tok0 + tok,
+                               g.head * P.group + r - tok * P.group, true, top, sum);
+        out.write8(k, o);
       }
       named_bar(kBar, 128);  // red and the limits are free
     }

@@ -144,10 +144,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
-  __syncthreads();
-  ptx::tc_fence_after();
   pdl_wait();
   pdl_launch_dependents();
+  // the tiles' memory holds the problems' sizes until the first load
+  size_problems(P, reinterpret_cast<ProblemSize*>(smem));
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+  ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;  // S (and P) of half h at h * 128, O at 256 + h * 128
 
   // (each role's branch begins with its own split, so that the compiler knows
@@ -157,7 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ---------------- schedule and TMA ----------------------------------
     Walker walk;
-    walk.start(P);
+    walk.start(P, reinterpret_cast<ProblemSize*>(smem));
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
     TileLoader<D> load(P);
     int n = 0;              // tiles brought in: K in slot 2n, V in slot 2n + 1
     int q_use[2] = {0, 0};  // segments of each half
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_expect_tx(&M.q_full[h], half_rows * D * 2);
           for (int x = 0; x < D / 64; ++x)
             tma_load_rows(smem + La::oQ + h * La::kTile + x * (kHalf * 128), &tm_q, &M.q_full[h],
-                          g.head * P.group, g.tok0 + (g.t.row0 + h * half_rows) / P.group, x);
+                          g.head * P.group, g.tok0 + P.by_group(g.t.row0 + h * half_rows), x);
         }
         ++q_use[h];
       }
@@ -298,13 +303,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile = 0;  // tiles of this half so far
     // The warpgroup's four warps meet at barriers: after a wait that gave up
     // they run on (every later wait returns at once) to the vote.
-    for (int sg = 0;; ++sg) {
-      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
-      if (named_any(bar, 128, *abort_f != 0)) break;
-      const Segment g = M.ring[sg % kRing];
-      if (g.n == 0) break;
+    // Segment -1 has nothing in it: its one tile, without waits and effects,
+    // brings the loop's instructions in while the first segment is looked for.
+    for (int sg = P.kv.T < 0 ? 0 : -1;; ++sg) {
+      const bool dry = sg < 0;
+      Segment g = {};
+      g.n = g.parts = 1;
+      if (!dry) {
+        wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+        if (named_any(bar, 128, *abort_f != 0)) break;
+        g = M.ring[sg % kRing];
+        if (g.n == 0) break;
+      }
       const int n_rows = min(g.t.n_rows - h * half_rows, half_rows);  // of this half
-      if (n_rows <= 0) {
+      if (n_rows <= 0 && !dry) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
         continue;
@@ -312,15 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows past the last copy the first one
       const bool mine = row < n_rows;
       const int in_prob = g.t.row0 + h * half_rows + (mine ? row : 0);
-      const int tok = in_prob / P.group, head = g.head * P.group + in_prob - tok * P.group;
+      const int tok = P.by_group(in_prob), head = g.head * P.group + in_prob - tok * P.group;
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo =
           P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < g.n; ++i, ++tile) {
+#pragma unroll 1
+      for (int i = 0; i < g.n; ++i, tile += dry ? 0 : 1) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys;
-        wait_quiet(&M.s_full[h], tile & 1, abort_f);
+        if (!dry) wait_quiet(&M.s_full[h], tile & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
         float s[kKeys];
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (h == 0 && tile_has_unseen(g.t, key0)) {
+        if (h == 0 && !dry && tile_has_unseen(g.t, key0)) {
           // (half 0 takes part in every tile, and its P V is issued first)
           const int k = 2 * tile + 1;
           wait_quiet(&M.full[k % kSlots], (k / kSlots) & 1, abort_f);
@@ -397,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum0 = add2(sum0, pack2(a, b));
             p[x] = pack_bf16x2(a, b);
           }
-          ptx::tmem_st16(tm_s + k / 2, p);
-          if (k == 32 || k == 96) {
+          if (!dry) ptx::tmem_st16(tm_s + k / 2, p);
+          if (!dry && (k == 32 || k == 96)) {
             // each half of the keys goes to the MMA as soon as it is there
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
@@ -414,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the item, or this CTA's part of it, is done
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
       const RowWriter<D> out(P, g.shared, g.tok0 + tok, head, mine && g.parts == 1, m, l);
+      if (dry) continue;
       wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
       __syncwarp();
       ptx::tc_fence_after();
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
   for (int x = threadIdx.x; x < 32 * (kCols / 8); x += 256) {
     const int r = x / (kCols / 8), k = x % (kCols / 8);
     if (row0 + r >= half_rows || h * half_rows + row0 + r >= it.n_rows) continue;
-    const int in_prob = it.row0 + h * half_rows + row0 + r, tok = in_prob / P.group;
+    const int in_prob = it.row0 + h * half_rows + row0 + r, tok = P.by_group(in_prob);
     const RowWriter<D> out(P, it.shared, it.tok0 + tok, it.head * P.group + in_prob - tok * P.group,
                            true, top_s[r], sum_s[r]);
     float v[8];
