@@ -267,6 +267,17 @@ __device__ __forceinline__ void size_problems(const AttnParams& P, ProblemSize* 
   for (int p = threadIdx.x; p < n; p += blockDim.x) sizes[p] = problem_size(P, load_problem(P, p));
 }
 
+// After it and a barrier, the long ones: a warp to a problem.
+__device__ __forceinline__ void size_long_problems(const AttnParams& P, ProblemSize* sizes) {
+  const int n = min(P.groups_phase ? P.n_groups : P.kv.n_seqs, kSized);
+  for (int p = threadIdx.x / 32; p < n; p += blockDim.x / 32) {
+    if (sizes[p].units >= 0) continue;
+    const int64_t units = problem_units(P, load_problem(P, p));
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0 && units <= INT32_MAX) sizes[p].units = static_cast<int>(units);
+  }
+}
+
 // 32 consecutive problems, one to a lane.  Those of many row tiles (prompts)
 // are added up by the whole warp.
 struct LaneSize {

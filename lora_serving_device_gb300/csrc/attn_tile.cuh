@@ -127,11 +127,12 @@ template <int D>
 __device__ __forceinline__ void zero_unseen_value(const RowTile& t, int key0, int j, uint8_t* V) {
   if (tile_key_seen(t, key0 + j)) return;
   uint8_t* row = V + (j / 8) * (D / 64) * 1024 + (j % 8) * 128;
+  // (each lane starts elsewhere in its 128 bytes: the rows lie 128 bytes apart)
 #pragma unroll
   for (int h = 0; h < D / 64; ++h)
 #pragma unroll
     for (int x = 0; x < 8; ++x)
-      *reinterpret_cast<uint4*>(row + h * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(row + h * 1024 + ((x + j) & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // L2 policies: what one CTA alone reads leaves first, so that a step's block
@@ -172,38 +173,49 @@ template <int D>
 struct TileLoader {
   int page, lg_page, box, boxes, per;
   uint64_t policy;
-  int now, next;  // where this lane's box starts in the cache, in groups of eight
-                  // rows, for two batches of `per` tiles; -1: not needed
+  int now;   // where this lane's box starts in the cache, in groups of eight rows,
+             // in this batch of `per` tiles; -1: not needed
+  int next;  // its page's id in the next batch; INT32_MIN: not needed
   __device__ __forceinline__ explicit TileLoader(const AttnParams& P)
       : page(P.kv.page_size),
         lg_page(P.lg_page),
         box(page < kKeys ? page : kKeys),
         boxes(kKeys / box),
         per(32 / boxes) {}
-  __device__ __forceinline__ int lookup(const AttnParams& P, const Segment& g, int i0) const {
-    const int lane = threadIdx.x & 31, i = i0 + lane / boxes;
-    const int key0 = key_tile(g.t, g.first + i) * kKeys + (lane & (boxes - 1)) * box;
-    if (i >= g.n || !((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) || key0 < g.t.n_sink))
-      return -1;
-    const int id =
-        P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages + (key0 >> lg_page)];
+  // This lane's box of the batch from tile i0: its page's id as the table has
+  // it (a load that nothing here waits for), and where it starts.
+  __device__ __forceinline__ int first_key(const Segment& g, int i0) const {
+    const int lane = threadIdx.x & 31;
+    return key_tile(g.t, g.first + i0 + lane / boxes) * kKeys + (lane & (boxes - 1)) * box;
+  }
+  __device__ __forceinline__ int fetch(const AttnParams& P, const Segment& g, int i0) const {
+    const int key0 = first_key(g, i0);
+    const bool seen = i0 + (threadIdx.x & 31) / boxes < g.n &&
+                      ((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) || key0 < g.t.n_sink);
+    return seen ? P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages +
+                                   (key0 >> lg_page)]
+                : INT32_MIN;
+  }
+  __device__ __forceinline__ int place(const AttnParams& P, const Segment& g, int i0, int id) const {
+    if (id == INT32_MIN) return -1;
     if (id < 0 || id >= P.kv.n_pages) {
       flag_error(P.err, LORA_DEVERR_BAD_PAGE);
       return P.kv.n_pages * P.kv.n_kv_heads * (page / 8);
     }
-    return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (key0 & (page - 1)) / 8;
+    return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (first_key(g, i0) & (page - 1)) / 8;
   }
   __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
     policy = l2_policy(g.once != 0);
-    now = lookup(P, g, 0);
-    next = g.n > per ? lookup(P, g, per) : -1;
+    const int id = fetch(P, g, 0);
+    next = g.n > per ? fetch(P, g, per) : INT32_MIN;
+    now = place(P, g, 0, id);
   }
   // The place of this lane's box of tile i (lanes below `boxes`).
   __device__ __forceinline__ int at(const AttnParams& P, const Segment& g, int i) {
     const int k = i % per;
     if (k == 0 && i > 0) {
-      now = next;
-      next = i + per < g.n ? lookup(P, g, i + per) : -1;
+      now = place(P, g, i, next);
+      next = i + per < g.n ? fetch(P, g, i + per) : INT32_MIN;
     }
     const int lane = threadIdx.x & 31;
     const int x = __shfl_sync(0xffffffffu, now, k * boxes + (lane & (boxes - 1)));
@@ -270,6 +282,21 @@ struct RowWriter {
       for (int i = 0; i < 8; ++i) y[i] += other * z[i];
     }
     store8(out + d, y);
+  }
+  // Sixteen values, in one 32-byte store where `out` allows it.
+  __device__ __forceinline__ void write16(int d, const float* x) const {
+    if (to_prior || join || (reinterpret_cast<uintptr_t>(out) & 31) != 0) {
+      write8(d, x);
+      write8(d + 8, x + 8);
+      return;
+    }
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(x[2 * i] * own, x[2 * i + 1] * own);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + d),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]),
+                 "r"(u[7])
+                 : "memory");
   }
 };
 

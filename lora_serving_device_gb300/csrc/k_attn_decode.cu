@@ -308,20 +308,12 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     // wait that gave up they run on (every later wait returns at once) to
     // the vote at the next segment.
     uint32_t tile = 0;  // tiles of this warpgroup so far
-    // A first segment with nothing in it: its one tile, without waits and
-    // effects, brings the loop's instructions in while the first real segment
-    // is looked for.
-    for (int sg = P.kv.T < 0 ? wg : wg - W;; sg += W) {
-      const bool dry = sg < 0;
-      Segment g = {};
-      g.n = g.parts = 1;
-      if (!dry) {
-        wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
-        if (named_any(kBar, 128, *abort_f != 0)) break;
-        g = M.ring[sg % kRing];
-        if (g.n == 0) break;
-        load_q(g);  // (the MMAs that read the last one's are done: so are its scores)
-      }
+    for (int sg = wg;; sg += W) {
+      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (named_any(kBar, 128, *abort_f != 0)) break;
+      const Segment g = M.ring[sg % kRing];
+      if (g.n == 0) break;
+      load_q(g);  // (the MMAs that read the last one's are done: so are its scores)
       // limits of the rows (rows past the last copy row 0's)
       for (int n = st_tid; n < A; n += 128) {
         const int pos = g.base + P.by_group(g.t.row0 + (n < g.t.n_rows ? n : 0));
@@ -343,10 +335,10 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
       }
 
 #pragma unroll 1
-      for (int i = 0; i < g.n; ++i, tile += dry ? 0 : 1) {
+      for (int i = 0; i < g.n; ++i, ++tile) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys, key = key0 + j;
         const uint32_t in_cta = g.tile0 + i;
-        if (!dry) wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
+        wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
         float s[N];
@@ -357,7 +349,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         ptx::tmem_ld_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !dry) ptx::mbar_arrive(&M.s_empty[wg][tile % SB]);
+        if (lane == 0) ptx::mbar_arrive(&M.s_empty[wg][tile % SB]);
         if (key0 < max_lo || key0 + kKeys - 1 > min_hi) {
 #pragma unroll
           for (int n = 0; n < A; ++n)
@@ -366,7 +358,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
                        : s[n];
         }
         // does a score exceed its reference maximum by more than 8?
-        bool up = dry;
+        bool up = false;
 #pragma unroll
         for (int n = 0; n < A; ++n) up |= fmaf(s[n], c, neg[n]) > 8.f;
         if (named_any(kBar, 128, up)) {
@@ -404,12 +396,12 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
             ptx::tc_fence_before();
           }
         }
-        if (!dry && tile_has_unseen(g.t, key0)) {
+        if (tile_has_unseen(g.t, key0)) {
           wait_quiet(&M.full_v[in_cta % kStages], (in_cta / kStages) & 1, abort_f);
           zero_unseen_value<D>(g.t, key0, j, smem + (in_cta % kStages) * La::kStage + La::kTile);
         }
         // P's buffer is free once the product that read it is done
-        if (tile >= PB && !dry) wait_quiet(&p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
+        if (tile >= PB) wait_quiet(&p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);
         uint8_t* Pb = Pbase + (tile % PB) * La::kP + (j / 64) * (kPV * 128) + (j % 8) * 2;
         const int ch = (j % 64) / 8;
 #pragma unroll
@@ -423,12 +415,11 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && !dry) ptx::mbar_arrive(&p_full[tile % PB]);
+        if (lane == 0) ptx::mbar_arrive(&p_full[tile % PB]);
       }
 
       // ---- the item, or this CTA's part of it, is done: O by way of P's
       // buffer to threads that hold eight values of a row each
-      if (dry) continue;
 #pragma unroll
       for (int n = 0; n < A; ++n) {
         const float x = warp_sum(l[n]);

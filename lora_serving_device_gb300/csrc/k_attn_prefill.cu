@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   // the tiles' memory holds the problems' sizes until the first load
   size_problems(P, reinterpret_cast<ProblemSize*>(smem));
+  __syncthreads();
+  size_long_problems(P, reinterpret_cast<ProblemSize*>(smem));
   ptx::fence_proxy_async_smem();
   __syncthreads();
   ptx::tc_fence_after();
@@ -303,20 +305,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile = 0;  // tiles of this half so far
     // The warpgroup's four warps meet at barriers: after a wait that gave up
     // they run on (every later wait returns at once) to the vote.
-    // Segment -1 has nothing in it: its one tile, without waits and effects,
-    // brings the loop's instructions in while the first segment is looked for.
-    for (int sg = P.kv.T < 0 ? 0 : -1;; ++sg) {
-      const bool dry = sg < 0;
-      Segment g = {};
-      g.n = g.parts = 1;
-      if (!dry) {
-        wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
-        if (named_any(bar, 128, *abort_f != 0)) break;
-        g = M.ring[sg % kRing];
-        if (g.n == 0) break;
-      }
+    for (int sg = 0;; ++sg) {
+      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (named_any(bar, 128, *abort_f != 0)) break;
+      const Segment g = M.ring[sg % kRing];
+      if (g.n == 0) break;
       const int n_rows = min(g.t.n_rows - h * half_rows, half_rows);  // of this half
-      if (n_rows <= 0 && !dry) {
+      if (n_rows <= 0) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
         continue;
@@ -331,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-      for (int i = 0; i < g.n; ++i, tile += dry ? 0 : 1) {
+      for (int i = 0; i < g.n; ++i, ++tile) {
         const int key0 = key_tile(g.t, g.first + i) * kKeys;
-        if (!dry) wait_quiet(&M.s_full[h], tile & 1, abort_f);
+        wait_quiet(&M.s_full[h], tile & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
         float s[kKeys];
@@ -385,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (h == 0 && !dry && tile_has_unseen(g.t, key0)) {
+        if (h == 0 && tile_has_unseen(g.t, key0)) {
           // (half 0 takes part in every tile, and its P V is issued first)
           const int k = 2 * tile + 1;
           wait_quiet(&M.full[k % kSlots], (k / kSlots) & 1, abort_f);
@@ -410,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum0 = add2(sum0, pack2(a, b));
             p[x] = pack_bf16x2(a, b);
           }
-          if (!dry) ptx::tmem_st16(tm_s + k / 2, p);
-          if (!dry && (k == 32 || k == 96)) {
+          ptx::tmem_st16(tm_s + k / 2, p);
+          if (k == 32 || k == 96) {
             // each half of the keys goes to the MMA as soon as it is there
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
@@ -427,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the item, or this CTA's part of it, is done
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
       const RowWriter<D> out(P, g.shared, g.tok0 + tok, head, mine && g.parts == 1, m, l);
-      if (dry) continue;
       wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
       __syncwarp();
       ptx::tc_fence_after();
@@ -445,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g.parts == 1) {
         if (mine) {
 #pragma unroll
-          for (int k = 0; k < D; k += 8) out.write8(k, o + k);
+          for (int k = 0; k < D; k += 16) out.write16(k, o + k);
         }
         continue;
       }
