@@ -10,7 +10,7 @@
 // cost of taking it up and finishing it.  All units, numbered row tile by row
 // tile, key head by key head, are cut into equal contiguous shares, one per
 // CTA, whatever the lengths are (they live on the device).  An item that
-// several CTAs share is finished by the last of them to arrive, which adds
+// several CTAs share (short ones are not shared) is finished by the last of them to arrive, which adds
 // their parts in CTA order: the result is a function of the lengths alone.
 // Each CTA finds its share itself: its threads size a problem each, and one
 // warp adds the sizes up and looks for its place.
@@ -80,6 +80,7 @@ struct AttnParams {
   FastDiv by_group, by_rows;
   int lg_page;         // log2 of the page size
   int over;            // units that an item costs beside its key tiles
+  int whole;           // items of up to that many key tiles are not split
   int n_q_heads;
   float scale_log2;    // scale * log2(e)
   int window, n_sink;
@@ -323,7 +324,7 @@ struct Walker {
   RowTile t;
   int prob, rt;      // the problem, and the row tile's number in it
   int tile;          // and over all problems
-  int u, end;        // next unit, end of the share
+  int u, begin, end; // next unit, the share's
   int total, share;  // units of the call, units of a CTA
   int tile_unit;     // first unit of the row tile
   int done;          // key tiles of the segments so far
@@ -361,6 +362,7 @@ struct Walker {
     share = even > least ? even : least;
     const int64_t first = static_cast<int64_t>(share) * blockIdx.x;
     u = first < total ? static_cast<int>(first) : total;
+    begin = u;
     end = total - u < share ? total : u + share;
     if (u >= end) return;
     // the problem that unit u belongs to
@@ -418,16 +420,29 @@ struct Walker {
   __device__ __forceinline__ Segment next(const AttnParams& P) {
     Segment g;
     g.n = 0;
-    if (u >= end) return g;
-    while (tile_unit + units(P) <= u) advance(P);
-    const int span = t.n_tiles + P.over;
-    g.head = (u - tile_unit) / span;
-    const int a = tile_unit + g.head * span + P.over;
-    const int b = a + t.n_tiles;
-    if (u < a) u = a;
-    if (u >= end) return g;  // the share ends in front of the item's key tiles
-    g.first = u - a;
-    g.n = (end < b ? end : b) - u;
+    int a, b;
+    for (;;) {
+      if (u >= end) return g;
+      while (tile_unit + units(P) <= u) advance(P);
+      const int span = t.n_tiles + P.over;
+      g.head = (u - tile_unit) / span;
+      a = tile_unit + g.head * span + P.over;
+      b = a + t.n_tiles;
+      if (t.n_tiles <= P.whole) {
+        // a short item goes whole to the CTA that its first unit falls to
+        u = b;
+        if (a - P.over < begin) continue;
+        g.first = 0;
+        g.n = t.n_tiles;
+        break;
+      }
+      if (u < a) u = a;
+      if (u >= end) return g;  // the share ends in front of the item's key tiles
+      g.first = u - a;
+      g.n = (end < b ? end : b) - u;
+      u += g.n;
+      break;
+    }
     g.table_row = pr.table_row;
     g.tok0 = pr.tok0;
     g.base = pr.base;
@@ -446,7 +461,6 @@ struct Walker {
     g.tile0 = done;
     g.once = pr.n_rows <= P.rows ? 1 : 0;
     done += g.n;
-    u += g.n;
     return g;
   }
 };

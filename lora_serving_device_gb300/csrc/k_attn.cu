@@ -132,7 +132,8 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.max_row_tiles = w.max_row_tiles[phase];
     P.rows = w.shape[phase].rows;
     P.by_rows = FastDiv::of(P.rows);
-    P.over = w.shape[phase].prefill ? 4 : 1;
+    P.over = w.shape[phase].prefill ? 3 : 1;
+    P.whole = w.shape[phase].prefill ? 2 : 8;
     cudaError_t e;
     if (w.shape[phase].prefill) {
       if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;

@@ -465,13 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the items that several CTAs shared: block (c, y, z) takes 32
 // rows (y) and half the columns (z) of the item that begins in CTA c and ends
-// in another, if there is one.  A lane is a row; the parts' factors come first,
-// then each warp adds up its columns, so that all reads are whole lines, and
+// in another, if there is one.  A lane is a row; each warp adds up its columns
+// over the parts, so that all reads are whole lines, and
 // the rows are written from shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
   constexpr int kCols = D / 2, kPer = kCols / 4 / 8;  // vectors of a warp
-  __shared__ float fac[kDecodeScheduleCtas][32];
+  __shared__ float2 fac[kDecodeScheduleCtas][32];  // maxima and sums
   __shared__ float4 rows[32][kCols / 4 + 1];
   __shared__ float top_s[32], sum_s[32];
   pdl_wait();
@@ -484,35 +484,48 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
   const bool used = row < half_rows && h * half_rows + row < it.n_rows;
   auto slot = [&](int q) { return static_cast<int64_t>(c + q) * 2 + (q == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(P.part_ml) + h * kHalf + row;
-  float top = -INFINITY, sum = 0.f;
-#pragma unroll 8
-  for (int q = 0; q < it.parts; ++q) top = fmaxf(top, used ? ml[slot(q) * 2 * kHalf].x : 0.f);
-  for (int q = warp; q < it.parts; q += 8)
-    fac[q][lane] =
-        !used || top == -INFINITY ? 0.f : exp2f(ml[slot(q) * 2 * kHalf].x - top);
-  __syncthreads();
-  if (warp == 0) {
-#pragma unroll 8
-    for (int q = 0; q < it.parts; ++q) sum += used ? fac[q][lane] * ml[slot(q) * 2 * kHalf].y : 0.f;
-    top_s[lane] = top;
-    sum_s[lane] = sum;
-  }
   const int k0 = blockIdx.z * (kCols / 4) + warp * kPer;
+  auto value = [&](int q, int x) { return part_row<D>(P, slot(q), h, row)[(k0 + x) * kHalf]; };
+  // the first parts' values are on their way beside the maxima and sums
+  constexpr int kAhead = 8;
+  float4 v[kAhead][kPer];
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) v[q][x] = q < it.parts ? value(q, x) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = warp; q < it.parts; q += 8)
+    fac[q][lane] = used ? ml[slot(q) * 2 * kHalf] : make_float2(-INFINITY, 0.f);
+  __syncthreads();
+  float top = -INFINITY, sum = 0.f;
+  for (int q = 0; q < it.parts; ++q) top = fmaxf(top, fac[q][lane].x);
+  const float ref = top == -INFINITY ? 0.f : top;
   float4 o[kPer];
 #pragma unroll
   for (int x = 0; x < kPer; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int q = 0; q < it.parts; ++q) {
-    const float f = fac[q][lane];
-    const float4* from = part_row<D>(P, slot(q), h, row) + k0 * kHalf;
+  for (int q0 = 0; q0 < it.parts; q0 += kAhead) {
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const float4 v = from[x * kHalf];
-      o[x].x += f * v.x;
-      o[x].y += f * v.y;
-      o[x].z += f * v.z;
-      o[x].w += f * v.w;
+    for (int q = 0; q < kAhead; ++q) {
+      if (q0 + q >= it.parts) break;
+      const float2 z = fac[q0 + q][lane];
+      const float f = exp2f(z.x - ref);
+      sum += f * z.y;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        o[x].x += f * v[q][x].x;
+        o[x].y += f * v[q][x].y;
+        o[x].z += f * v[q][x].z;
+        o[x].w += f * v[q][x].w;
+      }
     }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+        if (q0 + kAhead + q < it.parts) v[q][x] = value(q0 + kAhead + q, x);
+  }
+  if (warp == 0) {
+    top_s[lane] = top;
+    sum_s[lane] = sum;
   }
 #pragma unroll
   for (int x = 0; x < kPer; ++x) rows[lane][warp * kPer + x] = o[x];

@@ -17,7 +17,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;
+constexpr int kBatch = 2;
 
 struct Rot {
   float c[8], s[8];
@@ -62,9 +62,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const lora_paged_kv
   pdl_wait();
   pdl_launch_dependents();
 
-  const int s = seq_of_row(kv.q_off, kv.n_seqs, t);
-  if (s < 0) return;
-
   const bf16* q = static_cast<const bf16*>(a.q) + t * a.q_stride;
   const bf16* k = static_cast<const bf16*>(a.k) + t * a.k_stride;
   const bf16* v = static_cast<const bf16*>(a.v) + t * a.v_stride;
@@ -83,7 +80,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const lora_paged_kv
     }
   };
   load(h0);
-
+  // (rows of no sequence are read, not used)
+  const int s = seq_of_row(kv.q_off, kv.n_seqs, t);
+  if (s < 0) return;
   const int p = kv.kv_len[s] - kv.q_off[s + 1] + t;
   Rot r;
   if (rotates) {
