@@ -81,12 +81,13 @@ struct AttnParams {
   int lg_page;         // log2 of the page size
   int over;            // units that an item costs beside its key tiles
   int whole;           // items of up to that many key tiles are not split
+  bool join_after;     // parts are joined by a kernel of their own (prefill)
   int n_q_heads;
   float scale_log2;    // scale * log2(e)
   int window, n_sink;
   int max_row_tiles;   // row tiles that the counters are laid out for
   uint32_t* err;
-  uint32_t* count;     // arrivals per item, zero between calls
+  uint32_t* count;     // arrivals per item (prefill: per half of one), zero between calls
   float* part;         // [CTA][2][row tile] partial sums
   float* part_ml;      // [CTA][2][rows][2] their maxima (log2 units) and sums
   SplitItem* split;    // [CTA] the item that begins there and ends in another (prefill)

@@ -306,15 +306,15 @@ __device__ __forceinline__ int64_t part_slot(const Segment& g, int c) {
 }
 
 // Threads of named barrier `bar` (cnt of them) have written this CTA's part:
-// is it the item's last?  Leaves the counter at zero.
-__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, bool leader,
-                                               int* flag, int bar, int cnt) {
+// is it the last of the item (or of its half)?  Leaves the counter at zero.
+__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, int counter,
+                                               bool leader, int* flag, int bar, int cnt) {
   __threadfence();
   named_bar(bar, cnt);
   if (leader) {
-    const uint32_t before = atomicAdd(&P.count[g.item], 1u);
+    const uint32_t before = atomicAdd(&P.count[counter], 1u);
     *flag = before + 1 == static_cast<uint32_t>(g.parts) ? 1 : 0;
-    if (*flag) P.count[g.item] = 0;
+    if (*flag) P.count[counter] = 0;
     __threadfence();
   }
   named_bar(bar, cnt);

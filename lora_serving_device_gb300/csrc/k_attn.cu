@@ -50,7 +50,8 @@ Layout layout(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
   for (int i = 0; i < (n_groups > 0 ? 2 : 1); ++i) {
     const int64_t tiles = total / w.shape[i].rows + (i == 0 ? kv.n_seqs : n_groups);
     w.max_row_tiles[i] = static_cast<int>(tiles);
-    if (tiles > items) items = tiles;
+    const int64_t counters = w.shape[i].prefill ? 2 * tiles : tiles;
+    if (counters > items) items = counters;
     if (w.shape[i].space > space) space = w.shape[i].space;
   }
   const size_t slots = static_cast<size_t>(kDecodeScheduleCtas) * 2 * space;
@@ -134,6 +135,9 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.by_rows = FastDiv::of(P.rows);
     P.over = w.shape[phase].prefill ? 3 : 1;
     P.whole = w.shape[phase].prefill ? 2 : 8;
+    // the fewest items that this many rows can make: at 38 and more one has six
+    // parts at most, if the others are as long
+    P.join_after = static_cast<int64_t>(kv.T) * P.group / P.rows * kv.n_kv_heads < 38;
     cudaError_t e;
     if (w.shape[phase].prefill) {
       if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;

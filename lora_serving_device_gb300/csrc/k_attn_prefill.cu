@@ -57,6 +57,7 @@ struct Misc {
   uint64_t seg_full[kRing], seg_empty[kRing];
   uint32_t tmem;
   int abort;
+  int last[2];
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (g.n == 0) break;
       load.begin(P, g);
-      if (g.parts > 1 && g.cta0 == blockIdx.x)
+      if (P.join_after && g.parts > 1 && g.cta0 == blockIdx.x)
         mine = {g.parts, g.tok0, g.t.row0, g.t.n_rows, g.head, g.shared, {0, 0}};
       for (int h = 0; h < 2 && ok; ++h) {
         if (g.t.n_rows <= h * half_rows) break;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) P.split[blockIdx.x] = mine;
+    if (P.join_after && lane == 0) P.split[blockIdx.x] = mine;
     if (!ok) {
       // gave up: what is on its way into shared memory has to land first
       int none = 0;
@@ -451,6 +452,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[(k / 4) * kHalf] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         ml[slot * 2 * kHalf] = make_float2(m, l);
       }
+      if (!P.join_after &&
+          last_to_arrive(P, g, g.item * 2 + h, row == 0, &M.last[h], bar, 128) && mine) {
+        // few parts: the last to arrive adds them up, in their order
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (int q = 0; q < g.parts; ++q)
+          top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
+#pragma unroll
+        for (int k = 0; k < D; ++k) o[k] = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
+          const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
+          const float f = exp2_fast(v.x - top);
+          sum += f * v.y;
+          const float4* from = part_row<D>(P, part_slot(g, q), h, row);
+#pragma unroll
+          for (int k = 0; k < D; k += 4) {
+            const float4 z = __ldcg(from + (k / 4) * kHalf);
+            o[k] += f * z.x;
+            o[k + 1] += f * z.y;
+            o[k + 2] += f * z.z;
+            o[k + 3] += f * z.w;
+          }
+        }
+        const RowWriter<D> joined(P, g.shared, g.tok0 + tok, head, true, top, sum);
+#pragma unroll
+        for (int k = 0; k < D; k += 16) joined.write16(k, o + k);
+      }
     }
   }
 
@@ -463,28 +492,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_f) flag_error(P.err, LORA_DEVERR_TIMEOUT);
 }
 
-// Joins the parts of the items that several CTAs shared: block (c, y, z) takes 32
-// rows (y) and half the columns (z) of the item that begins in CTA c and ends
-// in another, if there is one.  A lane is a row; each warp adds up its columns
-// over the parts, so that all reads are whole lines, and
-// the rows are written from shared memory.
+// Joins the parts of the items that several CTAs shared, where there can be
+// many of each.  The work is cut into pieces of 32 rows and half the columns;
+// each block looks up the split items and takes every kJoinBlocks-th piece.
+// A lane is a row; each warp adds up its columns over the parts, so that all
+// reads are whole lines, and the rows are written from shared memory.
+constexpr int kJoinBlocks = 4 * kDecodeScheduleCtas;
+
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
+__device__ __forceinline__ void join_piece(const AttnParams& P, const SplitItem& it, int c, int h,
+                                           int row0, int z, float2 (*fac)[32],
+                                           float4 (*rows)[D / 8 + 1], float* top_s, float* sum_s) {
   constexpr int kCols = D / 2, kPer = kCols / 4 / 8;  // vectors of a warp
-  __shared__ float2 fac[kDecodeScheduleCtas][32];  // maxima and sums
-  __shared__ float4 rows[32][kCols / 4 + 1];
-  __shared__ float top_s[32], sum_s[32];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const SplitItem it = P.split[c];
-  const int half_rows = P.rows / 2;
-  const int h = blockIdx.y / 4, row0 = blockIdx.y % 4 * 32, row = row0 + lane;  // in the half
-  if (it.parts <= 1 || row0 >= half_rows || h * half_rows + row0 >= it.n_rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int half_rows = P.rows / 2, row = row0 + lane;
   const bool used = row < half_rows && h * half_rows + row < it.n_rows;
   auto slot = [&](int q) { return static_cast<int64_t>(c + q) * 2 + (q == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(P.part_ml) + h * kHalf + row;
-  const int k0 = blockIdx.z * (kCols / 4) + warp * kPer;
+  const int k0 = z * (kCols / 4) + warp * kPer;
   auto value = [&](int q, int x) { return part_row<D>(P, slot(q), h, row)[(k0 + x) * kHalf]; };
   // the first parts' values are on their way beside the maxima and sums
   constexpr int kAhead = 8;
@@ -536,10 +561,53 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
     const int in_prob = it.row0 + h * half_rows + row0 + r, tok = P.by_group(in_prob);
     const RowWriter<D> out(P, it.shared, it.tok0 + tok, it.head * P.group + in_prob - tok * P.group,
                            true, top_s[r], sum_s[r]);
-    float v[8];
-    *reinterpret_cast<float4*>(v) = rows[r][2 * k];
-    *reinterpret_cast<float4*>(v + 4) = rows[r][2 * k + 1];
-    out.write8(blockIdx.z * kCols + 8 * k, v);
+    float y[8];
+    *reinterpret_cast<float4*>(y) = rows[r][2 * k];
+    *reinterpret_cast<float4*>(y + 4) = rows[r][2 * k + 1];
+    out.write8(z * kCols + 8 * k, y);
+  }
+  __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams P) {
+  __shared__ float2 fac[kDecodeScheduleCtas][32];  // maxima and sums
+  __shared__ float4 rows[32][D / 8 + 1];
+  __shared__ float top_s[32], sum_s[32];
+  __shared__ int before[256], warp_sum_s[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  // pieces of the item that begins in CTA `tid`: 32-row pieces of each half in use
+  const int tid = threadIdx.x, lane = tid & 31, half_rows = P.rows / 2;
+  auto blocks_of = [&](int rows_left) {
+    return rows_left <= 0 ? 0 : (min(rows_left, half_rows) + 31) / 32;
+  };
+  int own = 0;
+  if (tid < kDecodeScheduleCtas) {
+    const SplitItem it = P.split[tid];
+    if (it.parts > 1) own = 2 * (blocks_of(it.n_rows) + blocks_of(it.n_rows - half_rows));
+  }
+  const int incl = warp_scan(own);
+  if (lane == 31) warp_sum_s[tid >> 5] = incl;
+  __syncthreads();
+  int base = 0, total = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < tid >> 5) base += warp_sum_s[w];
+    total += warp_sum_s[w];
+  }
+  before[tid] = base + incl - own;
+  __syncthreads();
+  for (int piece = blockIdx.x; piece < total; piece += kJoinBlocks) {
+    int lo = 0, hi = 256;  // before[lo] <= piece < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before[mid] <= piece) lo = mid; else hi = mid;
+    }
+    const SplitItem it = P.split[lo];
+    const int x = (piece - before[lo]) / 2, first = blocks_of(it.n_rows);
+    const int h = x >= first ? 1 : 0;
+    join_piece<D>(P, it, lo, h, (x - h * first) * 32, (piece - before[lo]) & 1, fac, rows, top_s,
+                  sum_s);
   }
 }
 
@@ -564,8 +632,9 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(kDecodeScheduleCtas, 8, 2);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P)) != cudaSuccess || !P.join_after)
+    return e;
+  cfg.gridDim = dim3(kJoinBlocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, P);
