@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
+  // (the next grid may not start early: its launch slows this one's last CTAs,
+  // which join parts, by more than its prologue takes)
   pdl_wait();
-  pdl_launch_dependents();
   // the tiles' memory holds the problems' sizes until the first load
   size_problems(P, reinterpret_cast<ProblemSize*>(smem));
   ptx::fence_proxy_async_smem();
