@@ -552,8 +552,9 @@ typedef struct {
  * Bytes of workspace lora_attn_paged (n_groups = 0) or lora_attn_prefix
  * (n_groups >= 1) needs for any batch of this size; 16 where the arguments
  * are out of range.  lora_kv_append needs the 16-byte error word only.
- * Zero-fill the workspace once; the calls leave its counters at zero.  After
- * LORA_DEVERR_TIMEOUT zero-fill it again.
+ * Zero-fill the workspace once; the calls leave its counters at zero, at one
+ * place whatever the batch, so calls of any sizes can share one that is large
+ * enough.  After LORA_DEVERR_TIMEOUT zero-fill it again.
  */
 size_t lora_attn_workspace_bytes(const lora_paged_kv_t* kv, int32_t n_q_heads, int32_t n_groups);
 

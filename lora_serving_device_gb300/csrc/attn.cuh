@@ -85,9 +85,9 @@ struct AttnParams {
   int n_q_heads;
   float scale_log2;    // scale * log2(e)
   int window, n_sink;
-  int max_row_tiles;   // row tiles that the counters are laid out for
   uint32_t* err;
-  uint32_t* count;     // arrivals per item (prefill: per half of one), zero between calls
+  uint32_t* count;     // [CTA][2] arrivals of the (halves of the) item that begins there
+                       // and ends in another; zero between calls
   float* part;         // [CTA][2][row tile] partial sums
   float* part_ml;      // [CTA][2][rows][2] their maxima (log2 units) and sums
   SplitItem* split;    // [CTA] the item that begins there and ends in another (prefill)
@@ -230,7 +230,6 @@ struct Segment {
   int table_row, tok0, base, k_lo;
   int shared;        // the rows have a prior part from the prefix phase
   RowTile t;
-  int item;          // its counter
   int cta0, parts;   // the CTAs that share the item: cta0 .. cta0 + parts - 1
   int tile0;         // key tiles of this CTA before the segment
   int once;          // no other CTA reads these key tiles
@@ -324,7 +323,6 @@ struct Walker {
   Problem pr;
   RowTile t;
   int prob, rt;      // the problem, and the row tile's number in it
-  int tile;          // and over all problems
   int u, begin, end; // next unit, the share's
   int total, share;  // units of the call, units of a CTA
   int tile_unit;     // first unit of the row tile
@@ -340,25 +338,24 @@ struct Walker {
     n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
     done = 0;
     // the sizes of all problems, then the equal share of a CTA
-    int64_t units = 0, tiles = 0;
+    int64_t units = 0, items = 0;
     for (int p0 = 0; p0 < n_prob; p0 += 32) {
       const LaneSize x = lane_sizes(P, sizes, p0, n_prob);
       units += x.units;
-      tiles += x.tiles;
+      items += x.tiles;
     }
     __syncwarp();
     units = warp_total(units) * hk;
-    tiles = warp_total(tiles);
-    // More row tiles than T allows (lengths out of order), or more units than a
-    // call could ever work off (2^31 of them read 10^14 bytes): refused.
-    const bool ok = tiles <= P.max_row_tiles && units <= INT32_MAX;
+    items = warp_total(items) * hk;
+    // more units than a call could ever work off (2^31 of them read 10^14
+    // bytes): refused
+    const bool ok = units <= INT32_MAX;
     if (!ok) flag_error(P.err, LORA_DEVERR_BAD_LEN);
     total = ok ? static_cast<int>(units) : 0;
     // Equal shares, but an item of a few key tiles is not worth splitting, nor
     // is less than four tiles worth a CTA.
-    const int items = ok ? static_cast<int>(tiles) * hk : 0;
-    const int even = (total + gridDim.x - 1) / gridDim.x;
-    const int span = items > 0 ? (total + items - 1) / items : 1;
+    const int even = static_cast<int>((static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x);
+    const int span = ok && items > 0 ? static_cast<int>((units + items - 1) / items) : 1;
     const int least = span <= 8 ? span : 4;
     share = even > least ? even : least;
     const int64_t first = static_cast<int64_t>(share) * blockIdx.x;
@@ -367,21 +364,18 @@ struct Walker {
     end = total - u < share ? total : u + share;
     if (u >= end) return;
     // the problem that unit u belongs to
-    tile = tile_unit = 0;
+    tile_unit = 0;
     for (int p0 = 0;; p0 += 32) {
       const LaneSize x = lane_sizes(P, sizes, p0, n_prob);
       const int own = static_cast<int>(x.units) * hk, incl = warp_scan(own);
-      const int t_incl = warp_scan(x.tiles);
       const uint32_t past = __ballot_sync(0xffffffffu, tile_unit + incl > u);
       if (past != 0) {
         const int k = __ffs(past) - 1;
         prob = p0 + k;
         tile_unit += __shfl_sync(0xffffffffu, incl - own, k);
-        tile += __shfl_sync(0xffffffffu, t_incl - x.tiles, k);
         break;
       }
       tile_unit += __shfl_sync(0xffffffffu, incl, 31);
-      tile += __shfl_sync(0xffffffffu, t_incl, 31);
     }
     pr = load_problem(P, prob);
     // the row tile in it, 32 at a time
@@ -401,13 +395,11 @@ struct Walker {
         tile_unit += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    tile += rt;
     t = row_tile(P, pr, rt);
   }
   // The next row tile; there is one while u is below the total.
   __device__ __forceinline__ void advance(const AttnParams& P) {
     tile_unit += units(P);
-    ++tile;
     ++rt;
     if (rt * P.rows >= pr.n_rows) {
       rt = 0;
@@ -450,7 +442,6 @@ struct Walker {
     g.k_lo = pr.k_lo;
     g.shared = pr.k_lo > 0 ? 1 : 0;
     g.t = t;
-    g.item = tile * P.kv.n_kv_heads + g.head;
     // (only key tiles make a CTA one of the item's)
     g.cta0 = blockIdx.x;
     g.parts = 1;

@@ -307,14 +307,15 @@ __device__ __forceinline__ int64_t part_slot(const Segment& g, int c) {
 
 // Threads of named barrier `bar` (cnt of them) have written this CTA's part:
 // is it the last of the item (or of its half)?  Leaves the counter at zero.
-__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, int counter,
+__device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segment& g, int half,
                                                bool leader, int* flag, int bar, int cnt) {
+  uint32_t* count = P.count + g.cta0 * 2 + half;
   __threadfence();
   named_bar(bar, cnt);
   if (leader) {
-    const uint32_t before = atomicAdd(&P.count[counter], 1u);
+    const uint32_t before = atomicAdd(count, 1u);
     *flag = before + 1 == static_cast<uint32_t>(g.parts) ? 1 : 0;
-    if (*flag) P.count[counter] = 0;
+    if (*flag) *count = 0;
     __threadfence();
   }
   named_bar(bar, cnt);

@@ -33,30 +33,23 @@ Shape shape_of(int64_t tokens, int group) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// The workspace: the error word, the counters (at one place for all batches, so
+// that batches can share a workspace), then what one call writes and reads.
 struct Layout {
   size_t count, split, part, part_ml, prior, prior_lse, bytes;
-  int max_row_tiles[2];  // sequences, groups
-  Shape shape[2];
+  Shape shape[2];  // sequences, groups
 };
 
 Layout layout(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
   Layout w;
   const int group = n_q_heads / kv.n_kv_heads;
-  const int64_t total = static_cast<int64_t>(kv.T) * group;
   w.shape[0] = shape_of(kv.max_q_len < kv.T ? kv.max_q_len : kv.T, group);
   w.shape[1] = shape_of(kv.T, group);
-  int64_t items = 0;
-  int space = 0;
-  for (int i = 0; i < (n_groups > 0 ? 2 : 1); ++i) {
-    const int64_t tiles = total / w.shape[i].rows + (i == 0 ? kv.n_seqs : n_groups);
-    w.max_row_tiles[i] = static_cast<int>(tiles);
-    const int64_t counters = w.shape[i].prefill ? 2 * tiles : tiles;
-    if (counters > items) items = counters;
-    if (w.shape[i].space > space) space = w.shape[i].space;
-  }
+  int space = w.shape[0].space;
+  if (n_groups > 0 && w.shape[1].space > space) space = w.shape[1].space;
   const size_t slots = static_cast<size_t>(kDecodeScheduleCtas) * 2 * space;
   w.count = 256;
-  w.split = up256(w.count + static_cast<size_t>(items) * kv.n_kv_heads * 4);
+  w.split = up256(w.count + kDecodeScheduleCtas * 2 * sizeof(uint32_t));
   w.part = up256(w.split + kDecodeScheduleCtas * sizeof(SplitItem));
   w.part_ml = w.part + slots * kv.head_dim * 4;
   w.prior = up256(w.part_ml + slots * 8);
@@ -130,7 +123,6 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.prior_lse = reinterpret_cast<float*>(base + w.prior_lse);
   for (int phase = a.n_groups > 0 ? 1 : 0; phase >= 0; --phase) {
     P.groups_phase = phase == 1;
-    P.max_row_tiles = w.max_row_tiles[phase];
     P.rows = w.shape[phase].rows;
     P.by_rows = FastDiv::of(P.rows);
     P.over = w.shape[phase].prefill ? 3 : 1;

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
           const float4 r = red[n];
           if (k == 0) ml[slot * A + n] = make_float2(M.m[wg][n], r.x + r.y + r.z + r.w);
         }
-        write = last_to_arrive(P, g, g.item, st_tid == 0, &M.last[wg], kBar, 128);
+        write = last_to_arrive(P, g, 0, st_tid == 0, &M.last[wg], kBar, 128);
       }
 #pragma unroll 1
       for (int x = write ? st_tid : vectors; x < vectors; x += 128) {

@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ml[slot * 2 * kHalf] = make_float2(m, l);
       }
       if (!P.join_after &&
-          last_to_arrive(P, g, g.item * 2 + h, row == 0, &M.last[h], bar, 128) && mine) {
+          last_to_arrive(P, g, h, row == 0, &M.last[h], bar, 128) && mine) {
         // few parts: the last to arrive adds them up, in their order
         float top = -INFINITY, sum = 0.f;
 #pragma unroll 4

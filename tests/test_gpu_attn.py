@@ -363,6 +363,27 @@ def test_prefix_longer_than_a_context_is_reported(L):
     assert np.all(np.abs(got - ref)[:2] <= U * np.abs(ref[:2]) + (U + 2.0 ** -12) * wv[:2])
 
 
+def test_one_workspace_for_batches_of_all_sizes(L):
+    import torch
+    cases = [Case([1], [900], 8, 1, 64, 16, seed=1), Case([300], [200], 8, 2, 128, 16, seed=2),
+             Case([1] * 70, [9 * i for i in range(70)], 4, 2, 64, 32, seed=3),
+             Case([3, 50], [700, 100], 16, 2, 128, 16, seed=4, window=60, n_sink=3)]
+    groups = ([0, 40], [300])
+    shared = Case([1] * 40, [300 + i for i in range(40)], 8, 2, 128, 16, seed=5, groups=groups)
+    off, pl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in groups)
+    ws = torch.zeros(max([L.attn_workspace(shared.kv(L), 8, 1).numel()] +
+                         [L.attn_workspace(c.kv(L), c.hq).numel() for c in cases]), dtype=torch.uint8, device="cuda")
+    ws[4096:].fill_(0xFF)     # whatever earlier calls left behind the counters
+    for _ in range(2):
+        for c in cases + [shared] + cases[::-1]:
+            if c is shared:
+                L.attn_prefix_t(c.kv(L), c.q, off, pl, ws, out=c.out)
+            else:
+                L.attn_paged_t(c.kv(L), c.q, ws, window=c.window, n_sink=c.n_sink, out=c.out)
+            c.check(c.out)
+    assert L.get_error_t(ws) == 0
+
+
 # ------------------------------------------------------------------ append
 
 def table_rows(torch, rng, n_pos, rot):
