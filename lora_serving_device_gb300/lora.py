@@ -9,6 +9,7 @@ fallback: if the library is missing or the device is not sm_103, calls fail.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora.so")
@@ -642,7 +643,8 @@ class PagedKV:
                                     block_table.shape[1], T, T if max_q_len is None else max_q_len)
         self.ref = ctypes.addressof(self.struct)
         self._device = k_cache.get_device()
-        self._bf16, self._empty, self._torch_device = torch.bfloat16, torch.empty, k_cache.device
+        self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self.new_like = torch.empty_like
         self._current_stream = torch._C._cuda_getCurrentRawStream
 
     def rows(self, x, n_heads, what):
@@ -656,9 +658,6 @@ class PagedKV:
             raise ValueError(f"{what}: shape {tuple(x.shape)}, strides {st} on {x.device}; need [{T}, {heads}, "
                              f"{d}] with the heads of a token contiguous, on the cache's device")
         return st[0] if T > 1 else heads * d
-
-    def empty_like(self, x):
-        return self._empty(x.shape, dtype=self._bf16, device=self._torch_device)
 
     def stream(self, stream):
         return self._current_stream(self._device) if stream is None else stream.cuda_stream
@@ -681,6 +680,11 @@ def rope_table(n_pos, rot_dim, base=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+@functools.lru_cache(maxsize=64)
+def _c_counts(counts):
+    return (ctypes.c_int32 * len(counts))(*counts)
+
+
 def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
                 stream=None):
     """Rotates q [T, n_q_heads, D] and k [T, n_kv_heads, D] by position, writes k and v into
@@ -693,26 +697,26 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
         n_q = q.shape[1]
         q_stride = kv.rows(q, n_q, "q")
         if q_out is None:
-            q_out = kv.empty_like(q)
+            q_out = kv.new_like(q)
             q_out_stride = n_q * kv.head_dim
         else:
             q_out_stride = kv.rows(q_out, n_q, "q_out")
     n_pos = rot = 0
     if cos_sin is not None:
         n_pos, rot = cos_sin.shape
-        if cos_sin.element_size() != 4 or not cos_sin.is_floating_point() or not cos_sin.is_contiguous() or \
-                cos_sin.get_device() != kv._device:
+        if cos_sin.dtype is not kv._f32 or not cos_sin.is_contiguous() or cos_sin.get_device() != kv._device:
             raise TypeError("cos_sin: contiguous fp32 [n_pos, rot_dim] on the cache's device")
     n_axes, pairs = 1, None
     if pos is not None:
-        n_axes = pos.shape[0] if pos.dim() == 2 else 1
-        if pos.element_size() != 4 or pos.is_floating_point() or not pos.is_contiguous() or \
-                pos.shape[-1] != kv.T or pos.get_device() != kv._device:
+        shape = pos.shape
+        n_axes = shape[0] if len(shape) == 2 else 1
+        if shape[-1] != kv.T or pos.dtype is not kv._i32 or not pos.is_contiguous() or \
+                pos.get_device() != kv._device:
             raise TypeError(f"pos: contiguous int32 [{kv.T}] or [n_axes, {kv.T}] on the cache's device")
     if axis_pairs is not None:
         if len(axis_pairs) != n_axes:
             raise ValueError(f"axis_pairs: {len(axis_pairs)} counts for {n_axes} axes")
-        pairs = (ctypes.c_int32 * n_axes)(*axis_pairs)
+        pairs = _c_counts(tuple(axis_pairs))
     hk = kv.n_kv_heads
     check(load().lora_kv_append(kv.ref, _ptr(q), q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(),
                                 kv.rows(v, hk, "v"), n_q, _ptr(cos_sin), n_pos, rot, _ptr(pos), n_axes, pairs,
@@ -727,7 +731,7 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
     n_q = q.shape[1]
     q_stride = kv.rows(q, n_q, "q")
     if out is None:
-        out = kv.empty_like(q)
+        out = kv.new_like(q)
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")
@@ -745,11 +749,10 @@ def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream
     q_stride = kv.rows(q, n_q, "q")
     n_groups = prefix_len.numel()
     for name, t, n in (("group_off", group_off, n_groups + 1), ("prefix_len", prefix_len, n_groups)):
-        if t.element_size() != 4 or t.is_floating_point() or t.numel() != n or not t.is_contiguous() or \
-                t.get_device() != kv._device:
+        if t.dtype is not kv._i32 or t.numel() != n or not t.is_contiguous() or t.get_device() != kv._device:
             raise TypeError(f"{name}: contiguous int32 [{n}] on the cache's device")
     if out is None:
-        out = kv.empty_like(q)
+        out = kv.new_like(q)
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")
