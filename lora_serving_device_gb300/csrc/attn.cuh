@@ -10,8 +10,9 @@
 // cost of taking it up and finishing it.  All units, numbered row tile by row
 // tile, key head by key head, are cut into equal contiguous shares, one per
 // CTA, whatever the lengths are (they live on the device).  An item that
-// several CTAs share (short ones are not shared) is finished by the last of them to arrive, which adds
-// their parts in CTA order: the result is a function of the lengths alone.
+// several CTAs share (short ones are not shared) is finished by the last of
+// them to arrive, or by a kernel after them; either adds the parts in CTA
+// order, so the result is a function of the lengths alone.
 // Each CTA finds its share itself: its threads size a problem each, and one
 // warp adds the sizes up and looks for its place.
 #pragma once

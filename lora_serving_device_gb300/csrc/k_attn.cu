@@ -16,9 +16,13 @@ cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k
 namespace {
 
 // The kernel of a phase, by the rows of a key head that the longest run of
-// new tokens has: up to 32 the keys stand in the MMA's M and the rows (4, 8,
-// 16 or 32 of them) in N; above, the rows stand in M, in two halves of whole
-// tokens.
+// new tokens has: up to 16 the keys stand in the MMA's M and the rows (4, 8 or
+// 16 of them) in N; above, the rows stand in M, in two halves of whole tokens.
+// Measured with 24 rows on ~3000 keys (8 key heads of 128), rows in N with room
+// for 32 against rows in M: 1 sequence 25.7 : 19.8 us, 8 sequences 36.2 : 33.1
+// us, 64 sequences 137.7 : 141.1 us; with 40 rows 24.6 : 20.2, 47.2 : 32.0 and
+// 242.8 : 135.2 us.  (A key head of more than 128 query heads does not fit a
+// half: its rows are cut into tiles of 16.)
 struct Shape {
   bool prefill;
   int rows;   // of a row tile
@@ -26,8 +30,8 @@ struct Shape {
 };
 Shape shape_of(int64_t tokens, int group) {
   const int64_t rows = (tokens > 1 ? tokens : 1) * group;
-  if (rows > 32 && group <= 128) return {true, 2 * (128 / group) * group, 256};
-  const int n = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  if (rows > 16 && group <= 128) return {true, 2 * (128 / group) * group, 256};
+  const int n = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   return {false, n, n};
 }
 
@@ -125,10 +129,20 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.groups_phase = phase == 1;
     P.rows = w.shape[phase].rows;
     P.by_rows = FastDiv::of(P.rows);
+    // Beside its key tiles an item costs its first scores and its results: in the
+    // prefill kernel as much as three tiles (6 against 1.4 us; 2 to 6 units
+    // differ by 2%), in the other, where a second warpgroup is at work, one.
+    // Splitting an item costs each of its CTAs a part, so short ones stay whole:
+    // up to 8 tiles of single tokens (the tokens after a prefix of 8K: 56.5 us,
+    // split 59.8), two of prompts.
     P.over = w.shape[phase].prefill ? 3 : 1;
     P.whole = w.shape[phase].prefill ? 2 : 8;
-    // the fewest items that this many rows can make: at 38 and more one has six
-    // parts at most, if the others are as long
+    // By the fewest items that this many rows can make: with 38 and more one has
+    // a few parts, which the last CTA to arrive adds up; fewer items have many
+    // parts, 128 KB each, more than one SM reads in good time.  In the kernel
+    // against by a kernel of its own: prompt of 4096 (512 items) 123.5 : 141.1 us,
+    // 60 rows on 30000 (8 items) 65.4 : 41.7 us, prefix of 8K (8 items) 70.7 :
+    // 50.6 us.
     P.join_after = static_cast<int64_t>(kv.T) * P.group / P.rows * kv.n_kv_heads < 38;
     cudaError_t e;
     if (w.shape[phase].prefill) {

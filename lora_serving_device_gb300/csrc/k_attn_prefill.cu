@@ -20,6 +20,14 @@
 // query head of the key head), so all query heads of a key head share each
 // K and V tile; a half holds whole tokens, which lets TMA fetch Q too.
 //
+// Measured: a prompt of 8192, 32 / 8 heads of 128: 357 us, 1540 TFLOP/s (0.79 of
+// the measured burst rate; 385 us when the card is under load for long); the
+// tensor pipe is active for 67% of the cycles, the exponentials' for 34%.  What
+// is left is the way from scores to weights and back: S and P share tensor
+// memory, which the two halves' S and O fill, so a half's next scores wait for
+// its last product.  P handed over as a whole costs 3%, in quarters 6%, after
+// three quarters 4%; two threads to a row, with a vote a tile, 14%.
+//
 // Warps: 0-3 softmax of half 0, 4-7 of half 1 (and their results), 8 schedule
 // and TMA, 9 MMA issue.  Every wait is bounded; on timeout the kernel raises
 // LORA_DEVERR_TIMEOUT.

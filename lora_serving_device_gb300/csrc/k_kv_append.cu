@@ -9,8 +9,11 @@
 // in the half form, neighbours in the interleaved form and past rot_dim) and
 // walks the heads with it, so the table's 16 values are loaded once for all
 // its heads and every access is 16 bytes wide.  The loads of kBatch heads are
-// in flight before the first is used; the lookups of the sequence, position
-// and page run beside them.
+// in flight first; the lookups of the sequence, position and page, which they
+// do not need, run beside them.
+// Measured: a prompt of 8192, 32 / 8 heads of 128: 33.3 us, 6.2 TB/s of 6.69;
+// 5238 tokens with 28 / 4 heads and three axes: 21.4 us, 4.6 TB/s (two heads a
+// batch, for registers: four 23.0 us); 64 tokens 3.5 us.
 #include "attn.cuh"
 
 namespace lora {
