@@ -80,6 +80,7 @@ struct AttnParams {
   int rows;            // rows of a row tile
   FastDiv by_group, by_rows;
   int lg_page;         // log2 of the page size
+  int box;             // rows of a page that are loaded at once
   int over;            // units that an item costs beside its key tiles
   int whole;           // items of up to that many key tiles are not split
   bool join_after;     // parts are joined by a kernel of their own (prefill)
@@ -105,12 +106,14 @@ struct Problem {
 };
 
 // One row tile's view.  Keys [vis_lo, vis_hi] and the first n_sink are those
-// that some row sees; key tile i of n_tiles is i < sink_tiles ? i : tile_lo +
-// i - sink_tiles.  n_tiles >= 1 unless the row tile has nothing to write.
+// that some row sees.  Its key tiles run over them closed up, in whole boxes:
+// place v is key v below sink_places and key origin + v - sink_places from there
+// on, tile i is places [128 i, 128 i + 128).  n_tiles >= 1 unless the row tile
+// has nothing to write.
 struct RowTile {
   int row0, n_rows;
   int vis_lo, vis_hi, n_sink;
-  int tile_lo, sink_tiles, n_tiles;
+  int sink_places, origin, n_tiles;
 };
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
@@ -203,7 +206,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams& P, const Problem& 
   if (P.groups_phase) {
     t.vis_lo = 0;
     t.vis_hi = pr.k_hi - 1;
-    t.n_sink = t.sink_tiles = t.tile_lo = 0;
+    t.n_sink = t.sink_places = t.origin = 0;
     t.n_tiles = (pr.k_hi + kKeys - 1) / kKeys;
     return t;
   }
@@ -212,15 +215,18 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams& P, const Problem& 
   t.vis_lo = P.window > 0 ? max(first - P.window + 1, 0) : 0;
   t.vis_lo = max(t.vis_lo, pr.k_lo);
   t.n_sink = P.window > 0 ? max(min(P.n_sink, t.vis_hi + 1), 0) : 0;
-  t.tile_lo = t.vis_lo / kKeys;
-  t.sink_tiles = min((t.n_sink + kKeys - 1) / kKeys, t.tile_lo);
-  t.n_tiles = t.sink_tiles + (t.vis_hi >= t.vis_lo ? t.vis_hi / kKeys - t.tile_lo + 1 : 0);
+  t.sink_places = (t.n_sink + P.box - 1) & -P.box;
+  t.origin = t.vis_lo & -P.box;
+  if (t.sink_places > t.origin) t.sink_places = t.origin = 0;  // they meet: one run from key 0
+  t.n_tiles = (t.sink_places + max(t.vis_hi - t.origin + 1, 0) + kKeys - 1) / kKeys;
   if (t.n_tiles < 1) t.n_tiles = 1;
   return t;
 }
 
-__device__ __forceinline__ int key_tile(const RowTile& t, int i) {
-  return i < t.sink_tiles ? i : t.tile_lo + i - t.sink_tiles;
+// The key at place v, if v is not one of the first tokens' places (there it is
+// below origin, and so below what any row's window begins with).
+__device__ __forceinline__ int window_key(const RowTile& t, int v) {
+  return t.origin + v - t.sink_places;
 }
 
 // What a CTA does next: key tiles [tile0, tile0 + n) of an item.

@@ -111,21 +111,23 @@ struct Patience {
   }
 };
 
-__device__ __forceinline__ bool tile_key_seen(const RowTile& t, int key) {
-  return (key >= t.vis_lo && key <= t.vis_hi) || key < t.n_sink;
+// Whether some row sees the key at place v.
+__device__ __forceinline__ bool place_seen(const RowTile& t, int v) {
+  const int key = window_key(t, v);
+  return (key >= t.vis_lo && key <= t.vis_hi) || v < t.n_sink;
 }
 
 // Whether a key tile holds keys that no row of the row tile sees.
-__device__ __forceinline__ bool tile_has_unseen(const RowTile& t, int key0) {
-  return key0 < t.vis_lo || key0 + kKeys - 1 > t.vis_hi;
+__device__ __forceinline__ bool tile_has_unseen(const RowTile& t, int v0) {
+  return window_key(t, v0) < t.vis_lo || window_key(t, v0 + kKeys - 1) > t.vis_hi;
 }
 // The values of key `j` of such a tile are made zero in shared memory if no row
 // sees the key (its weights are zero, but 0 * NaN is not): rows of the cache
 // past the length or before the window, and what was not loaded at all.  V as
 // the tensor map lays it out; the caller fences before the MMA reads it.
 template <int D>
-__device__ __forceinline__ void zero_unseen_value(const RowTile& t, int key0, int j, uint8_t* V) {
-  if (tile_key_seen(t, key0 + j)) return;
+__device__ __forceinline__ void zero_unseen_value(const RowTile& t, int v0, int j, uint8_t* V) {
+  if (place_seen(t, v0 + j)) return;
   uint8_t* row = V + (j / 8) * (D / 64) * 1024 + (j % 8) * 128;
   // (each lane starts elsewhere in its 128 bytes: the rows lie 128 bytes apart)
 #pragma unroll
@@ -179,19 +181,24 @@ struct TileLoader {
   __device__ __forceinline__ explicit TileLoader(const AttnParams& P)
       : page(P.kv.page_size),
         lg_page(P.lg_page),
-        box(page < kKeys ? page : kKeys),
+        box(P.box),
         boxes(kKeys / box),
         per(32 / boxes) {}
   // This lane's box of the batch from tile i0: its page's id as the table has
   // it (a load that nothing here waits for), and where it starts.
-  __device__ __forceinline__ int first_key(const Segment& g, int i0) const {
+  __device__ __forceinline__ int first_place(const Segment& g, int i0) const {
     const int lane = threadIdx.x & 31;
-    return key_tile(g.t, g.first + i0 + lane / boxes) * kKeys + (lane & (boxes - 1)) * box;
+    return (g.first + i0 + lane / boxes) * kKeys + (lane & (boxes - 1)) * box;
+  }
+  __device__ __forceinline__ int first_key(const Segment& g, int i0) const {
+    const int v = first_place(g, i0);
+    return v < g.t.sink_places ? v : window_key(g.t, v);
   }
   __device__ __forceinline__ int fetch(const AttnParams& P, const Segment& g, int i0) const {
     const int key0 = first_key(g, i0);
     const bool seen = i0 + (threadIdx.x & 31) / boxes < g.n &&
-                      ((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) || key0 < g.t.n_sink);
+                      ((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) ||
+                       first_place(g, i0) < g.t.n_sink);
     return seen ? P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages +
                                    (key0 >> lg_page)]
                 : INT32_MIN;

@@ -115,6 +115,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.by_group = FastDiv::of(P.group);
   P.n_q_heads = a.n_q_heads;
   P.lg_page = 31 - __builtin_clz(static_cast<unsigned>(kv.page_size));
+  P.box = kv.page_size < kKeys ? kv.page_size : kKeys;
   P.scale_log2 = a.scale * 1.4426950408889634f;
   P.window = a.window;
   P.n_sink = a.n_sink;

@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
 
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++tile) {
-        const int key0 = key_tile(g.t, g.first + i) * kKeys, key = key0 + j;
+        const int v0 = (g.first + i) * kKeys, v = v0 + j;  // places
+        const int key0 = window_key(g.t, v0), key = key0 + j;
         const uint32_t in_cta = g.tile0 + i;
         wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
         __syncwarp();
@@ -360,9 +361,10 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         if (key0 < max_lo || key0 + kKeys - 1 > min_hi) {
 #pragma unroll
           for (int n = 0; n < A; ++n)
-            s[n] = (key > M.row_hi[wg][n]) | ((key < M.row_lo[wg][n]) & (key >= g.t.n_sink))
-                       ? -INFINITY
-                       : s[n];
+            s[n] = ((key <= M.row_hi[wg][n]) & (key >= M.row_lo[wg][n])) |
+                           ((v < g.t.n_sink) & (v <= M.row_hi[wg][n]))
+                       ? s[n]
+                       : -INFINITY;
         }
         // does a score exceed its reference maximum by more than 8?
         bool up = false;
@@ -403,9 +405,9 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
             ptx::tc_fence_before();
           }
         }
-        if (tile_has_unseen(g.t, key0)) {
+        if (tile_has_unseen(g.t, v0)) {
           wait_quiet(&M.full_v[in_cta % kStages], (in_cta / kStages) & 1, abort_f);
-          zero_unseen_value<D>(g.t, key0, j, smem + (in_cta % kStages) * La::kStage + La::kTile);
+          zero_unseen_value<D>(g.t, v0, j, smem + (in_cta % kStages) * La::kStage + La::kTile);
         }
         // P's buffer is free once the product that read it is done
         if (tile >= PB) wait_quiet(&p_done[tile % PB], ((tile / PB) & 1) ^ 1, abort_f);

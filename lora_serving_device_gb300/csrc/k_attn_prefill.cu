@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++tile) {
-        const int key0 = key_tile(g.t, g.first + i) * kKeys;
+        const int v0 = (g.first + i) * kKeys, key0 = window_key(g.t, v0);  // place, key
         wait_quiet(&M.s_full[h], tile & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
@@ -347,11 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
         ptx::tmem_ld_wait();
         if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) {
-          // a bit per key: up to hi, and from lo or below the first tokens' end
+          // a bit per key: from lo to hi, or one of the first tokens
+          const int first = min(g.t.n_sink, hi + 1) - v0;
 #pragma unroll
           for (int k = 0; k < kKeys; k += 32) {
-            const uint32_t seen = low_bits(hi + 1 - key0 - k) &
-                                  (~low_bits(lo - key0 - k) | low_bits(g.t.n_sink - key0 - k));
+            const uint32_t seen = (low_bits(hi + 1 - key0 - k) & ~low_bits(lo - key0 - k)) |
+                                  low_bits(first - k);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (!(seen & (1u << x))) s[k + x] = -INFINITY;
@@ -390,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (h == 0 && tile_has_unseen(g.t, key0)) {
+        if (h == 0 && tile_has_unseen(g.t, v0)) {
           // (half 0 takes part in every tile, and its P V is issued first)
           const int k = 2 * tile + 1;
           wait_quiet(&M.full[k % kSlots], (k / kSlots) & 1, abort_f);
-          zero_unseen_value<D>(g.t, key0, row, smem + (k % kSlots) * La::kTile);
+          zero_unseen_value<D>(g.t, v0, row, smem + (k % kSlots) * La::kTile);
           ptx::fence_proxy_async_smem();
         }
         const float neg = m == -INFINITY ? 0.f : -m;

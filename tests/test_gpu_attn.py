@@ -177,6 +177,16 @@ def test_windows_and_first_tokens(L, window, n_sink, d):
     attend(L, Case([150, 1, 30, 0], [0, 450, 333, 8], 4, 2, d, 16, seed=window, window=window, n_sink=n_sink))
 
 
+@pytest.mark.parametrize("d,page,n_sink", [(128, 32, 33), (64, 64, 4), (128, 128, 128), (64, 256, 5)])
+def test_windows_that_move_over_pages(L, d, page, n_sink):
+    # the window's first key at, before and after a page's first, and where its
+    # pages reach those of the first tokens
+    n = [150, 159, 160, 161, 287, 288, 289, 415, 416, 417, 543, 545]
+    attend(L, Case([1] * len(n), [x - 1 for x in n], 8, 1, d, page, seed=page, window=32, n_sink=n_sink))
+    attend(L, Case([40, 1, 200, 3], [x - 40 for x in (289, 545, 700, 161)], 8, 1, d, page, seed=n_sink,
+                   window=129, n_sink=n_sink))
+
+
 def test_rows_that_see_nothing(L):
     # kv_len below the number of new tokens: the first rows lie before position 0
     c = Case([3, 1, 2, 140], [0, -1, -2, -20], 4, 2, 64, 16, seed=5)
