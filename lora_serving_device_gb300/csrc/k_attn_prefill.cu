@@ -41,10 +41,10 @@ namespace lora {
 namespace {
 
 // Three warpgroups: the softmax threads hold a row of 128 scores each and take
-// registers from the third, of which two warps work.  208 x 256 + 88 x 128 is
+// registers from the third, of which two warps work.  192 x 256 + 120 x 128 is
 // within the launch's 168 x 384.
 constexpr int kThreads = 384;
-constexpr int kRegsMost = 208, kRegsLeast = 88;
+constexpr int kRegsMost = 192, kRegsLeast = 120;
 constexpr int kRing = 4;     // segments that the producer may run ahead
 constexpr int kHalf = 128;   // rows of a half in the MMA
 
