@@ -41,12 +41,25 @@ __device__ __forceinline__ bool named_any(int id, int n, bool x) {
       : "memory");
   return r != 0;
 }
-// Every lane waits (and so sees what the barrier orders); the same answer in
-// all of them.  Once a wait of the CTA gave up the others return at once.
+// Once a wait of the CTA gave up, the others return at once.  One loop of few
+// instructions: the roles' loops run side by side, and what they take together
+// has to fit the instruction caches (with the loop doubled, a quick one before
+// one that minds the clock, prompts are slower by 3 to 10%).
+__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint32_t n = 0, t0 = 0;
+#pragma unroll 1
+  while (!ptx::mbar_try_wait(bar, parity) && !*abort) {
+    if ((++n & 4095u) != 0u) continue;
+    const uint32_t now = static_cast<uint32_t>(ptx::globaltimer_ns() >> 10);
+    if (n == 4096u) t0 = now;
+    if (now - t0 > static_cast<uint32_t>(kAttnWaitNs >> 10)) *abort = 1;
+  }
+}
+// Every lane waits (and so sees what the barrier orders); false, in all of
+// them, once a wait of the CTA gave up.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = ptx::mbar_test_wait(bar, parity) ||
-                  (!*abort && ptx::mbar_wait_bounded(bar, parity, abort, kAttnWaitNs));
-  return __all_sync(0xffffffffu, ok);
+  wait_quiet(bar, parity, abort);
+  return __all_sync(0xffffffffu, *abort == 0);
 }
 // One lane of a converged warp, in a form the compiler knows to be one thread.
 // A loop that runs wholly inside such a branch issues an MMA in ~20 cycles; in
@@ -89,12 +102,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
       "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// The same without a vote, where no lane acts on the answer: once a wait of the
-// CTA gave up it returns at once.
-__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (!ptx::mbar_try_wait(bar, parity) && !*abort)
-    ptx::mbar_wait_bounded(bar, parity, abort, kAttnWaitNs);
 }
 // Bounds one thread's polling loop in time: out() after each fruitless round.
 struct Patience {

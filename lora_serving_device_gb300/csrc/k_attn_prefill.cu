@@ -20,13 +20,16 @@
 // query head of the key head), so all query heads of a key head share each
 // K and V tile; a half holds whole tokens, which lets TMA fetch Q too.
 //
-// Measured: a prompt of 8192, 32 / 8 heads of 128: 357 us, 1540 TFLOP/s (0.79 of
-// the measured burst rate; 385 us when the card is under load for long); the
+// Measured: a prompt of 8192, 32 / 8 heads of 128: 345 us, 1590 TFLOP/s (0.82 of
+// the measured burst rate; 370 us when the card is under load for long); the
 // tensor pipe is active for 67% of the cycles, the exponentials' for 34%.  What
 // is left is the way from scores to weights and back: S and P share tensor
 // memory, which the two halves' S and O fill, so a half's next scores wait for
 // its last product.  P handed over as a whole costs 3%, in quarters 6%, after
 // three quarters 4%; two threads to a row, with a vote a tile, 14%.
+// The roles' loops are kept short.  With more instructions in them one issue in
+// six waited for its instruction: chunks with a window of 1024 took 140 us where
+// they take 121, a prompt of 4000, 64 values a head, 182 where it takes 160.
 //
 // Warps: 0-3 softmax of half 0, 4-7 of half 1 (and their results), 8 schedule
 // and TMA, 9 MMA issue.  Every wait is bounded; on timeout the kernel raises
@@ -234,10 +237,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the tensor cores have the other half's work while a softmax runs.
     if (elect_one()) {
       const uint32_t slots = desc_lo(ptx::smem_u32(smem), 0);
-      uint32_t segs[2] = {0, 0};   // segments of each half so far
-      uint32_t tiles[2] = {0, 0};  // tiles of each half whose P V was issued
+      // A bit for each half: parities of its Qs, of its tiles' P and of its O, and
+      // whether it has had a segment.
+      uint32_t q_par = 0, p_par = 0, o_par = 0, begun = 0;
       auto issue_qk = [&](bool first, bool last, int n, int h, bool frees) {
-        if (first) wait_quiet(&M.q_full[h], segs[h]++ & 1, abort_f);
+        if (first) {
+          wait_quiet(&M.q_full[h], (q_par >> h) & 1, abort_f);
+          q_par ^= 1u << h;
+        }
         const int k = 2 * n, st = k % kSlots;
         wait_quiet(&M.full[st], (k / kSlots) & 1, abort_f);
         ptx::tc_fence_after();
@@ -256,11 +263,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k = 2 * n + 1, st = k % kSlots;
         const uint32_t va = slots + st * (La::kTile / 16) + ((1024u / 16) << 16);
         if (h == 0) wait_quiet(&M.full[st], (k / kSlots) & 1, abort_f);
-        // the half's previous segment has been read out of O
-        if (first && segs[h] > 1) wait_quiet(&M.o_empty[h], segs[h] & 1, abort_f);
+        if (first) {
+          // the half's previous segment has been read out of O
+          if ((begun >> h) & 1) {
+            wait_quiet(&M.o_empty[h], (o_par >> h) & 1, abort_f);
+            o_par ^= 1u << h;
+          }
+          begun |= 1u << h;
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          wait_quiet(x ? &M.p_full[h] : &M.p_half[h], tiles[h] & 1, abort_f);
+          wait_quiet(x ? &M.p_full[h] : &M.p_half[h], (p_par >> h) & 1, abort_f);
           ptx::tc_fence_after();
 #pragma unroll
           for (int ks = 4 * x; ks < 4 * x + 4; ++ks)
@@ -270,32 +283,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mma_commit(&M.o_done[h]);
         if (frees) ptx::mma_commit(&M.empty[st]);
-        ++tiles[h];
+        p_par ^= 1u << h;
       };
-      wait_quiet(&M.seg_full[0], 0, abort_f);
-      int sg = 0, left = M.ring[0].n;  // this segment's key tiles to go
-      bool two = M.ring[0].t.n_rows > half_rows, first = true;
-      if (left > 0) {
-        issue_qk(true, left == 1, 0, 0, !two);
-        if (two) issue_qk(true, left == 1, 0, 1, true);
-      }
-      for (int n = 0; left > 0 && !*abort_f; ++n) {
+      int sg = -1, left = 0;  // the segment of tile n, and its key tiles to go
+      bool two = false, first = false;
+#pragma unroll 1
+      for (int n = -1; !*abort_f; ++n) {
         int next = left - 1;
         bool next_two = two, next_first = false;
-        if (next == 0) {  // the next tile is of the next segment
+        if (next <= 0) {  // the next tile is of the next segment
           wait_quiet(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
           next = M.ring[(sg + 1) % kRing].n;
           next_two = M.ring[(sg + 1) % kRing].t.n_rows > half_rows;
           next_first = true;
         }
-        issue_pv(first, n, 0, !two);
-        if (next > 0) issue_qk(next_first, next == 1, n + 1, 0, !next_two);
-        if (two) issue_pv(first, n, 1, true);
-        if (next > 0 && next_two) issue_qk(next_first, next == 1, n + 1, 1, true);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (left > 0 && h <= two) issue_pv(first, n, h, h == two);
+          if (next > 0 && h <= next_two) issue_qk(next_first, next == 1, n + 1, h, h == next_two);
+        }
         if (next_first) {
-          ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+          if (sg >= 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
           ++sg;
         }
+        if (next <= 0) break;
         left = next;
         two = next_two;
         first = next_first;
@@ -347,16 +358,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
         ptx::tmem_ld_wait();
         if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) {
-          // a bit per key: from lo to hi, or one of the first tokens
+          // A bit per key: from lo to hi, or one of the first tokens.  The scores
+          // are changed in tensor memory, by a loop, and read again: changing
+          // them in registers takes 5 KB of instructions (prompt of 4000, 64
+          // values a head: 182 : 167 us).
           const int first = min(g.t.n_sink, hi + 1) - v0;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < kKeys; k += 32) {
             const uint32_t seen = (low_bits(hi + 1 - key0 - k) & ~low_bits(lo - key0 - k)) |
                                   low_bits(first - k);
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+            uint32_t x[32];
+            ptx::tmem_ld32(tm_s + k, x);
+            ptx::tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!(seen & (1u << x))) s[k + x] = -INFINITY;
+            for (int y = 0; y < 32; ++y)
+              if (!(seen & (1u << y))) x[y] = 0xff800000u;  // -infinity
+            ptx::tmem_st32(tm_s + k, x);
           }
+          ptx::tmem_st_wait();
+#pragma unroll
+          for (int k = 0; k < kKeys; k += 32)
+            ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
+          ptx::tmem_ld_wait();
         }
         float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
         float mz = max3(s[6], s[7], s[8]), mw = max3(s[9], s[10], s[11]);
