@@ -460,24 +460,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
       __syncwarp();
       ptx::tc_fence_after();
+      auto read = [&] {  // O has been read
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&M.o_empty[h]);
+          ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+        }
+      };
+      if (g.parts == 1) {
+        // (rolled, for the instructions' sake: chunks with a window of 1024 117 us,
+        // unrolled 121)
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+          float o[16];
+          ptx::tmem_ld16(tm_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
+          ptx::tmem_ld_wait();
+          if (mine) out.write16(k, o);
+        }
+        read();
+        continue;
+      }
       float o[D];
 #pragma unroll
       for (int k = 0; k < D; k += 32)
         ptx::tmem_ld32(tm_o + k, *reinterpret_cast<uint32_t(*)[32]>(o + k));
       ptx::tmem_ld_wait();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(&M.o_empty[h]);
-        ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
-      }
-      if (g.parts == 1) {
-        if (mine) {
-#pragma unroll
-          for (int k = 0; k < D; k += 16) out.write16(k, o + k);
-        }
-        continue;
-      }
+      read();
       float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
       if (mine) {
         float4* part = part_row<D>(P, slot, h, row);
