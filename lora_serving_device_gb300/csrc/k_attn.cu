@@ -131,8 +131,8 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.rows = w.shape[phase].rows;
     P.by_rows = FastDiv::of(P.rows);
     // Beside its key tiles an item costs its first scores and its results: in the
-    // prefill kernel as much as three tiles (6 against 1.4 us; 2 to 6 units
-    // differ by 2%), in the other, where a second warpgroup is at work, one.
+    // prefill kernel as much as three tiles (prompt of 8192: 346 us; 2, 4 and 5
+    // units 352, 349 and 355), in the other, where a second warpgroup is at work, one.
     // Splitting an item costs each of its CTAs a part, so short ones stay whole:
     // up to 8 tiles of single tokens (the tokens after a prefix of 8K: 56.5 us,
     // split 59.8), two of prompts.

@@ -22,14 +22,15 @@
 //
 // Measured: a prompt of 8192, 32 / 8 heads of 128: 345 us, 1590 TFLOP/s (0.82 of
 // the measured burst rate; 370 us when the card is under load for long); the
-// tensor pipe is active for 67% of the cycles, the exponentials' for 34%.  What
+// tensor pipe is active for 69% of the cycles, the exponentials' for 35%.  What
 // is left is the way from scores to weights and back: S and P share tensor
 // memory, which the two halves' S and O fill, so a half's next scores wait for
 // its last product.  P handed over as a whole costs 3%, in quarters 6%, after
 // three quarters 4%; two threads to a row, with a vote a tile, 14%.
-// The roles' loops are kept short.  With more instructions in them one issue in
-// six waited for its instruction: chunks with a window of 1024 took 140 us where
-// they take 121, a prompt of 4000, 64 values a head, 182 where it takes 160.
+// Chunks with a window of 1024 (9.1 tiles an item): 117 us, 46% of the cycles.
+// The roles' loops are kept short.  With more instructions in them a warp waited
+// 0.61 cycles an issue for its instruction (now 0.39): those chunks took 140 us,
+// a prompt of 4000, 64 values a head, 182 where it takes 160.
 //
 // Warps: 0-3 softmax of half 0, 4-7 of half 1 (and their results), 8 schedule
 // and TMA, 9 MMA issue.  Every wait is bounded; on timeout the kernel raises
