@@ -68,7 +68,10 @@ struct Misc {
   using La = Lay<D, A>;
   static constexpr int W = La::W, kStages = La::kStages;
   Segment ring[kRing];
-  float4 red[W][A];  // of a row: the four warps' maxima or sums
+  // Of a row: the four warps' maxima (of a tile) and sums (of a segment).  They
+  // are apart because no barrier of the warpgroup lies between the last tile's
+  // maxima and the sums: one warp may add up while another still reads maxima.
+  float4 red_max[W][A], red_sum[W][A];
   float m[W][A];
   int row_hi[W][A], row_lo[W][A];
   uint64_t full_k[kStages], full_v[kStages], empty[kStages];
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     const int d = D == 128 ? j : w * 16 + lane;  // this thread's column of O
     const float c = P.scale_log2;
     const int kBar = 1 + wg;
-    float4* red = M.red[wg];
+    float4 *const red_max = M.red_max[wg], *const red_sum = M.red_sum[wg];
     uint8_t* const Pbase = smem + La::oP + wg * PB * La::kP;
     const uint32_t tm_o = tmem_o + wg * kPV + lanes;
     uint64_t* const p_full = M.p_full[wg];
@@ -380,13 +383,13 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
 #pragma unroll
           for (int n = 0; n < A; ++n) {
             const float mx = warp_max(s[n]);
-            if (lane == 0) reinterpret_cast<float*>(&red[n])[w] = mx;
+            if (lane == 0) reinterpret_cast<float*>(&red_max[n])[w] = mx;
           }
           named_bar(kBar, 128);
           float fac[A];
 #pragma unroll
           for (int n = 0; n < A; ++n) {
-            const float4 r = red[n];
+            const float4 r = red_max[n];
             const float mx = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)) * c;
             const float now = fminf(neg[n], -mx);
             fac[n] = neg[n] == INFINITY ? 0.f : exp2_fast(now - neg[n]);
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
 #pragma unroll
       for (int n = 0; n < A; ++n) {
         const float x = warp_sum(l[n]);
-        if (lane == 0) reinterpret_cast<float*>(&red[n])[w] = x;
+        if (lane == 0) reinterpret_cast<float*>(&red_sum[n])[w] = x;
         if (st_tid == 0) M.m[wg][n] = -neg[n];
       }
       wait_quiet(&p_done[(tile - 1) % PB], ((tile - 1) / PB) & 1, abort_f);
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
           const int n = x / (D / 8), k = x % (D / 8) * 8;
           store8(P.part + (slot * A + n) * D + k,
                  *reinterpret_cast<const float(*)[8]>(stage + n * D + k));
-          const float4 r = red[n];
+          const float4 r = red_sum[n];
           if (k == 0) ml[slot * A + n] = make_float2(M.m[wg][n], r.x + r.y + r.z + r.w);
         }
         write = last_to_arrive(P, g, 0, st_tid == 0, &M.last[wg], kBar, 128);
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         const int n = x / (D / 8), k = x % (D / 8) * 8;
         float o[8], top, sum;
         if (g.parts == 1) {
-          const float4 r = red[n];
+          const float4 r = red_sum[n];
           top = M.m[wg][n];
           sum = r.x + r.y + r.z + r.w;
           load8(stage + n * D + k, o);
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
                                g.head * P.group + r - tok * P.group, true, top, sum);
         out.write8(k, o);
       }
-      named_bar(kBar, 128);  // red and the limits are free
+      named_bar(kBar, 128);  // the sums and the limits are free
     }
   }
 

@@ -1,0 +1,41 @@
+"""Edges of the paged-cache operators on the GPU: items of one key tile by the hundred, windows
+and positions at the types' ends, block-table entries of any value, other streams, empty
+batches, many sequences and groups, and head counts of every route.
+
+Tolerances are those of test_gpu_attn.py, derived there, unless a test derives its own.
+"""
+import numpy as np
+import pytest
+
+from tests.test_gpu_attn import HEADS, U, Case, L, attend, prefix_attend  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 2, 64), (16, 2, 64), (32, 2, 128)])
+def test_items_of_one_tile_repeat_bit_for_bit(L, hq, hkv, d):
+    """Every item is one key tile or two, so that each moves its maxima in the tile that its
+    sums follow: values against fp64, and the same bits from every call."""
+    import torch
+    torch.manual_seed(d + hq)
+    n, page = 608, 16
+    kv_len = torch.randint(1, 200, (n,), dtype=torch.int32, device="cuda")
+    pages = -(-200 // page)
+    table = torch.randperm(n * pages, device="cuda").to(torch.int32).view(n, pages)
+    kc, vc = (torch.randn(n * pages, hkv, page, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = (3 * torch.randn(n, hq, d, device="cuda")).to(torch.bfloat16)
+    kv = L.PagedKV(kc, vc, table, torch.arange(n + 1, dtype=torch.int32, device="cuda"), kv_len, n, max_q_len=1)
+    ws = L.attn_workspace(kv, hq)
+    first = L.attn_paged_t(kv, q, ws).clone()
+    k, v = (c[table.long()].transpose(2, 3).reshape(n, -1, hkv, d).double().repeat_interleave(hq // hkv, 2)
+            for c in (kc, vc))
+    x = torch.einsum("thd,tnhd->thn", q.double(), k) * d ** -0.5
+    x = x.masked_fill(torch.arange(pages * page, device="cuda") >= kv_len[:, None, None], -float("inf"))
+    w = x.softmax(-1)
+    ref, wv = (torch.einsum("thn,tnhd->thd", w, y) for y in (v, v.abs()))
+    # (scores three times as large: their error's share of the bound is, too)
+    assert ((first.double() - ref).abs() <= U * ref.abs() + (U + 3 * 2.0 ** -12) * wv).all()
+    out = torch.empty_like(q)
+    for _ in range(200):
+        assert torch.equal(L.attn_paged_t(kv, q, ws, out=out).view(torch.int16), first.view(torch.int16))
+    assert L.get_error_t(ws) == 0
