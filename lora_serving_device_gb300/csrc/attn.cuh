@@ -120,6 +120,13 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
   return x < lo ? lo : x > hi ? hi : x;
 }
 
+// The first position in the window of a row at `pos`.  (Compared before the
+// subtraction, which overflows for a row before position 0 and the widest
+// windows.)
+__device__ __forceinline__ int window_first(const AttnParams& P, int pos) {
+  return P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
+}
+
 // The group of sequence s (0 .. n_groups - 1), or -1.
 __device__ __forceinline__ int group_of_seq(const AttnParams& P, int s) {
   const int n = P.n_groups;
@@ -212,8 +219,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams& P, const Problem& 
   }
   const int first = pr.base + P.by_group(t.row0);
   t.vis_hi = min(pr.base + P.by_group(t.row0 + t.n_rows - 1), pr.k_hi - 1);
-  t.vis_lo = P.window > 0 ? max(first - P.window + 1, 0) : 0;
-  t.vis_lo = max(t.vis_lo, pr.k_lo);
+  t.vis_lo = max(window_first(P, first), pr.k_lo);
   t.n_sink = P.window > 0 ? max(min(P.n_sink, t.vis_hi + 1), 0) : 0;
   t.sink_places = (t.n_sink + P.box - 1) & -P.box;
   t.origin = t.vis_lo & -P.box;

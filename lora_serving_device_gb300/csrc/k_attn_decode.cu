@@ -334,8 +334,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
       for (int n = st_tid; n < A; n += 128) {
         const int pos = g.base + P.by_group(g.t.row0 + (n < g.t.n_rows ? n : 0));
         M.row_hi[wg][n] = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
-        M.row_lo[wg][n] =
-            P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
+        M.row_lo[wg][n] = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
       }
       named_bar(kBar, 128);
       int min_hi = M.row_hi[wg][lane % A], max_lo = M.row_lo[wg][lane % A];

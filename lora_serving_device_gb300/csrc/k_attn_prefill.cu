@@ -344,8 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = P.by_group(in_prob), head = g.head * P.group + in_prob - tok * P.group;
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
-      const int lo =
-          P.groups_phase ? 0 : max(P.window > 0 ? max(pos - P.window + 1, 0) : 0, g.k_lo);
+      const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++tile) {

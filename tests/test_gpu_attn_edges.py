@@ -39,3 +39,12 @@ def test_items_of_one_tile_repeat_bit_for_bit(L, hq, hkv, d):
     for _ in range(200):
         assert torch.equal(L.attn_paged_t(kv, q, ws, out=out).view(torch.int16), first.view(torch.int16))
     assert L.get_error_t(ws) == 0
+
+
+@pytest.mark.parametrize("window,n_sink", [(2 ** 31 - 1, 0), (2 ** 31 - 2, 2 ** 31 - 1), (2 ** 31 - 20, 3), (1, 0),
+                                           (30, 2), (130, 0)])
+def test_windows_with_rows_before_the_first_position(L, window, n_sink):
+    # the first row's position is -20 or lower where the window may be the type's largest
+    attend(L, Case([140], [-20], 4, 2, 64, 16, seed=5, window=window, n_sink=n_sink))
+    attend(L, Case([3, 30, 1, 400], [-2, -21, -1, -130], 4, 2, 128, 32, seed=6, window=window, n_sink=n_sink))
+    attend(L, Case([4, 4, 1, 1], [-3, -4, 300, 5], 8, 4, 64, 16, seed=7, window=window, n_sink=n_sink))
