@@ -525,7 +525,8 @@ lora_status_t lora_slot_upload(void* A_pool, void* B_pool, float* scale, int32_t
  *          kv_len[s] - (q_off[s+1] - q_off[s]) + i.  A row before position 0
  *          is not cached and sees nothing.
  *   n_pages, page_size (8, 16, 32, 64, 128 or 256), n_kv_heads, head_dim (64
- *          or 128), n_seqs, max_pages, T (rows of q, k, v, out).
+ *          or 128), n_seqs, max_pages (at most 2^31 - 1024 positions of a
+ *          sequence), T (rows of q, k, v, out).
  *   max_q_len  the most new tokens of any one sequence, as the host knows it.
  *          It selects kernels; results do not depend on it beyond rounding.
  * All arrays are device memory and 16-byte aligned (the int32 ones: 4-byte);

@@ -15,7 +15,8 @@ bool kv_shape_ok(const lora_paged_kv_t& kv) {
          kv.n_pages >= 1 && kv.max_pages >= 1 && pg >= 8 && pg <= 256 && (pg & (pg - 1)) == 0 &&
          (kv.head_dim == 64 || kv.head_dim == 128) && kv.n_kv_heads >= 1 &&
          kv.n_kv_heads <= LORA_MAX_HEADS &&
-         static_cast<int64_t>(kv.max_pages) * pg <= INT32_MAX &&
+         // positions, and what the kernels round up from them (tiles, pages), in 32 bits
+         static_cast<int64_t>(kv.max_pages) * pg <= INT32_MAX - 1023 &&
          // eight-row groups of one cache, the tensor map's outermost extent
          static_cast<int64_t>(kv.n_pages) * kv.n_kv_heads * (pg / 8) <= INT32_MAX;
 }

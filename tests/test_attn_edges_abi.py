@@ -1,0 +1,17 @@
+"""Edges of the paged-cache entry points on the host (nothing valid enough to launch is
+passed)."""
+import pytest
+
+from tests.test_attn_abi import FAKE, SHAPE, WORKSPACE, L, append, attend  # noqa: F401
+
+
+@pytest.mark.parametrize("page", [8, 64, 256])
+def test_positions_leave_room_for_rounding_up(L, page):
+    # a length of 2^31 - 8 rounded up to tiles of 128 keys would leave 32 bits
+    for max_pages in ((2 ** 31 - 1) // page, (2 ** 31 - 1024) // page + 1):
+        kw = dict(page_size=page, max_pages=max_pages)
+        assert append(L, kw) == SHAPE
+        assert attend(L, kw) == SHAPE
+        assert attend(L, kw, prefix=(FAKE, FAKE, 1)) == SHAPE
+    kw = dict(page_size=page, max_pages=(2 ** 31 - 1024) // page)
+    assert append(L, kw, ws=None) == attend(L, kw, ws=None) == WORKSPACE
