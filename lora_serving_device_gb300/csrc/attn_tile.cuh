@@ -184,15 +184,18 @@ struct TileLoader {
   uint64_t policy;
   int now;   // where this lane's box starts in the cache, in groups of eight rows,
              // in this batch of `per` tiles; -1: not needed
-  int next;  // its page's id in the next batch; INT32_MIN: not needed
+  int next;  // its page's id in the next batch, as the table has it, if it is needed
+  bool next_seen;
   __device__ __forceinline__ explicit TileLoader(const AttnParams& P)
       : page(P.kv.page_size),
         lg_page(P.lg_page),
         box(P.box),
         boxes(kKeys / box),
-        per(32 / boxes) {}
-  // This lane's box of the batch from tile i0: its page's id as the table has
-  // it (a load that nothing here waits for), and where it starts.
+        per(32 / boxes),
+        next(0) {}
+  // This lane's box of the batch from tile i0: whether some row sees it, its page's
+  // id as the table has it (a load that nothing here waits for; any value of the
+  // type may come), and where it starts.
   __device__ __forceinline__ int first_place(const Segment& g, int i0) const {
     const int lane = threadIdx.x & 31;
     return (g.first + i0 + lane / boxes) * kKeys + (lane & (boxes - 1)) * box;
@@ -201,17 +204,19 @@ struct TileLoader {
     const int v = first_place(g, i0);
     return v < g.t.sink_places ? v : window_key(g.t, v);
   }
-  __device__ __forceinline__ int fetch(const AttnParams& P, const Segment& g, int i0) const {
+  __device__ __forceinline__ int fetch(const AttnParams& P, const Segment& g, int i0,
+                                       bool& seen) const {
     const int key0 = first_key(g, i0);
-    const bool seen = i0 + (threadIdx.x & 31) / boxes < g.n &&
-                      ((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) ||
-                       first_place(g, i0) < g.t.n_sink);
+    seen = i0 + (threadIdx.x & 31) / boxes < g.n &&
+           ((key0 <= g.t.vis_hi && key0 + box - 1 >= g.t.vis_lo) ||
+            first_place(g, i0) < g.t.n_sink);
     return seen ? P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages +
                                    (key0 >> lg_page)]
-                : INT32_MIN;
+                : 0;
   }
-  __device__ __forceinline__ int place(const AttnParams& P, const Segment& g, int i0, int id) const {
-    if (id == INT32_MIN) return -1;
+  __device__ __forceinline__ int place(const AttnParams& P, const Segment& g, int i0, int id,
+                                       bool seen) const {
+    if (!seen) return -1;
     if (id < 0 || id >= P.kv.n_pages) {
       flag_error(P.err, LORA_DEVERR_BAD_PAGE);
       return P.kv.n_pages * P.kv.n_kv_heads * (page / 8);
@@ -220,16 +225,19 @@ struct TileLoader {
   }
   __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
     policy = l2_policy(g.once != 0);
-    const int id = fetch(P, g, 0);
-    next = g.n > per ? fetch(P, g, per) : INT32_MIN;
-    now = place(P, g, 0, id);
+    bool seen;
+    const int id = fetch(P, g, 0, seen);
+    next_seen = false;
+    if (g.n > per) next = fetch(P, g, per, next_seen);
+    now = place(P, g, 0, id, seen);
   }
   // The place of this lane's box of tile i (lanes below `boxes`).
   __device__ __forceinline__ int at(const AttnParams& P, const Segment& g, int i) {
     const int k = i % per;
     if (k == 0 && i > 0) {
-      now = place(P, g, i, next);
-      next = i + per < g.n ? fetch(P, g, i + per) : INT32_MIN;
+      now = place(P, g, i, next, next_seen);
+      next_seen = false;
+      if (i + per < g.n) next = fetch(P, g, i + per, next_seen);
     }
     const int lane = threadIdx.x & 31;
     const int x = __shfl_sync(0xffffffffu, now, k * boxes + (lane & (boxes - 1)));

@@ -48,3 +48,17 @@ def test_windows_with_rows_before_the_first_position(L, window, n_sink):
     attend(L, Case([140], [-20], 4, 2, 64, 16, seed=5, window=window, n_sink=n_sink))
     attend(L, Case([3, 30, 1, 400], [-2, -21, -1, -130], 4, 2, 128, 32, seed=6, window=window, n_sink=n_sink))
     attend(L, Case([4, 4, 1, 1], [-3, -4, 300, 5], 8, 4, 64, 16, seed=7, window=window, n_sink=n_sink))
+
+
+@pytest.mark.parametrize("wild", [-2 ** 31, -2 ** 31 + 1, -1, 2 ** 31 - 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_missing_page_may_have_any_id_outside_the_cache(L, wild, d):
+    """Missing pages in the first, a middle and the last tile of single tokens and of a chunk.
+    The batch of whole pages before leaves its keys and values in the shared memory."""
+    for q_lens, ctx in (([1, 1, 1], [100, 700, 20]), ([1, 20, 150], [100, 60, 400])):
+        missing = {(0, 2), (0, 6), (1, 0), (1, 3), (2, 1)}
+        attend(L, Case(q_lens, ctx, 4, 2, d, 16, seed=9))
+        c = Case(q_lens, ctx, 4, 2, d, 16, seed=9, missing=missing)
+        for s, p in missing:
+            c.table[s, p] = wild
+        attend(L, c, err=L.DEVERR_BAD_PAGE)
