@@ -3,7 +3,10 @@
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  The raw functions keep the C names and take integer device
 pointers; the ``*_t`` helpers take torch tensors (device memory and streams
-come from PyTorch) and raise ``LoraError`` on a non-OK status.  There is no
+come from PyTorch) and raise ``LoraError`` on a non-OK status.  A ``*_t`` call that is
+given a stream makes its results from that stream's memory, as PyTorch does
+under ``torch.cuda.stream``: their use on another stream takes the usual wait
+and ``record_stream``.  There is no
 fallback: if the library is missing or the device is not sm_103, calls fail.
 """
 from __future__ import annotations
@@ -282,6 +285,16 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _on(stream, make, *args, **kw):
+    """make(...), a tensor that a call on `stream` (None: the current one) is going to write:
+    its memory is that stream's.  Memory of the current stream could still be in use there."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _dt(t):
     import torch
     if t.dtype == torch.bfloat16:
@@ -308,10 +321,10 @@ def build_segments_t(slot_ids, n_slots, ws, stream=None):
     T = slot_ids.numel()
     cap = max(1, min(T, n_slots))
     dev = slot_ids.device
-    perm = torch.empty(max(T, 1), dtype=torch.int32, device=dev)
-    seg_slot = torch.empty(cap, dtype=torch.int32, device=dev)
-    seg_off = torch.empty(cap + 1, dtype=torch.int32, device=dev)
-    n_seg = torch.empty(1, dtype=torch.int32, device=dev)
+    perm = _on(stream, torch.empty, max(T, 1), dtype=torch.int32, device=dev)
+    seg_slot = _on(stream, torch.empty, cap, dtype=torch.int32, device=dev)
+    seg_off = _on(stream, torch.empty, cap + 1, dtype=torch.int32, device=dev)
+    n_seg = _on(stream, torch.empty, 1, dtype=torch.int32, device=dev)
     check(lora_build_segments(_ptr(slot_ids), T, n_slots, _ptr(perm), _ptr(seg_slot),
                               _ptr(seg_off), _ptr(n_seg), _ptr(ws), ws.numel(), _stream(stream)),
           "lora_build_segments")
@@ -323,7 +336,7 @@ def bgmv_shrink_t(x, A_pool, slot_ids, scale, ksplit, ws, v_partial=None, stream
     T, d_in = x.shape
     n_slots, _, r = A_pool.shape
     if v_partial is None:
-        v_partial = torch.empty((ksplit, T, r), dtype=torch.float32, device=x.device)
+        v_partial = _on(stream, torch.empty, (ksplit, T, r), dtype=torch.float32, device=x.device)
     check(lora_bgmv_shrink(_ptr(x), _ptr(A_pool), _ptr(slot_ids), _ptr(scale), _ptr(v_partial), T,
                            d_in, r, n_slots, ksplit, _dt(x), _ptr(ws), ws.numel(), _stream(stream)),
           "lora_bgmv_shrink")
@@ -345,7 +358,7 @@ def sgmv_shrink_t(x, A_pool, segs, scale, ksplit, ws, v_partial=None, stream=Non
     T, d_in = x.shape
     n_slots, _, r = A_pool.shape
     if v_partial is None:
-        v_partial = torch.empty((ksplit, T, r), dtype=torch.float32, device=x.device)
+        v_partial = _on(stream, torch.empty, (ksplit, T, r), dtype=torch.float32, device=x.device)
     check(lora_sgmv_shrink(_ptr(x), _ptr(A_pool), _ptr(perm), _ptr(seg_slot), _ptr(seg_off),
                            _ptr(n_seg), _ptr(scale), _ptr(v_partial), T, d_in, r, n_slots, ksplit,
                            _dt(x), _ptr(ws), ws.numel(), _stream(stream)), "lora_sgmv_shrink")
@@ -369,7 +382,7 @@ def linear_fused_t(x, W0, A_pool, B_pool, slot_ids, scale, ws, y=None, stream=No
     d_out = W0.shape[1]
     n_slots, _, r = A_pool.shape
     if y is None:
-        y = torch.empty((T, d_out), dtype=x.dtype, device=x.device)
+        y = _on(stream, torch.empty, (T, d_out), dtype=x.dtype, device=x.device)
     check(lora_linear_fused(_ptr(x), _ptr(W0), _ptr(A_pool), _ptr(B_pool), _ptr(slot_ids),
                             _ptr(scale), _ptr(y), T, d_in, d_out, r, n_slots, _dt(x), _ptr(ws),
                             ws.numel(), _stream(stream)), "lora_linear_fused")
@@ -383,7 +396,7 @@ def base_gemm_expand_t(x, W0, B_pool, slot_ids, v_partial, ws, y=None, stream=No
     d_out = W0.shape[1]
     n_slots, r, _ = B_pool.shape
     if y is None:
-        y = torch.empty((T, d_out), dtype=x.dtype, device=x.device)
+        y = _on(stream, torch.empty, (T, d_out), dtype=x.dtype, device=x.device)
     check(lora_base_gemm_expand(_ptr(x), _ptr(W0), _ptr(B_pool), _ptr(slot_ids), _ptr(v_partial),
                                 v_partial.shape[0], _ptr(y), T, d_in, d_out, r, n_slots, _dt(x),
                                 _ptr(ws), ws.numel(), _stream(stream)), "lora_base_gemm_expand")
@@ -396,7 +409,7 @@ def bgmv_delta_t(v_partial, B_pool, slot_ids, ws, delta=None, stream=None):
     ksplit, T, r = v_partial.shape
     n_slots, _, d_out = B_pool.shape
     if delta is None:
-        delta = torch.zeros((T, d_out), dtype=torch.float32, device=v_partial.device)
+        delta = _on(stream, torch.zeros, (T, d_out), dtype=torch.float32, device=v_partial.device)
     check(lora_bgmv_delta(_ptr(v_partial), ksplit, _ptr(B_pool), _ptr(slot_ids), _ptr(delta), T, r,
                           d_out, n_slots, _dt(B_pool), _ptr(ws), ws.numel(), _stream(stream)),
           "lora_bgmv_delta")
@@ -410,7 +423,7 @@ def bgmv_adapter_t(x, A_pool, B_pool, slot_ids, scale, ws, delta=None, stream=No
     T, d_in = x.shape
     n_slots, r, d_out = B_pool.shape
     if delta is None:
-        delta = torch.zeros((T, d_out), dtype=torch.float32, device=x.device)
+        delta = _on(stream, torch.zeros, (T, d_out), dtype=torch.float32, device=x.device)
     check(lora_bgmv_adapter(_ptr(x), _ptr(A_pool), _ptr(B_pool), _ptr(slot_ids), _ptr(scale),
                             _ptr(delta), T, d_in, d_out, r, n_slots, _dt(x), _ptr(ws), ws.numel(),
                             _stream(stream)),
@@ -442,7 +455,7 @@ def base_gemm_splitk_t(x, W0, ws, ksplit=None, partial=None, stream=None):
         ksplit = 0 if 1 <= T <= 256 else 1
     S = lora_decode_split(T, d_in, d_out) if ksplit == 0 else ksplit
     if partial is None:
-        partial = torch.empty((max(S, 1), T, d_out), dtype=torch.float32, device=x.device)
+        partial = _on(stream, torch.empty, (max(S, 1), T, d_out), dtype=torch.float32, device=x.device)
     check(lora_base_gemm_splitk(_ptr(x), _ptr(W0), _ptr(partial), T, d_in, d_out, ksplit, _dt(x),
                                 _ptr(ws), ws.numel(), _stream(stream)),
           "lora_base_gemm_splitk")
@@ -455,7 +468,7 @@ def bgmv_adapter_merge_t(x, A_pool, B_pool, slot_ids, scale, partial, ws, y=None
     T, d_in = x.shape
     n_slots, r, d_out = B_pool.shape
     if y is None:
-        y = torch.empty((T, d_out), dtype=x.dtype, device=x.device)
+        y = _on(stream, torch.empty, (T, d_out), dtype=x.dtype, device=x.device)
     check(lora_bgmv_adapter_merge(_ptr(x), _ptr(A_pool), _ptr(B_pool), _ptr(slot_ids),
                                   _ptr(scale), _ptr(partial), partial.shape[0], _ptr(y), T, d_in,
                                   d_out, r, n_slots, _dt(x), _ptr(ws), ws.numel(),
@@ -524,7 +537,7 @@ def bgmv_adapter_ragged_t(x, pool, slot_ids, scale, ws, delta=None, stream=None)
     import torch
     T, d_in = x.shape
     if delta is None:
-        delta = torch.zeros((T, pool.d_out), dtype=torch.float32, device=x.device)
+        delta = _on(stream, torch.zeros, (T, pool.d_out), dtype=torch.float32, device=x.device)
     check(lora_bgmv_adapter_ragged(_ptr(x), _ptr(pool.A_flat), _ptr(pool.B_flat),
                                    _ptr(pool.a_off), _ptr(pool.b_off), _ptr(pool.rank),
                                    pool.A_flat.numel(), pool.B_flat.numel(), pool.r_max,
@@ -543,7 +556,7 @@ def linear_fused_ragged_t(x, W0, pool, slot_ids, scale, ws, y=None, stream=None)
     T, d_in = x.shape
     d_out = W0.shape[1]
     if y is None:
-        y = torch.empty((T, d_out), dtype=x.dtype, device=x.device)
+        y = _on(stream, torch.empty, (T, d_out), dtype=x.dtype, device=x.device)
     check(lora_linear_fused_ragged(_ptr(x), _ptr(W0), _ptr(pool.A_flat), _ptr(pool.B_flat),
                                    _ptr(pool.a_off), _ptr(pool.b_off), _ptr(pool.rank),
                                    pool.A_flat.numel(), pool.B_flat.numel(), pool.r_max,
@@ -568,8 +581,8 @@ class Base4bit:
         """Quantise a bf16 W0 [d_in, d_out] with the library's kernel."""
         import torch
         d_in, d_out = W0.shape
-        W0q = torch.empty((d_out, d_in // 2), dtype=torch.uint8, device=W0.device)
-        absmax = torch.empty((d_in // 64, d_out), dtype=torch.bfloat16, device=W0.device)
+        W0q = _on(stream, torch.empty, (d_out, d_in // 2), dtype=torch.uint8, device=W0.device)
+        absmax = _on(stream, torch.empty, (d_in // 64, d_out), dtype=torch.bfloat16, device=W0.device)
         check(lora_quantize_base_4bit(_ptr(W0), _ptr(codebook), _ptr(W0q), _ptr(absmax), d_in,
                                       d_out, _stream(stream)), "lora_quantize_base_4bit")
         return cls(W0q, absmax, codebook)
@@ -586,7 +599,7 @@ def base_gemm_4bit_splitk_t(x, base, ws, ksplit=None, partial=None, stream=None)
     if ksplit is None:
         ksplit = lora_decode_split(T, d_in, base.d_out) or 1
     if partial is None:
-        partial = torch.empty((ksplit, T, base.d_out), dtype=torch.float32, device=x.device)
+        partial = _on(stream, torch.empty, (ksplit, T, base.d_out), dtype=torch.float32, device=x.device)
     check(lora_base_gemm_4bit_splitk(_ptr(x), _ptr(base.W0q), _ptr(base.absmax),
                                      _ptr(base.codebook), _ptr(partial), T, d_in, base.d_out,
                                      ksplit, _ptr(ws), ws.numel(), _stream(stream)),
@@ -601,7 +614,7 @@ def linear_fused_4bit_t(x, base, A_pool, B_pool, slot_ids, scale, ws, y=None, st
     T, d_in = x.shape
     n_slots, _, r = A_pool.shape
     if y is None:
-        y = torch.empty((T, base.d_out), dtype=x.dtype, device=x.device)
+        y = _on(stream, torch.empty, (T, base.d_out), dtype=x.dtype, device=x.device)
     check(lora_linear_fused_4bit(_ptr(x), _ptr(base.W0q), _ptr(base.absmax), _ptr(base.codebook),
                                  _ptr(A_pool), _ptr(B_pool), _ptr(slot_ids), _ptr(scale), _ptr(y),
                                  T, d_in, base.d_out, r, n_slots, _ptr(ws), ws.numel(),
@@ -697,7 +710,7 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
         n_q = q.shape[1]
         q_stride = kv.rows(q, n_q, "q")
         if q_out is None:
-            q_out = kv.new_like(q)
+            q_out = _on(stream, kv.new_like, q)
             q_out_stride = n_q * kv.head_dim
         else:
             q_out_stride = kv.rows(q_out, n_q, "q_out")
@@ -731,7 +744,7 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
     n_q = q.shape[1]
     q_stride = kv.rows(q, n_q, "q")
     if out is None:
-        out = kv.new_like(q)
+        out = _on(stream, kv.new_like, q)
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")
@@ -752,7 +765,7 @@ def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream
         if t.dtype is not kv._i32 or t.numel() != n or not t.is_contiguous() or t.get_device() != kv._device:
             raise TypeError(f"{name}: contiguous int32 [{n}] on the cache's device")
     if out is None:
-        out = kv.new_like(q)
+        out = _on(stream, kv.new_like, q)
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")

@@ -62,3 +62,34 @@ def test_a_missing_page_may_have_any_id_outside_the_cache(L, wild, d):
         for s, p in missing:
             c.table[s, p] = wild
         attend(L, c, err=L.DEVERR_BAD_PAGE)
+
+
+@pytest.mark.parametrize("op", ["append", "paged", "prefix"])
+def test_results_of_a_call_on_another_stream_are_made_there(L, op):
+    """The current stream is behind: a tensor of the result's size that it has still to write is
+    let go on the host.  The call's result must not be in that memory."""
+    import torch
+    groups = ([0, 2], [40])
+    c = Case([1, 1], [300, 40], 4, 2, 64, 16, seed=4, groups=groups)
+    kv = c.kv(L)
+    ws = L.attn_workspace(kv, c.hq, n_groups=1)
+    off, plen = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in groups)
+    k = torch.zeros(c.T, c.hkv, c.d, dtype=torch.bfloat16, device="cuda")
+
+    def call(stream=None):
+        if op == "append":
+            return L.kv_append_t(kv, c.q, k, k, None, ws, stream=stream)
+        if op == "prefix":
+            return L.attn_prefix_t(kv, c.q, off, plen, ws, stream=stream)
+        return L.attn_paged_t(kv, c.q, ws, stream=stream)
+
+    want = call().clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    late = torch.full_like(want, 7.0)
+    where = late.data_ptr()
+    del late
+    got = call(side)
+    torch.cuda.synchronize()
+    assert got.data_ptr() != where and torch.equal(got, want)
