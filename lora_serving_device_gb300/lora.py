@@ -659,6 +659,7 @@ class PagedKV:
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
         self.new_like = torch.empty_like
         self._current_stream = torch._C._cuda_getCurrentRawStream
+        self._current_device = torch._C._cuda_getDevice
 
     def rows(self, x, n_heads, what):
         """Checks x [T, n_heads, head_dim] bf16 and returns its distance between tokens."""
@@ -673,6 +674,11 @@ class PagedKV:
         return st[0] if T > 1 else heads * d
 
     def stream(self, stream):
+        """The handle of `stream`, or of the current one.  The launch goes to the current
+        device, so that has to be the cache's."""
+        if self._current_device() != self._device:
+            raise ValueError(f"the cache is on cuda:{self._device}, the current device is "
+                             f"cuda:{self._current_device()}")
         return self._current_stream(self._device) if stream is None else stream.cuda_stream
 
 

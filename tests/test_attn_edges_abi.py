@@ -15,3 +15,13 @@ def test_positions_leave_room_for_rounding_up(L, page):
         assert attend(L, kw, prefix=(FAKE, FAKE, 1)) == SHAPE
     kw = dict(page_size=page, max_pages=(2 ** 31 - 1024) // page)
     assert append(L, kw, ws=None) == attend(L, kw, ws=None) == WORKSPACE
+
+
+def test_calls_need_the_caches_device_to_be_current(L):
+    kv = object.__new__(L.PagedKV)
+    kv._device, kv._current_device = 1, lambda: 1
+    kv._current_stream = lambda device: 100 + device
+    assert kv.stream(None) == 101
+    kv._current_device = lambda: 0
+    with pytest.raises(ValueError, match="current device"):
+        kv.stream(None)
