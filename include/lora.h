@@ -533,7 +533,8 @@ lora_status_t lora_slot_upload(void* A_pool, void* B_pool, float* scale, int32_t
  * the struct itself is host memory, read during the call.  q, k, v and out
  * are bf16 [T, heads, head_dim] with any distance between tokens that is a
  * multiple of 8 elements (*_stride, in elements), so that they can be parts of
- * one wider projection's rows.  Offsets are 64-bit throughout.
+ * one wider projection's rows.  Offsets are 64-bit throughout.  With T = 0
+ * nothing is launched, and pointers to rows and their positions may be NULL.
  */
 typedef struct {
   void* k_cache;

@@ -34,9 +34,9 @@ lora_status_t check_kv(const lora_paged_kv_t* kv) {
 }
 
 // Rows [T, heads, head_dim]: 16-byte loads from every head of every row, and
-// rows that do not overlap.
+// rows that do not overlap.  An empty batch has no rows to point to.
 lora_status_t check_rows(const void* p, int64_t stride, const lora_paged_kv_t& kv, int heads) {
-  if (p == nullptr || !aligned16(p)) return LORA_ERR_INVALID_ARG;
+  if ((p == nullptr && kv.T > 0) || !aligned16(p)) return LORA_ERR_INVALID_ARG;
   if (stride % 8 != 0 || stride > (int64_t{1} << 38) ||
       stride < static_cast<int64_t>(heads) * kv.head_dim)
     return LORA_ERR_SHAPE;
@@ -58,7 +58,7 @@ lora_status_t attn_common(const lora_paged_kv_t* kv, const AttnArgs& a, size_t w
   if (!q_heads_ok(a.n_q_heads, *kv)) return LORA_ERR_SHAPE;
   if ((s = check_rows(a.q, a.q_stride, *kv, a.n_q_heads)) != LORA_OK) return s;
   if ((s = check_rows(a.out, a.out_stride, *kv, a.n_q_heads)) != LORA_OK) return s;
-  if (a.q == a.out || !(a.scale > 0.f && a.scale < 1e30f) || a.window < 0 || a.n_sink < 0)
+  if ((a.q == a.out && a.q != nullptr) || !(a.scale > 0.f && a.scale < 1e30f) || a.window < 0 || a.n_sink < 0)
     return LORA_ERR_INVALID_ARG;
   if ((s = check_ws(a.ws, ws_bytes, attn_ws_bytes(*kv, a.n_q_heads, a.n_groups))) != LORA_OK)
     return s;
@@ -100,7 +100,7 @@ lora_status_t lora_kv_append(const lora_paged_kv_t* kv, const void* q, int64_t q
   if (rot_dim > 0 && (cos_sin == nullptr || !aligned16(cos_sin) || n_pos < 1))
     return LORA_ERR_INVALID_ARG;
   if (n_axes > 1) {
-    if (pos == nullptr || axis_pairs == nullptr) return LORA_ERR_INVALID_ARG;
+    if ((pos == nullptr && kv->T > 0) || axis_pairs == nullptr) return LORA_ERR_INVALID_ARG;
     int64_t sum = 0;
     for (int i = 0; i < n_axes; ++i) {
       if (axis_pairs[i] < 0) return LORA_ERR_INVALID_ARG;

@@ -2,7 +2,9 @@
 passed)."""
 import pytest
 
-from tests.test_attn_abi import FAKE, SHAPE, WORKSPACE, L, append, attend  # noqa: F401
+from tests.test_attn_abi import FAKE, INVALID, SHAPE, WORKSPACE, L, append, attend  # noqa: F401
+
+OK = 0
 
 
 @pytest.mark.parametrize("page", [8, 64, 256])
@@ -25,3 +27,15 @@ def test_calls_need_the_caches_device_to_be_current(L):
     kv._current_device = lambda: 0
     with pytest.raises(ValueError, match="current device"):
         kv.stream(None)
+
+
+def test_an_empty_batch_has_no_rows_to_point_to(L):
+    none = dict(T=0)
+    assert append(L, none, q=None, k=None, v=None, qo=None) == OK
+    assert append(L, none, q=None, k=None, v=None, qo=None, axes=3, pairs=[8, 12, 12]) == OK
+    assert append(L, none, q=None, k=None, v=None, qo=None, axes=3) == INVALID      # the pairs are host memory
+    for prefix in (None, (FAKE, FAKE, 2)):
+        assert attend(L, none, prefix=prefix, q=None, out=None) == OK
+        assert attend(L, none, prefix=prefix, q=None, out=None, scale=0.0) == INVALID
+        assert attend(L, prefix=prefix, q=None, out=None) == INVALID
+        assert attend(L, none, prefix=prefix, q=FAKE, out=FAKE) == INVALID

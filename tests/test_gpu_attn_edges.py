@@ -93,3 +93,20 @@ def test_results_of_a_call_on_another_stream_are_made_there(L, op):
     got = call(side)
     torch.cuda.synchronize()
     assert got.data_ptr() != where and torch.equal(got, want)
+
+
+def test_empty_batches(L):
+    import torch
+    c = Case([0, 0, 0], [5, 0, 40], 4, 2, 64, 16, seed=1, groups=([0, 3], [2]))
+    kv = c.kv(L)
+    ws = L.attn_workspace(kv, 4, n_groups=1)
+    q, k = (torch.empty(0, h, 64, dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    pos = torch.empty(3, 0, dtype=torch.int32, device="cuda")
+    off, plen = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 3], [2]))
+    cs = L.rope_table(64, 64)
+    assert L.kv_append_t(kv, q, k, k, cs, ws).shape == q.shape
+    assert L.kv_append_t(kv, q, k, k, cs, ws, pos=pos, axis_pairs=(8, 12, 12)).shape == q.shape
+    assert L.kv_append_t(kv, None, k, k, cs, ws) is None
+    assert L.attn_paged_t(kv, q, ws).shape == q.shape
+    assert L.attn_prefix_t(kv, q, off, plen, ws).shape == q.shape
+    assert L.get_error_t(ws) == 0
