@@ -614,8 +614,8 @@ lora_status_t lora_attn_paged(const lora_paged_kv_t* kv, const void* q, int64_t 
  * lora_attn_paged without a window for a batch whose sequences share prefixes:
  * keys and values depend on the adapter, so the requests of one adapter share
  * its system prompt's pages.  Group g is sequences group_off[g] ..
- * group_off[g+1) (int32 [n_groups + 1], device, ascending, group_off[0] = 0;
- * sequences after the last group share nothing); the first prefix_len[g]
+ * group_off[g+1) (int32 [n_groups + 1], device, ascending; sequences before the
+ * first group and after the last share nothing); the first prefix_len[g]
  * positions of all of them hold the same keys and values and are read ONCE,
  * through the block table row of the group's first sequence.  The other rows'
  * entries for pages that lie wholly inside the prefix are not read.

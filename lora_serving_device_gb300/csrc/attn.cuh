@@ -137,7 +137,7 @@ __device__ __forceinline__ int group_of_seq(const AttnParams& P, int s) {
     return g < n ? g : -1;
   }
   int lo = 0, hi = n;  // group_off[lo] <= s < group_off[hi], if in any
-  if (s >= P.group_off[hi]) return -1;
+  if (s < P.group_off[lo] || s >= P.group_off[hi]) return -1;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (P.group_off[mid] <= s) lo = mid; else hi = mid;

@@ -110,3 +110,20 @@ def test_empty_batches(L):
     assert L.attn_paged_t(kv, q, ws).shape == q.shape
     assert L.attn_prefix_t(kv, q, off, plen, ws).shape == q.shape
     assert L.get_error_t(ws) == 0
+
+
+@pytest.mark.parametrize("n_groups", [2, 16, 17, 40])
+def test_sequences_before_the_first_group_share_nothing(L, n_groups):
+    # (many groups are searched another way than few)
+    import torch
+    first = [3 + 2 * i for i in range(n_groups + 1)]
+    prefix = [20 + 5 * (i % 7) for i in range(n_groups)]
+    ctx = [9, 100, 30] + [prefix[i // 2] + i % 3 for i in range(2 * n_groups)] + [70]
+    groups = (first, prefix)
+    c = Case([1] * len(ctx), ctx, 4, 2, 64, 16, seed=n_groups, groups=groups)
+    kv = c.kv(L)
+    ws = L.attn_workspace(kv, 4, n_groups=n_groups)
+    ws[4096:].fill_(0x7F)      # a prefix part that nothing wrote would show
+    off, plen = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in groups)
+    c.check(L.attn_prefix_t(kv, c.q, off, plen, ws, out=c.out))
+    assert L.get_error_t(ws) == 0
