@@ -127,3 +127,52 @@ def test_sequences_before_the_first_group_share_nothing(L, n_groups):
     off, plen = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in groups)
     c.check(L.attn_prefix_t(kv, c.q, off, plen, ws, out=c.out))
     assert L.get_error_t(ws) == 0
+
+
+# ------------------------------------------------------------------ branches by size
+
+@pytest.mark.parametrize("max_q", [1, None])
+def test_more_sequences_than_are_sized_ahead(L, max_q):
+    """2300 sequences, with prompts and empty ones past the first 2048, by both routes."""
+    rng = np.random.default_rng(3)
+    q = [int(x) for x in rng.integers(0, 2, 2300)]
+    ctx = [int(x) for x in rng.integers(0, 40, 2300)]
+    for s, n in ((2047, 9), (2048, 33), (2049, 0), (2100, 70), (2299, 12)):
+        q[s] = n
+    attend(L, Case(q, ctx, 2, 1, 64, 16, seed=11), max_q=max_q)
+
+
+def test_more_groups_than_are_sized_ahead(L):
+    rng = np.random.default_rng(4)
+    n = 2200
+    prefix = [int(x) for x in rng.integers(0, 20, n)]
+    groups = (list(range(n + 1)), prefix)
+    q = [1] * n
+    q[2100] = 40
+    prefix_attend(L, Case(q, [p + int(x) for p, x in zip(prefix, rng.integers(0, 5, n))], 2, 1, 64, 16, seed=12,
+                          groups=groups), groups)
+
+
+@pytest.mark.parametrize("n_groups", [16, 17, 33])
+def test_many_groups(L, n_groups):
+    # empty groups at the ends and in the middle, prefixes of nothing, sequences after the last
+    sizes = [[2, 1, 0, 3][i % 4] for i in range(n_groups)]
+    sizes[0] = sizes[-1] = sizes[n_groups // 2] = 0
+    first = [0] + [int(x) for x in np.cumsum(sizes)]
+    prefix = [0 if i % 5 == 4 else 15 + 20 * (i % 6) for i in range(n_groups)]
+    group = [g for g in range(n_groups) for _ in range(sizes[g])]
+    ctx = [prefix[g] + 3 * (i % 4) for i, g in enumerate(group)] + [50, 0]
+    q = [1 + (7 if i % 9 == 3 else 0) for i in range(len(ctx))]
+    groups = (first, prefix)
+    prefix_attend(L, Case(q, ctx, 8, 2, 64, 16, seed=n_groups, groups=groups, pad_rows=2), groups)
+
+
+@pytest.mark.parametrize("group", [16, 17, 64, 65, 100, 128, 129, 144])
+@pytest.mark.parametrize("d", [64, 128])
+def test_query_heads_of_one_key_head(L, group, d):
+    """Up to 16: rows in N; to 128: whole tokens in a half (one from 65 on); above: cut into
+    tiles of 16 rows across tokens."""
+    attend(L, Case([1, 1, 1], [0, 150, 300], 2 * group, 2, d, 16, seed=group))
+    attend(L, Case([9, 1, 0, 3], [140, 37, 4, 0], group, 1, d, 32, seed=group, window=60, n_sink=3, pad_rows=1))
+    groups = ([0, 3], [150])
+    prefix_attend(L, Case([1, 5, 1], [150, 160, 300], group, 1, d, 16, seed=group, groups=groups), groups)
