@@ -595,9 +595,13 @@ lora_status_t lora_kv_append(const lora_paged_kv_t* kv, const void* q, int64_t q
  * with the keys and values of key head h / (n_q_heads / n_kv_heads).  A row at
  * position p sees j <= p; with window >= 1 only j > p - window or j < n_sink
  * (the first tokens stay visible).  window = 0: no window.  A row that sees
- * nothing gets zeros.  Scores, maxima, sums and the accumulator are fp32, the
- * weights enter the product with v as bf16 (single tokens: as a pair of them),
- * the result is rounded once.
+ * nothing gets zeros.  Scores, maxima, sums and the accumulator are fp32, and
+ * the result is rounded once.  The weights enter the product with v as bf16, or
+ * as a pair of them (the value and its rest) where the tensor cores have the time:
+ * where max_q_len tokens make at most 16 rows (tokens x query heads of a key
+ * head; in the prefix part of lora_attn_prefix, T tokens), and with more than
+ * 128 query heads of a key head.  So max_q_len, and a prompt in the same batch,
+ * change the rounding of a single token's weights.
  * n_q_heads is a multiple of n_kv_heads.  Any mix of lengths in one call:
  * prompts, chunks, single tokens.  Cache rows that no row of the sequence sees
  * may hold anything, NaN included; a value that some row sees has to be

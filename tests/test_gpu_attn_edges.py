@@ -176,3 +176,42 @@ def test_query_heads_of_one_key_head(L, group, d):
     attend(L, Case([9, 1, 0, 3], [140, 37, 4, 0], group, 1, d, 32, seed=group, window=60, n_sink=3, pad_rows=1))
     groups = ([0, 3], [150])
     prefix_attend(L, Case([1, 5, 1], [150, 160, 300], group, 1, d, 16, seed=group, groups=groups), groups)
+
+
+# ------------------------------------------------------------------ weights as a pair of bf16
+
+@pytest.mark.parametrize("q_len,hq,hkv,d", [(1, 8, 2, 128), (1, 8, 8, 64), (1, 16, 2, 64), (1, 32, 2, 128),
+                                            (4, 8, 2, 64), (2, 144, 1, 64)])
+@pytest.mark.parametrize("prefix", [0, 3])
+def test_few_rows_take_the_weights_as_a_pair(L, q_len, hq, hkv, d, prefix):
+    """Against a bound that one bf16 a weight would not keep.  The value and its rest leave 2^-16
+    of a weight, the product adds 16 keys at a time in fp32 (below 2^-17 over these lengths), the
+    exponential and the sum 2^-20: below 2^-15 sum_j w_j |v_j|, beside the scores' 2^-12 and the
+    rounding of the result (2^-8 of it).  The oracle with weights rounded once exceeds it."""
+    import torch
+    from oracle import attn_ref as R
+    group = hq // hkv
+    n = 9 if not prefix or group > 128 else max(1, 16 // (q_len * group))
+    ctx = [prefix + 3 * i for i in range(n)]
+    groups = ([0, n], [prefix]) if prefix else None
+    c = Case([q_len] * n, ctx, hq, hkv, d, 16, seed=hq, groups=groups)
+    kv = c.kv(L)
+    ws = L.attn_workspace(kv, hq, n_groups=1 if prefix else 0)
+    if prefix:
+        off, plen = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in groups)
+        got = L.attn_prefix_t(kv, c.q, off, plen, ws, out=c.out)
+    else:
+        got = L.attn_paged_t(kv, c.q, ws, out=c.out)
+    assert L.get_error_t(ws) == 0
+    k, v = ([x.double().numpy() for x in rows] for rows in (c.rows_k, c.rows_v))
+    ref, wv = R.attention(c.q_host, k, v, c.q_off, c.kv_len, d ** -0.5)
+    bound = U * np.abs(ref) + (1 + U) * (2.0 ** -15 + 2.0 ** -12) * wv
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= bound)
+    once = np.empty_like(ref)
+    for t, s, p in R.positions(c.q_off, c.kv_len):
+        for h in range(hq):
+            g = h // group
+            x = d ** -0.5 * (k[s][:p + 1, g] @ c.q_host[t, h])
+            w = np.exp(x - x.max())
+            once[t, h] = torch.from_numpy(w).bfloat16().double().numpy() @ v[s][:p + 1, g] / w.sum()
+    assert np.any(np.abs(once - ref) > bound)
