@@ -20,17 +20,19 @@
 // query head of the key head), so all query heads of a key head share each
 // K and V tile; a half holds whole tokens, which lets TMA fetch Q too.
 //
-// Measured: a prompt of 8192, 32 / 8 heads of 128: 345 us, 1590 TFLOP/s (0.82 of
-// the measured burst rate; 370 us when the card is under load for long); the
-// tensor pipe is active for 69% of the cycles, the exponentials' for 35%.  What
-// is left is the way from scores to weights and back: S and P share tensor
+// Measured: a prompt of 8192, 32 / 8 heads of 128: 373 us, 1475 TFLOP/s (0.76 of
+// the measured burst rate, 0.83 of the sustained one); 348 us in the first
+// moments on a cool card.  The tensor pipe is active for 69% of the cycles (345
+// us under the profiler), the exponentials' for 35%.  What is
+// left is the way from scores to weights and back: S and P share tensor
 // memory, which the two halves' S and O fill, so a half's next scores wait for
 // its last product.  P handed over as a whole costs 3%, in quarters 6%, after
 // three quarters 4%; two threads to a row, with a vote a tile, 14%.
 // Chunks with a window of 1024 (9.1 tiles an item): 117 us, 46% of the cycles.
 // The roles' loops are kept short.  With more instructions in them a warp waited
 // 0.61 cycles an issue for its instruction (now 0.39): those chunks took 140 us,
-// a prompt of 4000, 64 values a head, 182 where it takes 160.
+// a prompt of 4000, 64 / 8 heads of 64, 182 where it takes 160 (the operations of
+// its product alone: 67 us; it takes twice the exponentials an operation).
 //
 // Warps: 0-3 softmax of half 0, 4-7 of half 1 (and their results), 8 schedule
 // and TMA, 9 MMA issue.  Every wait is bounded; on timeout the kernel raises
