@@ -102,6 +102,7 @@ typedef enum {
 #define LORA_DEVERR_BAD_PAGE 0x10u
 #define LORA_DEVERR_BAD_POS 0x20u /* a rotary position outside [0, n_pos) was read */
 #define LORA_DEVERR_BAD_LEN 0x40u /* q_off, kv_len, group_off or prefix_len out of order or range */
+#define LORA_DEVERR_NO_PAGE 0x80u /* lora_batch_plan: more pages needed than are free */
 
 #define LORA_MAX_SLOTS 16384
 #define LORA_MAX_TOKENS (1 << 20)
@@ -631,6 +632,94 @@ lora_status_t lora_attn_prefix(const lora_paged_kv_t* kv, const int32_t* group_o
                                const int32_t* prefix_len, int32_t n_groups, const void* q,
                                int64_t q_stride, int32_t n_q_heads, float scale, void* out,
                                int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A batch's place in a paged cache, made on the device from the lengths of its
+ * requests, so that a captured step can cross page borders, take up requests and
+ * drop them without the host: block tables, lengths and slot maps.
+ *   n_cached [n_seqs] int32: positions of sequence s that are cached already.
+ *   n_new    [n_seqs] int32: its new tokens; 0 = none in this step; < 0: the request
+ *            has ended and gives its pages back.
+ *   n_shared [n_seqs] int32 or NULL: pages in front of its row that others hold too (a
+ *            shared prefix); they are not given back.
+ *   free_pages [free_cap], n_free [1] int32: the free pages, a stack of ids whose top is
+ *            free_pages[n_free - 1].
+ *   block_table [n_seqs, max_pages] int32.
+ * First the ended requests' pages, entries n_shared[s] .. ceil(n_cached[s] / page_size)
+ * of their rows, go on the stack, request by request in their order (entries that are no
+ * pages, outside [0, n_pages), are left out; the row itself is left as it is).  Then
+ * every other sequence gets what it lacks, entries ceil(n_cached / page_size) ..
+ * ceil((n_cached + n_new) / page_size) of its row, from the top of the stack, sequence by
+ * sequence and entry by entry.  Nothing else of the table is written.
+ *   q_off  [n_seqs + 1] out, kv_len [n_seqs] out: as lora_paged_kv_t takes them (kv_len =
+ *          n_cached + n_new; 0 and no rows for an ended request).
+ *   slots  [T] int64 out or NULL: the place of each row, block_table entry x page_size +
+ *          row in the page; -1 for rows from q_off[n_seqs] on and for missing pages.
+ *   pos    [T] int32 out or NULL: the position of each row; -1 from q_off[n_seqs] on.
+ *   n_free_out [1] int32 out.
+ * kv_len may be n_cached, and n_free_out may be n_free: a decode loop then calls it with the same
+ * arrays in every step.  With arrays apart, equal calls give equal results.
+ * Errors: rows past T are dropped, a page past max_pages is not taken, a length or n_free
+ * outside its range is cut, pages given back past free_cap are lost (LORA_DEVERR_BAD_LEN); with
+ * no page left the entry becomes -1 (LORA_DEVERR_NO_PAGE); a row whose page is missing
+ * has slot -1 (LORA_DEVERR_BAD_PAGE).
+ * Shapes: page_size 8, 16, 32, 64, 128 or 256; 1 <= n_seqs <= LORA_MAX_SEQS; 0 <= T <=
+ * LORA_MAX_TOKENS; max_pages as in lora_paged_kv_t; free_cap >= 1.
+ * Workspace: lora_batch_plan_workspace_bytes(n_seqs).
+ */
+size_t lora_batch_plan_workspace_bytes(int32_t n_seqs);
+lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
+                              const int32_t* n_shared, int32_t n_seqs, int32_t T,
+                              int32_t page_size, int32_t max_pages, int32_t n_pages,
+                              int32_t* free_pages, int32_t free_cap, const int32_t* n_free,
+                              int32_t* block_table, int32_t* q_off, int32_t* kv_len,
+                              int64_t* slots, int32_t* pos, int32_t* n_free_out, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * The cache in 8 bits: half the bytes of the one above, for the same calls.
+ *   kv->k_cache, kv->v_cache [n_pages, n_kv_heads, page_size, head_dim] e4m3 codes.
+ *   k_scale, v_scale [n_pages, n_kv_heads, page_size / B] uint8: one scale for B = 16 tokens
+ *            (8 in pages of 8) of a head.  Byte b stands for 2^(b - 127), b = 1 .. 253; 0
+ *            reads as 1, so zero-filled memory is a valid cache of zeros, and 254, 255 as 253.
+ *   value    = code * 2^(b - 127), the same in every call; exact in bf16.
+ * A power of two is enough of a scale: e4m3 is a floating type, so the scale's fraction
+ * would not make its rounding finer.  Caches, scales and rows 16-byte aligned.
+ *
+ * lora_kv_append_8bit: lora_kv_append with k and v rounded once, from the rotated fp32
+ * value, to e4m3 at the scale of their block: the least power of two that the block's
+ * largest new value fits under with 448 codes, or the scale the block has from earlier calls if
+ * that is larger (a block has one if its first position is not among the call's rows).
+ * Where the scale grows, the codes of the block's earlier rows are moved to it, which is exact
+ * but for codes that become subnormal.  So scales do not depend on how tokens are
+ * divided over calls.  An infinite value becomes the largest code, NaN stays NaN.  No two sequences
+ * of a call may append to one block.
+ *
+ * lora_attn_paged_8bit, lora_attn_prefix_8bit: lora_attn_paged and lora_attn_prefix over
+ * it; the same masks, workspaces (lora_attn_workspace_bytes) and errors.  Weights and q enter their products
+ * as sums of e4m3 terms where the keys stand in the MMA's M (where lora_attn_paged has
+ * the weights as a pair of bf16): three terms of a weight, exact to 2^-12 of itself and
+ * 2^-23 of the row's largest (at the largest v_scale seen), and two of q, exact to 2^-17
+ * of its row's largest value.  Elsewhere codes become bf16 values, exactly, and the weights are
+ * one bf16, as in lora_attn_paged.  Scales of blocks that no row sees may hold anything.
+ */
+lora_status_t lora_kv_append_8bit(const lora_paged_kv_t* kv, uint8_t* k_scale, uint8_t* v_scale,
+                                  const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride,
+                                  int32_t n_q_heads, const float* cos_sin, int32_t n_pos,
+                                  int32_t rot_dim, const int32_t* pos, int32_t n_axes,
+                                  const int32_t* axis_pairs, int32_t interleaved, void* q_out,
+                                  int64_t q_out_stride, void* ws, size_t ws_bytes, void* stream);
+lora_status_t lora_attn_paged_8bit(const lora_paged_kv_t* kv, const uint8_t* k_scale,
+                                   const uint8_t* v_scale, const void* q, int64_t q_stride,
+                                   int32_t n_q_heads, float scale, int32_t window,
+                                   int32_t n_sink, void* out, int64_t out_stride, void* ws,
+                                   size_t ws_bytes, void* stream);
+lora_status_t lora_attn_prefix_8bit(const lora_paged_kv_t* kv, const uint8_t* k_scale,
+                                    const uint8_t* v_scale, const int32_t* group_off,
+                                    const int32_t* prefix_len, int32_t n_groups, const void* q,
+                                    int64_t q_stride, int32_t n_q_heads, float scale, void* out,
+                                    int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, copies the workspace error word to *device_err and

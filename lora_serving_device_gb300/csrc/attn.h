@@ -24,9 +24,29 @@ struct AppendArgs {
   void* q_out;
   int64_t q_out_stride;
   uint32_t* err;
+  uint8_t *k_scale, *v_scale;  // of a cache in 8 bits
 };
 // see k_kv_append.cu
 cudaError_t launch_kv_append(const lora_paged_kv_t& kv, const AppendArgs& a, cudaStream_t st);
+// see k_kv_append_8bit.cu
+cudaError_t launch_kv_append_8bit(const lora_paged_kv_t& kv, const AppendArgs& a, cudaStream_t st);
+
+struct PlanArgs {
+  const int32_t *n_cached, *n_new, *n_shared;
+  int n_seqs, T, page_size, lg_page, max_pages, n_pages;
+  int32_t* free_pages;
+  int free_cap;
+  const int32_t* n_free;
+  int32_t *block_table, *q_off, *kv_len;
+  int64_t* slots;
+  int32_t *pos, *n_free_out;
+  uint32_t* err;
+  int32_t* top;        // pages on the stack before any is taken
+  int32_t* take_off;   // [n_seqs] pages that the sequences before take
+  bool fill_here;      // one kernel does all
+};
+// see k_batch_plan.cu
+cudaError_t launch_batch_plan(const PlanArgs& a, cudaStream_t st);
 
 struct AttnArgs {
   const void* q;
@@ -39,10 +59,13 @@ struct AttnArgs {
   void* out;
   int64_t out_stride;
   void* ws;
+  const uint8_t *k_scale, *v_scale;  // of a cache in 8 bits, or null
 };
 // see k_attn.cu
 cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st,
                         const DeviceInfo& dev);
+// see k_attn_8bit.cu
+cudaError_t launch_attn_8bit(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st);
 size_t attn_ws_bytes(const lora_paged_kv_t& kv, int n_q_heads, int n_groups);
 
 }  // namespace lora

@@ -15,16 +15,13 @@
 // 5238 tokens with 28 / 4 heads and three axes: 21.4 us, 4.6 TB/s (two heads a
 // batch, for registers: four 23.0 us); 64 tokens 3.5 us.
 #include "attn.cuh"
+#include "rotary.cuh"
 
 namespace lora {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 2;
-
-struct Rot {
-  float c[8], s[8];
-};
 
 template <bool kInter>
 __device__ __forceinline__ void rotate(uint4& lo, uint4& hi, const Rot& r) {
@@ -88,40 +85,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const lora_paged_kv
   if (s < 0) return;
   const int p = kv.kv_len[s] - kv.q_off[s + 1] + t;
   Rot r;
-  if (rotates) {
-    auto pos_of = [&](int axis) {
-      const int x = a.pos != nullptr ? a.pos[static_cast<int64_t>(axis) * kv.T + t] : p;
-      if (x >= 0 && x < a.n_pos) return x;
-      flag_error(a.err, LORA_DEVERR_BAD_POS);
-      return -1;
-    };
-    auto axis_of = [&](int pair) {
-      int ax = 0;
-#pragma unroll
-      for (int i = 0; i < LORA_MAX_POS_AXES - 1; ++i) ax += pair >= a.axis_end[i] ? 1 : 0;
-      return ax < a.n_axes ? ax : a.n_axes - 1;
-    };
-    const int ax = axis_of(8 * u);
-    if (ax == axis_of(8 * u + 7)) {
-      const int x = pos_of(ax);
-      if (x >= 0) {
-        const float* row = a.cos_sin + static_cast<int64_t>(x) * a.rot_dim + 8 * u;
-        load8(row, r.c);
-        load8(row + a.rot_dim / 2, r.s);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r.c[j] = 1.f, r.s[j] = 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int x = pos_of(axis_of(8 * u + j));
-        const float* row = a.cos_sin + static_cast<int64_t>(x < 0 ? 0 : x) * a.rot_dim + 8 * u + j;
-        r.c[j] = x < 0 ? 1.f : row[0];
-        r.s[j] = x < 0 ? 0.f : row[a.rot_dim / 2];
-      }
-    }
-  }
+  if (rotates) load_rot(a, kv.T, t, p, u, r);
 
   // the row's place in the cache: element offset of its head 0, or -1
   int64_t place = -1;

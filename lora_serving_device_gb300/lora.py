@@ -11,6 +11,7 @@ fallback: if the library is missing or the device is not sm_103, calls fail.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import functools
 import os
@@ -29,7 +30,7 @@ OP_SGMV_SHRINK, OP_SGMV_EXPAND, OP_LINEAR_FUSED, OP_BASE_GEMM_EXPAND = 3, 4, 5, 
 OP_LINEAR_FUSED_4BIT = 7
 OP_LINEAR_FUSED_RAGGED = 8
 DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_BAD_RANK, DEVERR_BOUNDS = 0x1, 0x2, 0x4, 0x8
-DEVERR_BAD_PAGE, DEVERR_BAD_POS, DEVERR_BAD_LEN = 0x10, 0x20, 0x40
+DEVERR_BAD_PAGE, DEVERR_BAD_POS, DEVERR_BAD_LEN, DEVERR_NO_PAGE = 0x10, 0x20, 0x40, 0x80
 RAGGED_RANKS = (8, 16, 32, 64, 128)
 MAX_SLOTS, MAX_TOKENS, MAX_KSPLIT = 16384, 1 << 20, 64
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -41,6 +42,8 @@ EXPORTS = ("lora_workspace_bytes", "lora_build_segments", "lora_bgmv_shrink", "l
            "lora_slot_upload", "lora_bgmv_adapter_ragged", "lora_linear_fused_ragged",
            "lora_quantize_base_4bit", "lora_base_gemm_4bit_splitk", "lora_linear_fused_4bit",
            "lora_attn_workspace_bytes", "lora_kv_append", "lora_attn_paged", "lora_attn_prefix",
+           "lora_batch_plan_workspace_bytes", "lora_batch_plan", "lora_kv_append_8bit",
+           "lora_attn_paged_8bit", "lora_attn_prefix_8bit",
            "lora_debug_gemm_wait_timeout", "lora_get_error", "lora_status_string")
 
 
@@ -96,6 +99,12 @@ _SIGS = {
     "lora_kv_append": (_I, [_P, _P, _L, _P, _L, _P, _L, _I, _P, _I, _I, _P, _I, _P, _I, _P, _L, _P, _Z, _P]),
     "lora_attn_paged": (_I, [_P, _P, _L, _I, _F, _I, _I, _P, _L, _P, _Z, _P]),
     "lora_attn_prefix": (_I, [_P, _P, _P, _I, _P, _L, _I, _F, _P, _L, _P, _Z, _P]),
+    "lora_batch_plan_workspace_bytes": (_Z, [_I]),
+    "lora_batch_plan": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "lora_kv_append_8bit": (_I, [_P, _P, _P, _P, _L, _P, _L, _P, _L, _I, _P, _I, _I, _P, _I, _P, _I, _P, _L, _P,
+                                 _Z, _P]),
+    "lora_attn_paged_8bit": (_I, [_P, _P, _P, _P, _L, _I, _F, _I, _I, _P, _L, _P, _Z, _P]),
+    "lora_attn_prefix_8bit": (_I, [_P, _P, _P, _P, _P, _I, _P, _L, _I, _F, _P, _L, _P, _Z, _P]),
     "lora_get_error": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "lora_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -262,6 +271,36 @@ def lora_attn_prefix(kv, group_off, prefix_len, n_groups, q, q_stride, n_q_heads
                      ws, ws_bytes, stream):
     return _call("lora_attn_prefix", kv, group_off, prefix_len, n_groups, q, q_stride, n_q_heads, scale, out,
                  out_stride, ws, ws_bytes, stream)
+
+
+def lora_batch_plan_workspace_bytes(n_seqs):
+    return _call("lora_batch_plan_workspace_bytes", n_seqs)
+
+
+def lora_batch_plan(n_cached, n_new, n_shared, n_seqs, T, page_size, max_pages, n_pages, free_pages, free_cap,
+                    n_free, block_table, q_off, kv_len, slots, pos, n_free_out, ws, ws_bytes, stream):
+    return _call("lora_batch_plan", n_cached, n_new, n_shared, n_seqs, T, page_size, max_pages, n_pages,
+                 free_pages, free_cap, n_free, block_table, q_off, kv_len, slots, pos, n_free_out, ws, ws_bytes,
+                 stream)
+
+
+def lora_kv_append_8bit(kv, k_scale, v_scale, q, q_stride, k, k_stride, v, v_stride, n_q_heads, cos_sin, n_pos,
+                        rot_dim, pos, n_axes, axis_pairs, interleaved, q_out, q_out_stride, ws, ws_bytes, stream):
+    return _call("lora_kv_append_8bit", kv, k_scale, v_scale, q, q_stride, k, k_stride, v, v_stride, n_q_heads,
+                 cos_sin, n_pos, rot_dim, pos, n_axes, axis_pairs, interleaved, q_out, q_out_stride, ws, ws_bytes,
+                 stream)
+
+
+def lora_attn_paged_8bit(kv, k_scale, v_scale, q, q_stride, n_q_heads, scale, window, n_sink, out, out_stride,
+                         ws, ws_bytes, stream):
+    return _call("lora_attn_paged_8bit", kv, k_scale, v_scale, q, q_stride, n_q_heads, scale, window, n_sink,
+                 out, out_stride, ws, ws_bytes, stream)
+
+
+def lora_attn_prefix_8bit(kv, k_scale, v_scale, group_off, prefix_len, n_groups, q, q_stride, n_q_heads, scale,
+                          out, out_stride, ws, ws_bytes, stream):
+    return _call("lora_attn_prefix_8bit", kv, k_scale, v_scale, group_off, prefix_len, n_groups, q, q_stride,
+                 n_q_heads, scale, out, out_stride, ws, ws_bytes, stream)
 
 
 def lora_get_error(ws, stream):
@@ -630,12 +669,14 @@ class PagedKV:
     any one sequence has at most max_q_len (default T).  The object keeps the tensors and
     their addresses: update them in place from step to step (a decode loop needs no other
     object), make a new one when T or a tensor changes."""
+    bits, _types = 16, ("bfloat16",)
 
     def __init__(self, k_cache, v_cache, block_table, q_off, kv_len, T, max_q_len=None):
         import torch
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
-                raise TypeError(f"{name}: contiguous bf16 [n_pages, n_kv_heads, page_size, head_dim]")
+            if str(t.dtype)[6:] not in self._types or t.dim() != 4 or not t.is_contiguous():
+                raise TypeError(f"{name}: contiguous {' or '.join(self._types)} [n_pages, n_kv_heads, page_size, "
+                                "head_dim]")
         for name, t in (("block_table", block_table), ("q_off", q_off), ("kv_len", kv_len)):
             if t.dtype != torch.int32 or not t.is_contiguous():
                 raise TypeError(f"{name}: contiguous int32")
@@ -661,6 +702,11 @@ class PagedKV:
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self._current_device = torch._C._cuda_getDevice
 
+    def needs(self, bits):
+        """A call for caches of `bits` takes no others."""
+        if self.bits != bits:
+            raise TypeError(f"the call takes a cache of {bits} bits, not of {self.bits}")
+
     def rows(self, x, n_heads, what):
         """Checks x [T, n_heads, head_dim] bf16 and returns its distance between tokens."""
         T, heads, d = self.T, n_heads, self.head_dim
@@ -682,9 +728,38 @@ class PagedKV:
         return self._current_stream(self._device) if stream is None else stream.cuda_stream
 
 
+class PagedKV8bit(PagedKV):
+    """A paged cache in 8 bits: k_cache, v_cache [n_pages, n_kv_heads, page_size, head_dim]
+    float8_e4m3fn (or uint8, the same codes), k_scale, v_scale [n_pages, n_kv_heads,
+    page_size / B] uint8 with B = min(16, page_size): byte b stands for 2^(b - 127).  Zeros
+    are a valid empty cache.  Otherwise as PagedKV."""
+    bits, _types = 8, ("float8_e4m3fn", "uint8")
+
+    def __init__(self, k_cache, v_cache, k_scale, v_scale, block_table, q_off, kv_len, T, max_q_len=None):
+        super().__init__(k_cache, v_cache, block_table, q_off, kv_len, T, max_q_len)
+        n_pages, n_kv_heads, page_size, _ = k_cache.shape
+        shape = (n_pages, n_kv_heads, page_size // min(16, page_size))
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if str(t.dtype)[6:] not in ("uint8", "float8_e8m0fnu") or t.shape != shape or not t.is_contiguous() or \
+                    t.device != k_cache.device:
+                raise TypeError(f"{name}: contiguous uint8 {list(shape)} on the cache's device")
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.scales = (_ptr(k_scale), _ptr(v_scale))
+
+    @classmethod
+    def empty_cache(cls, n_pages, n_kv_heads, page_size, head_dim, device="cuda"):
+        """k_cache, v_cache, k_scale, v_scale of a cache of zeros."""
+        import torch
+        codes = [torch.zeros(n_pages, n_kv_heads, page_size, head_dim, dtype=torch.uint8, device=device)
+                 .view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.zeros(n_pages, n_kv_heads, page_size // min(16, page_size), dtype=torch.uint8, device=device)
+                  for _ in range(2)]
+        return (*codes, *scales)
+
+
 def attn_workspace(kv, n_q_heads, n_groups=0):
     """A zero-filled workspace for attn_paged_t (n_groups = 0), attn_prefix_t (n_groups >= 1)
-    and kv_append_t over `kv`."""
+    and kv_append_t over `kv`, and for their 8-bit forms over a PagedKV8bit."""
     import torch
     n = lora_attn_workspace_bytes(kv.ref, n_q_heads, n_groups)
     return torch.zeros(max(int(n), 16), dtype=torch.uint8, device=kv.k_cache.device)
@@ -704,13 +779,8 @@ def _c_counts(counts):
     return (ctypes.c_int32 * len(counts))(*counts)
 
 
-def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
-                stream=None):
-    """Rotates q [T, n_q_heads, D] and k [T, n_kv_heads, D] by position, writes k and v into
-    kv's cache and returns the rotated q (a new tensor unless q_out is given; q itself is
-    allowed).  q None: keys and values only.  cos_sin [n_pos, rot_dim] fp32 (rope_table) or
-    None for no rotation.  pos: None (the position in the cache), [T], or [n_axes, T] with
-    axis_pairs, the rotated pairs of each axis."""
+def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream):
+    """Checks the arguments of an append; the C call's, from q to the stream, and q_out."""
     n_q = q_stride = q_out_stride = 0
     if q is not None:
         n_q = q.shape[1]
@@ -737,16 +807,37 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
             raise ValueError(f"axis_pairs: {len(axis_pairs)} counts for {n_axes} axes")
         pairs = _c_counts(tuple(axis_pairs))
     hk = kv.n_kv_heads
-    check(load().lora_kv_append(kv.ref, _ptr(q), q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(),
-                                kv.rows(v, hk, "v"), n_q, _ptr(cos_sin), n_pos, rot, _ptr(pos), n_axes, pairs,
-                                1 if interleaved else 0, _ptr(q_out), q_out_stride, ws.data_ptr(),
-                                ws.numel(), kv.stream(stream)), "lora_kv_append")
+    return (_ptr(q), q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(), kv.rows(v, hk, "v"), n_q,
+            _ptr(cos_sin), n_pos, rot, _ptr(pos), n_axes, pairs, 1 if interleaved else 0, _ptr(q_out), q_out_stride,
+            ws.data_ptr(), ws.numel(), kv.stream(stream)), q_out
+
+
+def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
+                stream=None):
+    """Rotates q [T, n_q_heads, D] and k [T, n_kv_heads, D] by position, writes k and v into
+    kv's cache and returns the rotated q (a new tensor unless q_out is given; q itself is
+    allowed).  q None: keys and values only.  cos_sin [n_pos, rot_dim] fp32 (rope_table) or
+    None for no rotation.  pos: None (the position in the cache), [T], or [n_axes, T] with
+    axis_pairs, the rotated pairs of each axis."""
+    kv.needs(16)
+    args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
+    check(load().lora_kv_append(kv.ref, *args), "lora_kv_append")
     return q_out
 
 
-def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
-    """Causal attention of q [T, n_q_heads, D] over kv's cache (lora_attn_paged); scale
-    defaults to D^-0.5, window 0 is none."""
+def kv_append_8bit_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
+                     stream=None):
+    """kv_append_t into a PagedKV8bit (lora_kv_append_8bit): k and v become e4m3 codes, at one
+    scale for each block of tokens and head, which grows as the block's values do."""
+    kv.needs(8)
+    args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
+    check(load().lora_kv_append_8bit(kv.ref, *kv.scales, *args), "lora_kv_append_8bit")
+    return q_out
+
+
+def _attn_args(kv, q, ws, scale, out, stream):
+    """Checks the rows of an attention call; the C call's arguments from q to the scale, those
+    from out to the stream, and out."""
     n_q = q.shape[1]
     q_stride = kv.rows(q, n_q, "q")
     if out is None:
@@ -754,32 +845,107 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
         out_stride = n_q * kv.head_dim
     else:
         out_stride = kv.rows(out, n_q, "out")
-    check(load().lora_attn_paged(kv.ref, q.data_ptr(), q_stride, n_q,
-                                 kv.head_dim ** -0.5 if scale is None else scale, window, n_sink,
-                                 out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(), kv.stream(stream)),
-          "lora_attn_paged")
+    return ((q.data_ptr(), q_stride, n_q, kv.head_dim ** -0.5 if scale is None else scale),
+            (out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(), kv.stream(stream)), out)
+
+
+def _group_args(kv, group_off, prefix_len):
+    n_groups = prefix_len.numel()
+    for name, t, n in (("group_off", group_off, n_groups + 1), ("prefix_len", prefix_len, n_groups)):
+        if t.dtype is not kv._i32 or t.numel() != n or not t.is_contiguous() or t.get_device() != kv._device:
+            raise TypeError(f"{name}: contiguous int32 [{n}] on the cache's device")
+    return group_off.data_ptr(), prefix_len.data_ptr(), n_groups
+
+
+def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
+    """Causal attention of q [T, n_q_heads, D] over kv's cache (lora_attn_paged); scale
+    defaults to D^-0.5, window 0 is none."""
+    kv.needs(16)
+    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
+    check(load().lora_attn_paged(kv.ref, *rows, window, n_sink, *rest), "lora_attn_paged")
+    return out
+
+
+def attn_paged_8bit_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
+    """attn_paged_t over a PagedKV8bit (lora_attn_paged_8bit)."""
+    kv.needs(8)
+    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
+    check(load().lora_attn_paged_8bit(kv.ref, *kv.scales, *rows, window, n_sink, *rest), "lora_attn_paged_8bit")
     return out
 
 
 def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
     """attn_paged_t for groups of sequences that share a prefix (lora_attn_prefix):
     group_off [n_groups + 1], prefix_len [n_groups] int32 on the device."""
-    n_q = q.shape[1]
-    q_stride = kv.rows(q, n_q, "q")
-    n_groups = prefix_len.numel()
-    for name, t, n in (("group_off", group_off, n_groups + 1), ("prefix_len", prefix_len, n_groups)):
-        if t.dtype is not kv._i32 or t.numel() != n or not t.is_contiguous() or t.get_device() != kv._device:
-            raise TypeError(f"{name}: contiguous int32 [{n}] on the cache's device")
+    kv.needs(16)
+    groups = _group_args(kv, group_off, prefix_len)
+    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
+    check(load().lora_attn_prefix(kv.ref, *groups, *rows, *rest), "lora_attn_prefix")
+    return out
+
+
+def attn_prefix_8bit_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
+    """attn_prefix_t over a PagedKV8bit (lora_attn_prefix_8bit)."""
+    kv.needs(8)
+    groups = _group_args(kv, group_off, prefix_len)
+    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
+    check(load().lora_attn_prefix_8bit(kv.ref, *kv.scales, *groups, *rows, *rest), "lora_attn_prefix_8bit")
+    return out
+
+
+class BatchPlan(collections.namedtuple("BatchPlan", "q_off kv_len slots pos n_free")):
+    """What batch_plan_t makes: q_off [n_seqs + 1], kv_len [n_seqs], pos [T] and n_free [1]
+    int32, slots [T] int64, on the device."""
+    __slots__ = ()
+
+    @classmethod
+    def empty(cls, n_seqs, T, device="cuda"):
+        import torch
+        return cls(*(torch.empty(n, dtype=t, device=device)
+                     for n, t in ((n_seqs + 1, torch.int32), (n_seqs, torch.int32), (T, torch.int64),
+                                  (T, torch.int32), (1, torch.int32))))
+
+
+def batch_plan_workspace(n_seqs, device="cuda"):
+    """A zero-filled workspace for batch_plan_t."""
+    import torch
+    return torch.zeros(lora_batch_plan_workspace_bytes(n_seqs), dtype=torch.uint8, device=device)
+
+
+def batch_plan_t(block_table, n_cached, n_new, free_pages, n_free, page_size, n_pages, ws, n_shared=None, T=None,
+                 out=None, stream=None):
+    """A batch's block table, offsets, lengths, slots and positions from the lengths of its
+    requests, on the GPU (lora_batch_plan).  block_table [n_seqs, max_pages], n_cached,
+    n_new, n_shared [n_seqs], free_pages and n_free [1] int32 on the device: new pages are
+    taken from the top of the stack free_pages[:n_free], a request with n_new < 0 gives its
+    pages back.  Writes block_table and free_pages; returns a BatchPlan of T rows, or `out`,
+    one that the caller keeps (its kv_len may be n_cached, its n_free may be n_free: then
+    a decode loop calls this with the same arrays in every step; slots or pos may be None)."""
+    import torch
+    n_seqs, dev, i32 = n_cached.numel(), block_table.device, torch.int32
     if out is None:
-        out = _on(stream, kv.new_like, q)
-        out_stride = n_q * kv.head_dim
-    else:
-        out_stride = kv.rows(out, n_q, "out")
-    check(load().lora_attn_prefix(kv.ref, group_off.data_ptr(), prefix_len.data_ptr(), n_groups,
-                                  q.data_ptr(), q_stride, n_q,
-                                  kv.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
-                                  out_stride, ws.data_ptr(), ws.numel(), kv.stream(stream)),
-          "lora_attn_prefix")
+        out = _on(stream, BatchPlan.empty, n_seqs, 0 if T is None else T, device=dev)
+    if T is None:
+        T = next((t.numel() for t in (out.slots, out.pos) if t is not None), 0)
+    for name, t, n, kind in (("block_table", block_table, None, i32), ("n_cached", n_cached, n_seqs, i32),
+                             ("n_new", n_new, n_seqs, i32), ("n_shared", n_shared, n_seqs, i32),
+                             ("free_pages", free_pages, None, i32), ("n_free", n_free, 1, i32),
+                             ("out.q_off", out.q_off, n_seqs + 1, i32), ("out.kv_len", out.kv_len, n_seqs, i32),
+                             ("out.slots", out.slots, T, torch.int64), ("out.pos", out.pos, T, i32),
+                             ("out.n_free", out.n_free, 1, i32)):
+        if t is None and name in ("n_shared", "out.slots", "out.pos"):
+            continue
+        if t.dtype is not kind or not t.is_contiguous() or t.device != dev or n not in (None, t.numel()):
+            raise TypeError(f"{name}: contiguous {kind}{'' if n is None else f' [{n}]'} on the block table's device")
+    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+        raise ValueError("block_table: [n_seqs, max_pages]")
+    if not block_table.is_cuda or torch.cuda.current_device() != dev.index:
+        raise ValueError(f"the block table is on {dev}; it has to be on the current CUDA device")
+    check(load().lora_batch_plan(_ptr(n_cached), _ptr(n_new), _ptr(n_shared), n_seqs, T, page_size,
+                                 block_table.shape[1], n_pages, _ptr(free_pages), free_pages.numel(), _ptr(n_free),
+                                 _ptr(block_table), _ptr(out.q_off), _ptr(out.kv_len), _ptr(out.slots),
+                                 _ptr(out.pos), _ptr(out.n_free), _ptr(ws), ws.numel(), _stream(stream)),
+          "lora_batch_plan")
     return out
 
 
