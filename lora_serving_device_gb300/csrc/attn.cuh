@@ -95,6 +95,7 @@ struct AttnParams {
   SplitItem* split;    // [CTA] the item that begins there and ends in another (prefill)
   float* prior;        // [T][n_q_heads][D] the prefix phase's result, fp32
   float* prior_lse;    // [T][n_q_heads] its log2-sum-exp
+  const uint8_t *k_scale, *v_scale;  // of a cache in 8 bits, or null
 };
 
 // One problem.

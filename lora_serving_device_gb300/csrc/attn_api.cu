@@ -73,8 +73,7 @@ lora_status_t attn_common(const lora_paged_kv_t* kv, const AttnArgs& a, bool bit
   if (kv->T == 0) return LORA_OK;
   DeviceInfo dev;
   if ((s = check_device(&dev)) != LORA_OK) return s;
-  const auto st = static_cast<cudaStream_t>(stream);
-  return (bits8 ? launch_attn_8bit(*kv, a, st) : launch_attn(*kv, a, st, dev)) == cudaSuccess
+  return launch_attn(*kv, a, static_cast<cudaStream_t>(stream), dev) == cudaSuccess
              ? LORA_OK
              : LORA_ERR_CUDA;
 }

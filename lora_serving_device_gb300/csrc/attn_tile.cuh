@@ -82,6 +82,10 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) 
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes) {
   return ((sbo_bytes >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29);
 }
+// The same with rows of `span` bytes, which the swizzle spans (128, 64, or 0: none).
+__host__ __device__ constexpr uint32_t desc_hi_span(uint32_t sbo_bytes, uint32_t span) {
+  return ((sbo_bytes >> 4) & 0x3FFFu) | (1u << 14) | ((span == 128 ? 2u : span == 64 ? 4u : 0u) << 29);
+}
 // D[tmem] (+)= A[smem] B[smem] and A[tmem] B[smem], descriptors in halves.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
                                        uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
@@ -90,6 +94,18 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
       "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same of 8-bit floating types.
+__device__ __forceinline__ void mma_ss_8bit(uint32_t d, uint32_t a_lo, uint32_t a_hi,
+                                            uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -177,8 +193,9 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, 
 // larger one).  The page ids of 32 boxes are looked up at once, a lane each, and
 // the next 32 ahead of their use.  Pages that no row sees are not touched.  A
 // page that is missing is asked for past the cache's end, where the tensor map
-// reads zeros.  One warp; the tiles of a segment in their order.
-template <int D>
+// reads zeros.  One warp; the tiles of a segment in their order.  kElem: bytes of
+// a value.
+template <int D, int kElem = 2>
 struct TileLoader {
   int page, lg_page, box, boxes, per;
   uint64_t policy;
@@ -246,7 +263,7 @@ struct TileLoader {
   __device__ __forceinline__ uint32_t bytes(int at) const {  // of all lanes' boxes
     return __popc(__ballot_sync(0xffffffffu, at >= 0)) * box_bytes();
   }
-  __device__ __forceinline__ uint32_t box_bytes() const { return static_cast<uint32_t>(box) * D * 2; }
+  __device__ __forceinline__ uint32_t box_bytes() const { return static_cast<uint32_t>(box) * D * kElem; }
   __device__ __forceinline__ void load(const CUtensorMap* tm, uint64_t* full, uint8_t* dst, int at,
                                        uint32_t all) const {
     const int lane = threadIdx.x & 31;
@@ -343,6 +360,65 @@ __device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segmen
   named_bar(bar, cnt);
   __threadfence();
   return *flag != 0;
+}
+
+// The end of an item, or of this CTA's part of it, in the kernels that have few rows
+// to a key head (A in a row tile): 128 threads of named barrier `bar` write the rows from
+// `stage` [A][D], maxima m [A] (log2 units) and the four warps' sums red_sum [A], joined with
+// the parts of other CTAs by the last to arrive.
+template <int D, int A>
+__device__ __forceinline__ void finish_rows(const AttnParams& P, const Segment& g,
+                                            const float* stage, const float* m,
+                                            const float4* red_sum, int tid, int* last, int bar) {
+  float2* ml = reinterpret_cast<float2*>(P.part_ml);
+  const int vectors = g.t.n_rows * (D / 8);
+  bool write = true;
+  if (g.parts > 1) {
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
+#pragma unroll 1
+    for (int x = tid; x < vectors; x += 128) {
+      const int n = x / (D / 8), k = x % (D / 8) * 8;
+      store8(P.part + (slot * A + n) * D + k,
+             *reinterpret_cast<const float(*)[8]>(stage + n * D + k));
+      const float4 r = red_sum[n];
+      if (k == 0) ml[slot * A + n] = make_float2(m[n], r.x + r.y + r.z + r.w);
+    }
+    write = last_to_arrive(P, g, 0, tid == 0, last, bar, 128);
+  }
+#pragma unroll 1
+  for (int x = write ? tid : vectors; x < vectors; x += 128) {
+    const int n = x / (D / 8), k = x % (D / 8) * 8;
+    float o[8], top, sum;
+    if (g.parts == 1) {
+      const float4 r = red_sum[n];
+      top = m[n];
+      sum = r.x + r.y + r.z + r.w;
+      load8(stage + n * D + k, o);
+    } else {
+      // all parts, in their order
+      top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+      for (int q = 0; q < g.parts; ++q)
+        top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * A + n].x));
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] = 0.f;
+#pragma unroll 4
+      for (int q = 0; q < g.parts; ++q) {
+        const float2 v = __ldcg(&ml[part_slot(g, q) * A + n]);
+        const float4* from =
+            reinterpret_cast<const float4*>(P.part + (part_slot(g, q) * A + n) * D + k);
+        const float4 a = __ldcg(from), b = __ldcg(from + 1);
+        const float f = top == -INFINITY ? 0.f : exp2_fast(v.x - top);
+        sum += f * v.y;
+        o[0] += f * a.x; o[1] += f * a.y; o[2] += f * a.z; o[3] += f * a.w;
+        o[4] += f * b.x; o[5] += f * b.y; o[6] += f * b.z; o[7] += f * b.w;
+      }
+    }
+    const int r = g.t.row0 + n, tok = P.by_group(r);
+    const RowWriter<D> out(P, g.shared, g.tok0 + tok, g.head * P.group + r - tok * P.group, true,
+                           top, sum);
+    out.write8(k, o);
+  }
 }
 
 }  // namespace lora

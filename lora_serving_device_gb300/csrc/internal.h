@@ -146,6 +146,10 @@ bool encode_tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, ui
 // three outer dimensions); elements outside the tensor read as zero.
 bool encode_tensor_map_bf16_4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
                                const uint64_t (&strides)[3], const uint32_t (&box)[4]);
+// 4-D uint8 tensor map with any strides, and a swizzle over the box's inner extent (64 or
+// 128 bytes); elements outside the tensor read as zero.
+bool encode_tensor_map_u8_4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
+                             const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 // SGMV shrink on tensor cores (bf16, r in {64, 128}), see k_sgmv_tc.cu; the
 // same contract as launch_sgmv_shrink.  With `fold` (sgmv_shrink_tc_items
 // zeroed words) and ksplit > 1, split 0 of vpart ends as the sum of all

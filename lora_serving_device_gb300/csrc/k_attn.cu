@@ -9,6 +9,8 @@ namespace lora {
 
 cudaError_t launch_attn_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                const AttnParams& P, cudaStream_t st, const DeviceInfo& dev);
+cudaError_t launch_attn_decode_8bit(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                    const AttnParams& P, cudaStream_t st, const DeviceInfo& dev);
 cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                 const CUtensorMap& tm_v, const AttnParams& P, cudaStream_t st,
                                 const DeviceInfo& dev);
@@ -78,6 +80,19 @@ bool encode_cache_map(CUtensorMap* m, void* base, const lora_paged_kv_t& kv) {
   return encode_tensor_map_bf16_4d(m, base, dims, strides, box);
 }
 
+// One cache of codes, as [groups of 8 rows][8 rows][D codes]: the rows, of 128 or 64 bytes, are
+// what the swizzle spans, whole.
+bool encode_cache_map_8bit(CUtensorMap* m, void* base, const lora_paged_kv_t& kv) {
+  const uint64_t d = kv.head_dim;
+  const uint64_t groups =
+      static_cast<uint64_t>(kv.n_pages) * kv.n_kv_heads * (kv.page_size / 8);
+  const uint64_t dims[4] = {d, 8, 1, groups};
+  const uint64_t strides[3] = {d, d * 8, d * 8};
+  const uint32_t box[4] = {static_cast<uint32_t>(d), 8, 1,
+                           static_cast<uint32_t>((kv.page_size < kKeys ? kv.page_size : kKeys) / 8)};
+  return encode_tensor_map_u8_4d(m, base, dims, strides, box);
+}
+
 // q as [64-value halves][tokens][heads][64 values]: a box is whole tokens' query
 // heads of one key head, rows of 128 bytes.
 bool encode_q_map(CUtensorMap* m, const AttnArgs& a, const lora_paged_kv_t& kv, int group) {
@@ -98,9 +113,13 @@ size_t attn_ws_bytes(const lora_paged_kv_t& kv, int n_q_heads, int n_groups) {
 cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st,
                         const DeviceInfo& dev) {
   CUtensorMap tm_q, tm_k, tm_v;
-  if (!encode_cache_map(&tm_k, kv.k_cache, kv) || !encode_cache_map(&tm_v, kv.v_cache, kv))
+  const bool bits8 = a.k_scale != nullptr;
+  const auto encode = bits8 ? encode_cache_map_8bit : encode_cache_map;
+  if (!encode(&tm_k, kv.k_cache, kv) || !encode(&tm_v, kv.v_cache, kv))
     return cudaErrorInvalidValue;
   const Layout w = layout(kv, a.n_q_heads, a.n_groups);
+  if (bits8 && (w.shape[0].prefill || (a.n_groups > 0 && w.shape[1].prefill)))
+    return launch_attn_8bit(kv, a, st);
   uint8_t* base = static_cast<uint8_t*>(a.ws);
   AttnParams P = {};
   P.kv = kv;
@@ -126,6 +145,8 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.part_ml = reinterpret_cast<float*>(base + w.part_ml);
   P.prior = reinterpret_cast<float*>(base + w.prior);
   P.prior_lse = reinterpret_cast<float*>(base + w.prior_lse);
+  P.k_scale = a.k_scale;
+  P.v_scale = a.v_scale;
   for (int phase = a.n_groups > 0 ? 1 : 0; phase >= 0; --phase) {
     P.groups_phase = phase == 1;
     P.rows = w.shape[phase].rows;
@@ -150,7 +171,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
       if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;
       e = launch_attn_prefill(tm_q, tm_k, tm_v, P, st, dev);
     } else {
-      e = launch_attn_decode(tm_k, tm_v, P, st, dev);
+      e = (bits8 ? launch_attn_decode_8bit : launch_attn_decode)(tm_k, tm_v, P, st, dev);
     }
     if (e != cudaSuccess) return e;
   }

@@ -468,55 +468,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
       }
       named_bar(kBar, 128);
       if (late) pdl_wait();  // the prior parts are read, and the parts' memory is free
-      float2* ml = reinterpret_cast<float2*>(P.part_ml);
-      const int vectors = g.t.n_rows * (D / 8);
-      bool write = true;
-      if (g.parts > 1) {
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
-#pragma unroll 1
-        for (int x = st_tid; x < vectors; x += 128) {
-          const int n = x / (D / 8), k = x % (D / 8) * 8;
-          store8(P.part + (slot * A + n) * D + k,
-                 *reinterpret_cast<const float(*)[8]>(stage + n * D + k));
-          const float4 r = red_sum[n];
-          if (k == 0) ml[slot * A + n] = make_float2(M.m[wg][n], r.x + r.y + r.z + r.w);
-        }
-        write = last_to_arrive(P, g, 0, st_tid == 0, &M.last[wg], kBar, 128);
-      }
-#pragma unroll 1
-      for (int x = write ? st_tid : vectors; x < vectors; x += 128) {
-        const int n = x / (D / 8), k = x % (D / 8) * 8;
-        float o[8], top, sum;
-        if (g.parts == 1) {
-          const float4 r = red_sum[n];
-          top = M.m[wg][n];
-          sum = r.x + r.y + r.z + r.w;
-          load8(stage + n * D + k, o);
-        } else {
-          // all parts, in their order
-          top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-          for (int q = 0; q < g.parts; ++q)
-            top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * A + n].x));
-#pragma unroll
-          for (int y = 0; y < 8; ++y) o[y] = 0.f;
-#pragma unroll 4
-          for (int q = 0; q < g.parts; ++q) {
-            const float2 v = __ldcg(&ml[part_slot(g, q) * A + n]);
-            const float4* from =
-                reinterpret_cast<const float4*>(P.part + (part_slot(g, q) * A + n) * D + k);
-            const float4 a = __ldcg(from), b = __ldcg(from + 1);
-            const float f = top == -INFINITY ? 0.f : exp2_fast(v.x - top);
-            sum += f * v.y;
-            o[0] += f * a.x; o[1] += f * a.y; o[2] += f * a.z; o[3] += f * a.w;
-            o[4] += f * b.x; o[5] += f * b.y; o[6] += f * b.z; o[7] += f * b.w;
-          }
-        }
-        const int r = g.t.row0 + n, tok = P.by_group(r);
-        const RowWriter<D> out(P, g.shared, g.tok0 + tok,
-                               g.head * P.group + r - tok * P.group, true, top, sum);
-        out.write8(k, o);
-      }
+      finish_rows<D, A>(P, g, stage, M.m[wg], red_sum, st_tid, &M.last[wg], kBar);
       named_bar(kBar, 128);  // the sums and the limits are free
     }
   }
