@@ -64,8 +64,6 @@ struct AttnArgs {
 // see k_attn.cu
 cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st,
                         const DeviceInfo& dev);
-// see k_attn_8bit.cu
-cudaError_t launch_attn_8bit(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream_t st);
 size_t attn_ws_bytes(const lora_paged_kv_t& kv, int n_q_heads, int n_groups);
 
 }  // namespace lora

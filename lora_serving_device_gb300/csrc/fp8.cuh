@@ -35,4 +35,21 @@ __device__ __forceinline__ float2 unpack2_e4m3(uint32_t two) {
       __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3)));
 }
 
+// Two codes (the low 16 bits) as f16, exactly; two f16 times two; two fp32 rounded to f16.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
+  return h.x | static_cast<uint32_t>(h.y) << 16;
+}
+__device__ __forceinline__ uint32_t scale2_f16(uint32_t x, uint32_t f) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+
 }  // namespace lora

@@ -30,7 +30,6 @@
 
 #include "attn.cuh"
 #include "attn_tile.cuh"
-#include "fp8.cuh"
 #include "ptx.cuh"
 
 namespace lora {
@@ -39,8 +38,6 @@ namespace {
 constexpr int kRing = 4;      // segments that the producer may run ahead
 constexpr float kTop = 5.f;   // log2 of a row's largest weight when its reference is set
 constexpr float kTerm = 16.f; // a term of P against the one before
-
-constexpr int kScaleRing = 16;  // tiles whose scales are there ahead
 
 // A rows of a row tile: 4, 8 or 16.  N is their number in Q K^T and kPV the columns of P
 // and O (three terms of A rows, in whole planes of 16).  W softmax warpgroups take the
@@ -75,17 +72,15 @@ struct Misc {
   // are apart because no barrier of the warpgroup lies between the last tile's
   // maxima and the sums: one warp may add up while another still reads maxima.
   float4 red_max[W][A], red_sum[W][A];
-  int red_scale[W][4];  // the warps' largest exponents of values in a tile
   float m[W][A];
   float q_scale[W][La::N];
-  uint8_t k_scale[kScaleRing][16], v_scale[kScaleRing][16];  // bytes of a tile's blocks
+  ScaleRing scales;
   int row_hi[W][A], row_lo[W][A];
   uint64_t full_k[kStages], full_v[kStages], empty[kStages];
   uint64_t s_full[W][La::kSBufs], s_empty[W][La::kSBufs];
   uint64_t p_full[W][La::kPBufs], p_done[W][La::kPBufs];
   uint64_t q_full[W], o_empty[W];
   uint64_t seg_full[kRing], seg_empty[kRing];
-  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
   uint32_t tmem;
   int abort;
   int last[W];
@@ -137,10 +132,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
       ptx::mbar_init(&M.seg_full[i], 1);
       ptx::mbar_init(&M.seg_empty[i], 6);
     }
-    for (int i = 0; i < kScaleRing; ++i) {
-      ptx::mbar_init(&M.sc_full[i], 1);
-      ptx::mbar_init(&M.sc_empty[i], 4);
-    }
+    init_scales(M.scales, 4);
     M.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -295,57 +287,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     __syncwarp();
   } else if (warp == 10) {
     // ---------------- scales ----------------------------------------------
-    // A lane to a block of a tile: as many tiles at once as 32 lanes have blocks of, and
-    // the next ones' page ids on their way beside them.
-    const int block = min(P.kv.page_size, kScaleBlock), per_tile = kKeys / block;
-    const int at_once = 32 / per_tile, lg_block = block == 8 ? 3 : 4;
-    const int page_blocks = P.kv.page_size >> lg_block;
-    bool ok = true;
-    for (int sg = 0; ok; ++sg) {
-      ok = wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
-      if (!ok) break;
-      const Segment g = M.ring[sg % kRing];
-      if (g.n == 0) break;
-      bool seen;
-      int key0;
-      auto fetch = [&](int i0) {
-        const int v = (g.first + i0 + lane / per_tile) * kKeys + lane % per_tile * block;
-        key0 = v < g.t.sink_places ? v : window_key(g.t, v);
-        seen = i0 + lane / per_tile < g.n &&
-               ((key0 <= g.t.vis_hi && key0 + block - 1 >= g.t.vis_lo) || v < g.t.n_sink);
-        return seen ? P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages +
-                                       (key0 >> P.lg_page)]
-                    : -1;
-      };
-      int id = fetch(0);
-      for (int i0 = 0; i0 < g.n && ok; i0 += at_once) {
-        // what no row sees leaves the scores as they are and R where it is
-        int kb = 127, vb = 1;
-        if (seen && id >= 0 && id < P.kv.n_pages) {
-          const int64_t at = (static_cast<int64_t>(id) * P.kv.n_kv_heads + g.head) * page_blocks +
-                             ((key0 & (P.kv.page_size - 1)) >> lg_block);
-          kb = scale_read(P.k_scale[at]);
-          vb = scale_read(P.v_scale[at]);
-        }
-        if (i0 + at_once < g.n) id = fetch(i0 + at_once);
-        const int last = min(at_once, g.n - i0);
-        const uint32_t tile = g.tile0 + i0;
-        for (int i = 0; i < last && ok; ++i)
-          if (tile + i >= kScaleRing)
-            ok = wait_all(&M.sc_empty[(tile + i) % kScaleRing], (((tile + i) / kScaleRing) & 1) ^ 1,
-                          abort_f);
-        if (!ok) break;
-        if (lane / per_tile < last) {
-          const int slot = (tile + lane / per_tile) % kScaleRing;
-          M.k_scale[slot][lane % per_tile] = static_cast<uint8_t>(kb);
-          M.v_scale[slot][lane % per_tile] = static_cast<uint8_t>(vb);
-        }
-        __syncwarp();
-        if (lane < last) ptx::mbar_arrive(&M.sc_full[(tile + lane) % kScaleRing]);
-        __syncwarp();
-      }
-      if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
-    }
+    fill_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
   } else {
     // ---------------- softmax and epilogue --------------------------------
     const int w = warp & 3;                 // TMEM lanes 32w .. 32w + 31
@@ -359,7 +301,6 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     const int kBar = 1 + wg;
     float4 *const red_max = M.red_max[wg], *const red_sum = M.red_sum[wg];
     uint8_t* const Pbase = smem + La::oP + wg * La::kPAll;
-    int* const red_scale = M.red_scale[wg];
     const int my_block = j / min(P.kv.page_size, kScaleBlock);
     const uint32_t tm_o = tmem_o + wg * kPV + lanes;
     uint64_t* const p_full = M.p_full[wg];
@@ -451,11 +392,11 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         const int key0 = window_key(g.t, v0), key = key0 + j;
         const uint32_t in_cta = g.tile0 + i;
         const uint32_t sc = in_cta % kScaleRing;
-        wait_quiet(&M.sc_full[sc], (in_cta / kScaleRing) & 1, abort_f);
-        const float kc = scale_of(M.k_scale[sc][my_block]) * c;
-        const int vb = M.v_scale[sc][my_block];
+        wait_quiet(&M.scales.full[sc], (in_cta / kScaleRing) & 1, abort_f);
+        const float kc = M.scales.k[sc][my_block] * c;
+        const int vb = M.scales.v[sc][my_block], top_v = M.scales.top[sc];
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.sc_empty[sc]);
+        if (lane == 0) ptx::mbar_arrive(&M.scales.empty[sc]);
         wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
@@ -479,7 +420,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
                        : -INFINITY;
         }
         // does a score exceed its reference by more than 8, or a scale R?
-        bool up = vb > R;
+        bool up = top_v > R;
 #pragma unroll
         for (int n = 0; n < A; ++n) up |= s[n] + neg[n] > 8.f;
         if (named_any(kBar, 128, up)) {
@@ -488,12 +429,9 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
             const float mx = warp_max(s[n]);
             if (lane == 0) reinterpret_cast<float*>(&red_max[n])[w] = mx;
           }
-          const int top_v = __reduce_max_sync(0xffffffffu, vb);
-          if (lane == 0) red_scale[w] = top_v;
           named_bar(kBar, 128);
-          const int R_now = max(max(max(red_scale[0], red_scale[1]), max(red_scale[2], red_scale[3])), R);
-          const float fac_v = R_now - R < 127 ? scale_of(127 - (R_now - R)) : 0.f;
-          R = R_now;
+          const float fac_v = top_v - R < 127 ? scale_of(127 - (top_v - R)) : 0.f;
+          R = top_v;
           float fac[A];
 #pragma unroll
           for (int n = 0; n < A; ++n) {

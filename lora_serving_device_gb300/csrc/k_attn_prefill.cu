@@ -39,9 +39,7 @@
 // LORA_DEVERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
-#include "attn.cuh"
-#include "attn_tile.cuh"
-#include "ptx.cuh"
+#include "attn_rows.cuh"
 
 namespace lora {
 namespace {
@@ -52,7 +50,6 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRegsMost = 192, kRegsLeast = 120;
 constexpr int kRing = 4;     // segments that the producer may run ahead
-constexpr int kHalf = 128;   // rows of a half in the MMA
 
 template <int D>
 struct Lay {
@@ -73,42 +70,6 @@ struct Misc {
   int abort;
   int last[2];
 };
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t x, float* a, float* b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// The lowest n bits (none below 0, all from 32 on).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// Part of a row tile, [slot][half][D / 4][128 rows][4]: neighbouring threads
-// (rows) write neighbouring vectors.
-template <int D>
-__device__ __forceinline__ float4* part_row(const AttnParams& P, int64_t slot, int half, int row) {
-  return reinterpret_cast<float4*>(P.part) + (slot * 2 + half) * (D / 4) * kHalf + row;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -359,31 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kKeys; k += 32)
           ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
         ptx::tmem_ld_wait();
-        if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) {
-          // A bit per key: from lo to hi, or one of the first tokens.  The scores
-          // are changed in tensor memory, by a loop, and read again: changing
-          // them in registers takes 5 KB of instructions (prompt of 4000, 64
-          // values a head: 182 : 167 us).
-          const int first = min(g.t.n_sink, hi + 1) - v0;
-#pragma unroll 1
-          for (int k = 0; k < kKeys; k += 32) {
-            const uint32_t seen = (low_bits(hi + 1 - key0 - k) & ~low_bits(lo - key0 - k)) |
-                                  low_bits(first - k);
-            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-            uint32_t x[32];
-            ptx::tmem_ld32(tm_s + k, x);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!(seen & (1u << y))) x[y] = 0xff800000u;  // -infinity
-            ptx::tmem_st32(tm_s + k, x);
-          }
-          ptx::tmem_st_wait();
-#pragma unroll
-          for (int k = 0; k < kKeys; k += 32)
-            ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
-          ptx::tmem_ld_wait();
-        }
+        mask_scores(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0, s);
         float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
         float mz = max3(s[6], s[7], s[8]), mw = max3(s[9], s[10], s[11]);
 #pragma unroll
@@ -406,15 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
             __syncwarp();
             ptx::tc_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              uint32_t o[32];
-              ptx::tmem_ld32(tm_o + k, o);
-              ptx::tmem_ld_wait();
-#pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              ptx::tmem_st32(tm_o + k, o);
-            }
+            scale_result<D>(tm_o, f);
           }
         }
         if (h == 0 && tile_has_unseen(g.t, v0)) {
@@ -457,74 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the item, or this CTA's part of it, is done
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
-      const RowWriter<D> out(P, g.shared, g.tok0 + tok, head, mine && g.parts == 1, m, l);
-      wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
-      __syncwarp();
-      ptx::tc_fence_after();
-      auto read = [&] {  // O has been read
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&M.o_empty[h]);
-          ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
-        }
-      };
-      if (g.parts == 1) {
-        // (rolled, for the instructions' sake: chunks with a window of 1024 117 us,
-        // unrolled 121)
-#pragma unroll 1
-        for (int k = 0; k < D; k += 16) {
-          float o[16];
-          ptx::tmem_ld16(tm_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
-          ptx::tmem_ld_wait();
-          if (mine) out.write16(k, o);
-        }
-        read();
-        continue;
-      }
-      float o[D];
-#pragma unroll
-      for (int k = 0; k < D; k += 32)
-        ptx::tmem_ld32(tm_o + k, *reinterpret_cast<uint32_t(*)[32]>(o + k));
-      ptx::tmem_ld_wait();
-      read();
-      float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
-      if (mine) {
-        float4* part = part_row<D>(P, slot, h, row);
-#pragma unroll
-        for (int k = 0; k < D; k += 4)
-          part[(k / 4) * kHalf] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        ml[slot * 2 * kHalf] = make_float2(m, l);
-      }
-      if (!P.join_after &&
-          last_to_arrive(P, g, h, row == 0, &M.last[h], bar, 128) && mine) {
-        // few parts: the last to arrive adds them up, in their order
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int q = 0; q < g.parts; ++q)
-          top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
-#pragma unroll
-        for (int k = 0; k < D; ++k) o[k] = 0.f;
-#pragma unroll 1
-        for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
-          const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
-          const float f = exp2_fast(v.x - top);
-          sum += f * v.y;
-          const float4* from = part_row<D>(P, part_slot(g, q), h, row);
-#pragma unroll
-          for (int k = 0; k < D; k += 4) {
-            const float4 z = __ldcg(from + (k / 4) * kHalf);
-            o[k] += f * z.x;
-            o[k + 1] += f * z.y;
-            o[k + 2] += f * z.z;
-            o[k + 3] += f * z.w;
-          }
-        }
-        const RowWriter<D> joined(P, g.shared, g.tok0 + tok, head, true, top, sum);
-#pragma unroll
-        for (int k = 0; k < D; k += 16) joined.write16(k, o + k);
-      }
+      finish_half<D>(P, g, h, row, mine, g.tok0 + tok, head, m, l, 1.f, tm_o, &M.o_done[h],
+                     (tile - 1) & 1, abort_f, &M.o_empty[h], &M.seg_empty[sg % kRing], &M.last[h], bar);
     }
   }
 
@@ -679,13 +542,24 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P)) != cudaSuccess || !P.join_after)
     return e;
-  cfg.gridDim = dim3(kJoinBlocks);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, P);
+  return launch_attn_join(P, st);
 }
 
 }  // namespace
+
+cudaError_t launch_attn_join(const AttnParams& P, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kJoinBlocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return P.kv.head_dim == 64 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<64>, P)
+                             : cudaLaunchKernelEx(&cfg, attn_join_kernel<128>, P);
+}
 
 cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                 const CUtensorMap& tm_v, const AttnParams& P, cudaStream_t st,

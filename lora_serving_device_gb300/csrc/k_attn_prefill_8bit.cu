@@ -1,0 +1,573 @@
+// Attention over the 8-bit paged cache for many rows per key head: prompts, chunks
+// of prompts and the tokens of a prefix group (lora_attn_paged_8bit and the prefix
+// phase of lora_attn_prefix_8bit).
+//
+// Mathematics, per item (two halves of up to 128 rows of one key head) and key tile of
+// 128 keys, for each half:
+//   S  = [Q_1 + Q_2] K^T      [128 rows, 128 keys]   e4m3, fp32 in tensor memory
+//   s  = c 2^(kb + qb) S      kb, qb the exponents of a key's block and a row
+//   P  = 2^(s - m),  l += row sums of P
+//   O += P V 2^(vb - R)       [128 rows, D]          f16, P from tensor memory
+// K stays as it lies in memory: a row of Q is divided by a power of two and the sum of two
+// e4m3 terms, off by at most 2^-17 of its largest value; two products at twice bf16's rate
+// take its time.  V would need three terms of P, one and a half times that, so it
+// becomes f16 instead: a code is exact there, as is its block's power of two relative to
+// the largest so far, R (to 2^-33 of that), and P keeps 11 bits, where a bf16 has 8.  One
+// warp does it, between the loads and the MMAs; values that no row sees it
+// makes zeros on the way.  A key block's scale is a factor of its 16 scores beside c.
+//
+// Bound by the tensor cores, as the bf16 kernel (k_attn_prefill.cu), whose schedule of halves,
+// softmax and results this is; a tile's codes are half its bytes.
+//
+// Warps: 0-3 softmax of half 0, 4-7 of half 1 (Q in, results out), 8 schedule and TMA,
+// 9 MMA issue, 10 scales, 11 V to f16.  Every wait is bounded; on timeout the kernel
+// raises LORA_DEVERR_TIMEOUT.
+#include <cudaTypedefs.h>
+
+#include "attn_rows.cuh"
+
+namespace lora {
+namespace {
+
+// Three warpgroups: the softmax threads hold a row of 128 scores each and take
+// registers from the third, of which two warps work.  192 x 256 + 120 x 128 is
+// within the launch's 168 x 384.
+constexpr int kThreads = 384;
+constexpr int kRegsMost = 192, kRegsLeast = 120;
+constexpr int kRing = 4;     // segments that the producer may run ahead
+// log2 of a row's largest weight when its reference is set, and of the largest that it then lets
+// pass: f16 holds 2^15, and what is 2^-30 of the first
+constexpr float kTop = 6.f, kMost = 14.f;
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t kTile = kKeys * D;   // codes of K or V of a tile
+  static constexpr uint32_t kWide = 2 * kTile;   // V of a tile in f16; Q's two terms of a half
+  static constexpr int kK = D == 128 ? 4 : 8;    // tiles of K in flight
+  static constexpr int kV = D == 128 ? 2 : 4;    // of V as codes
+  static constexpr int kW = D == 128 ? 2 : 4;    // of V in f16
+  static constexpr uint32_t oV = kK * kTile;
+  static constexpr uint32_t oW = oV + kV * kTile;
+  static constexpr uint32_t oQ = oW + kW * kWide;
+  static constexpr uint32_t oMisc = oQ + 2 * kWide;
+};
+
+template <int D>
+struct Misc {
+  using La = Lay<D>;
+  Segment ring[kRing];
+  ScaleRing scales;
+  uint64_t k_full[La::kK], k_empty[La::kK];
+  uint64_t v_full[La::kV], v_empty[La::kV];
+  uint64_t w_full[La::kW], w_empty[La::kW];
+  uint64_t q_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
+  uint64_t seg_full[kRing], seg_empty[kRing];
+  uint32_t tmem;
+  int abort;
+  int last[2];
+};
+
+// V of a tile from codes to f16, one warp: times 2^(its block's exponent - top), the layout that
+// the MMA reads ([eight keys][64 values][8 keys][64 values], 128-byte swizzle).  Values that no
+// row sees become zeros.  Lanes take the 16-code chunks of a key first, so that reads and
+// writes (the two halves of the lanes in opposite order) hit all banks.
+template <int D, int kBlock>
+__device__ __forceinline__ void widen_values(const uint8_t* V, uint8_t* W, const uint8_t* bytes,
+                                             int top, const RowTile& t, int v0) {
+  constexpr int kChunks = D / 16, kRowsAtOnce = 32 / kChunks;
+  const int lane = threadIdx.x & 31, c = lane % kChunks, r0 = lane / kChunks;
+  const bool edge = tile_has_unseen(t, v0);
+  // the first of a lane's two stores: its chunk's first or second eight values
+  const int sub0 = D == 128 ? c / 4 : 0;
+#pragma unroll 1
+  for (int b = 0; b < kKeys / kBlock; ++b) {
+    const int e = static_cast<int>(bytes[b]) - top;  // <= 0
+    const uint32_t f = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+    const uint32_t f2 = f | f << 16;
+    uint4 x[kBlock / kRowsAtOnce > 0 ? kBlock / kRowsAtOnce : 1];
+#pragma unroll
+    for (int k = 0; k < kBlock / kRowsAtOnce; ++k) {
+      const int r = b * kBlock + k * kRowsAtOnce + r0;
+      const int at = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+      x[k] = *reinterpret_cast<const uint4*>(V + r * D + at * 16);
+    }
+#pragma unroll
+    for (int k = 0; k < kBlock / kRowsAtOnce; ++k) {
+      const int r = b * kBlock + k * kRowsAtOnce + r0;
+      const bool zero = edge && !place_seen(t, v0 + r);
+      uint32_t w[8];
+      const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[2 * i] = scale2_f16(e4m3x2_f16x2(in[i]), f2);
+        w[2 * i + 1] = scale2_f16(e4m3x2_f16x2(in[i] >> 16), f2);
+      }
+      if (zero)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0;
+      uint8_t* row = W + (r / 8) * (D / 64) * 1024 + (c / 4) * 1024 + (r % 8) * 128;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int sub = s ^ sub0;
+        const uint4 y = sub ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(row + ((((c % 4) * 2 + sub) ^ (r & 7)) << 4)) = y;
+      }
+    }
+  }
+}
+
+// A thread's row of Q (`from`, or null: zeros) as two e4m3 terms, each 128 bytes a row: planes
+// of kHalf rows, or the halves of one row with D = 64.  Returns the power of two that it was divided by.
+template <int D>
+__device__ __forceinline__ float split_query(const bf16* from, uint8_t* Q, int row) {
+  uint4 x[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+    x[i] = from ? *reinterpret_cast<const uint4*>(from + 8 * i) : make_uint4(0, 0, 0, 0);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    float y[8];
+    load8(reinterpret_cast<const bf16*>(&x[i]), y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(y[k]));
+  }
+  const int byte = min(scale_byte(top), 253);
+  const float inv = scale_of(254 - byte);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t t1[4], t2[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float y[8];
+      load8(reinterpret_cast<const bf16*>(&x[2 * c + i]), y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= inv;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t t = pack4_e4m3(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        const float2 lo = unpack2_e4m3(t), hi = unpack2_e4m3(t >> 16);
+        t1[2 * i + k] = t;
+        t2[2 * i + k] = pack4_e4m3(y[4 * k] - lo.x, y[4 * k + 1] - lo.y, y[4 * k + 2] - hi.x,
+                                   y[4 * k + 3] - hi.y);
+      }
+    }
+    uint8_t* to = Q + row * 128;
+    const int second = D == 128 ? kHalf * 128 : 0, c2 = D == 128 ? c : 4 + c;
+    *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    *reinterpret_cast<uint4*>(to + second + ((c2 ^ (row & 7)) << 4)) =
+        make_uint4(t2[0], t2[1], t2[2], t2[3]);
+  }
+  return scale_of(byte);
+}
+
+template <int D, int kBlock>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prefill_8bit_kernel(const __grid_constant__ CUtensorMap tm_k,
+                             const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
+  using La = Lay<D>;
+  constexpr int kK = La::kK, kV = La::kV, kW = La::kW;
+  using Mi = Misc<D>;
+  constexpr uint32_t kIdescQK = ptx::idesc_e4m3_f32(kHalf, kKeys, false, false);
+  constexpr uint32_t kIdescPV = ptx::idesc_f16_f32(kHalf, D, false, true);
+  constexpr uint32_t kGroupBytes = (D / 64) * 1024;  // eight keys of V in f16
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Mi& M = *reinterpret_cast<Mi*>(smem + La::oMisc);
+  volatile int* abort_f = &M.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int half_rows = P.rows / 2;  // rows of a half that are in use
+
+  if (tid == 0) {
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+    for (int i = 0; i < kK; ++i) {
+      ptx::mbar_init(&M.k_full[i], 1);
+      ptx::mbar_init(&M.k_empty[i], 1);
+    }
+    for (int i = 0; i < kV; ++i) {
+      ptx::mbar_init(&M.v_full[i], 1);
+      ptx::mbar_init(&M.v_empty[i], 1);
+    }
+    for (int i = 0; i < kW; ++i) {
+      ptx::mbar_init(&M.w_full[i], 1);
+      ptx::mbar_init(&M.w_empty[i], 1);
+    }
+    init_scales(M.scales, 9);
+    for (int h = 0; h < 2; ++h) {
+      ptx::mbar_init(&M.q_full[h], 4);
+      ptx::mbar_init(&M.s_full[h], 1);
+      ptx::mbar_init(&M.p_half[h], 4);
+      ptx::mbar_init(&M.p_full[h], 4);
+      ptx::mbar_init(&M.o_done[h], 1);
+      ptx::mbar_init(&M.o_empty[h], 4);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      ptx::mbar_init(&M.seg_full[i], 1);
+      ptx::mbar_init(&M.seg_empty[i], 11);
+    }
+    M.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&M.tmem, 512);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  // (the next grid may not start early: its launch slows this one's last CTAs,
+  // which join parts, by more than its prologue takes)
+  pdl_wait();
+  // the tiles' memory holds the problems' sizes until the first load
+  size_problems(P, reinterpret_cast<ProblemSize*>(smem));
+  __syncthreads();
+  size_long_problems(P, reinterpret_cast<ProblemSize*>(smem));
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = M.tmem;  // S (and P) of half h at h * 128, O at 256 + h * 128
+
+  // (each role's branch begins with its own split, so that the compiler knows
+  // the number of registers on every path)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLeast));
+  if (warp == 8) {
+    // ---------------- schedule and TMA ----------------------------------
+    Walker walk;
+    walk.start(P, reinterpret_cast<ProblemSize*>(smem));
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    TileLoader<D, 1> load(P);
+    int nk = 0, nv = 0;  // tiles brought in
+    bool ok = true;
+    SplitItem mine = {};
+    for (int sg = 0; ok; ++sg) {
+      const Segment g = walk.next(P);
+      if (sg >= kRing)
+        ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
+      if (!ok) break;
+      if (lane == 0) {
+        M.ring[sg % kRing] = g;
+        ptx::mbar_arrive(&M.seg_full[sg % kRing]);
+      }
+      __syncwarp();
+      if (g.n == 0) break;
+      load.begin(P, g);
+      if (P.join_after && g.parts > 1 && g.cta0 == blockIdx.x)
+        mine = {g.parts, g.tok0, g.t.row0, g.t.n_rows, g.head, g.shared, {0, 0}};
+      for (int i = 0; i < g.n && ok; ++i) {
+        const int at = load.at(P, g, i);
+        const uint32_t bytes = load.bytes(at);
+        if (nk >= kK) ok = wait_all(&M.k_empty[nk % kK], ((nk / kK) & 1) ^ 1, abort_f);
+        if (!ok) break;
+        load.load(&tm_k, &M.k_full[nk % kK], smem + nk % kK * La::kTile, at, bytes);
+        ++nk;
+        if (nv >= kV) ok = wait_all(&M.v_empty[nv % kV], ((nv / kV) & 1) ^ 1, abort_f);
+        if (!ok) break;
+        load.load(&tm_v, &M.v_full[nv % kV], smem + La::oV + nv % kV * La::kTile, at, bytes);
+        ++nv;
+      }
+    }
+    if (P.join_after && lane == 0) P.split[blockIdx.x] = mine;
+    if (!ok) {
+      // gave up: what is on its way into shared memory has to land first
+      int none = 0;
+      for (int k = nk > kK ? nk - kK : 0; k < nk; ++k)
+        ptx::mbar_wait_bounded(&M.k_full[k % kK], (k / kK) & 1, &none, kAttnWaitNs / 8);
+      for (int k = nv > kV ? nv - kV : 0; k < nv; ++k)
+        ptx::mbar_wait_bounded(&M.v_full[k % kV], (k / kV) & 1, &none, kAttnWaitNs / 8);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issue ------------------------------------------
+    // One thread: P V of tile n and Q K^T of tile n + 1, half by half, so that
+    // the tensor cores have the other half's work while a softmax runs.
+    if (elect_one()) {
+      const uint32_t k_tiles = desc_lo(ptx::smem_u32(smem), 16);
+      const uint32_t w_tiles = desc_lo(ptx::smem_u32(smem + La::oW), 1024);
+      // A bit for each half: parities of its Qs, of its tiles' P and of its O, and
+      // whether it has had a segment.
+      uint32_t q_par = 0, p_par = 0, o_par = 0, begun = 0;
+      auto issue_qk = [&](bool first, int n, int h, bool frees) {
+        if (first) {
+          wait_quiet(&M.q_full[h], (q_par >> h) & 1, abort_f);
+          q_par ^= 1u << h;
+        }
+        const int st = n % kK;
+        wait_quiet(&M.k_full[st], (n / kK) & 1, abort_f);
+        ptx::tc_fence_after();
+        const uint32_t qa = desc_lo(ptx::smem_u32(smem + La::oQ + h * La::kWide), 16);
+        const uint32_t ka = k_tiles + st * (La::kTile / 16);
+#pragma unroll
+        for (int ks = 0; ks < 2 * D / 32; ++ks)  // both terms of Q against the same keys
+          mma_ss_8bit(tmem + h * 128, qa + ((ks / 4) * (kHalf * 128) + (ks % 4) * 32) / 16,
+                      desc_hi(1024), ka + ks % (D / 32) * 2, desc_hi_span(8 * D, D), kIdescQK,
+                      ks > 0 ? 1u : 0u);
+        ptx::mma_commit(&M.s_full[h]);
+        if (frees) ptx::mma_commit(&M.k_empty[st]);
+      };
+      auto issue_pv = [&](bool first, int n, int h, bool frees) {
+        const int st = n % kW;
+        const uint32_t va = w_tiles + st * (La::kWide / 16);
+        if (h == 0) wait_quiet(&M.w_full[st], (n / kW) & 1, abort_f);
+        if (first) {
+          // the half's previous segment has been read out of O
+          if ((begun >> h) & 1) {
+            wait_quiet(&M.o_empty[h], (o_par >> h) & 1, abort_f);
+            o_par ^= 1u << h;
+          }
+          begun |= 1u << h;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          wait_quiet(x ? &M.p_full[h] : &M.p_half[h], (p_par >> h) & 1, abort_f);
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int ks = 4 * x; ks < 4 * x + 4; ++ks)
+            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
+                   va + ks * 2 * kGroupBytes / 16, desc_hi(kGroupBytes), kIdescPV,
+                   ks > 0 || !first ? 1u : 0u);
+        }
+        ptx::mma_commit(&M.o_done[h]);
+        if (frees) ptx::mma_commit(&M.w_empty[st]);
+        p_par ^= 1u << h;
+      };
+      int sg = -1, left = 0;  // the segment of tile n, and its key tiles to go
+      bool two = false, first = false;
+#pragma unroll 1
+      for (int n = -1; !*abort_f; ++n) {
+        int next = left - 1;
+        bool next_two = two, next_first = false;
+        if (next <= 0) {  // the next tile is of the next segment
+          wait_quiet(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
+          next = M.ring[(sg + 1) % kRing].n;
+          next_two = M.ring[(sg + 1) % kRing].t.n_rows > half_rows;
+          next_first = true;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (left > 0 && h <= two) issue_pv(first, n, h, h == two);
+          if (next > 0 && h <= next_two) issue_qk(next_first, n + 1, h, h == next_two);
+        }
+        if (next_first) {
+          if (sg >= 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+          ++sg;
+        }
+        if (next <= 0) break;
+        left = next;
+        two = next_two;
+        first = next_first;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---------------- scales ----------------------------------------------
+    fill_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
+  } else {
+    // ---------------- V from codes to f16 ---------------------------------
+    bool ok = true;
+    int n = 0;
+    for (int sg = 0; ok; ++sg) {
+      ok = wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (!ok) break;
+      const int tiles = M.ring[sg % kRing].n, first = M.ring[sg % kRing].first;
+      const RowTile t = M.ring[sg % kRing].t;
+      if (tiles == 0) break;
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
+        const int sc = n % kScaleRing;
+        ok = wait_all(&M.scales.full[sc], (n / kScaleRing) & 1, abort_f) &&
+             wait_all(&M.v_full[n % kV], (n / kV) & 1, abort_f) &&
+             (n < kW || wait_all(&M.w_empty[n % kW], ((n / kW) & 1) ^ 1, abort_f));
+        if (!ok) break;
+        widen_values<D, kBlock>(smem + La::oV + n % kV * La::kTile, smem + La::oW + n % kW * La::kWide,
+                                M.scales.v[sc], M.scales.top[sc], t, (first + i) * kKeys);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&M.w_full[n % kW]);
+          ptx::mbar_arrive(&M.v_empty[n % kV]);
+          ptx::mbar_arrive(&M.scales.empty[sc]);
+        }
+      }
+      if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMost));
+    // ---------------- softmax and results ---------------------------------
+    const int h = warp >> 2, w = warp & 3;
+    const int row = w * 32 + lane;  // of the half, and the TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const uint32_t tm_s = tmem + lanes + h * 128, tm_o = tmem + lanes + 256 + h * 128;
+    const float c = P.scale_log2;
+    const int bar = 1 + h;
+    int tile = 0;  // tiles of this half so far
+    // The warpgroup's four warps meet at barriers: after a wait that gave up
+    // they run on (every later wait returns at once) to the vote.
+    for (int sg = 0;; ++sg) {
+      wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (named_any(bar, 128, *abort_f != 0)) break;
+      const Segment g = M.ring[sg % kRing];
+      if (g.n == 0) break;
+      const int n_rows = min(g.t.n_rows - h * half_rows, half_rows);  // of this half
+      if (n_rows <= 0) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+        continue;
+      }
+      // rows past the last copy the first one
+      const bool mine = row < n_rows;
+      const int in_prob = g.t.row0 + h * half_rows + (mine ? row : 0);
+      const int tok = P.by_group(in_prob), head = g.head * P.group + in_prob - tok * P.group;
+      const int pos = g.base + tok;
+      const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
+      const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
+      // (the MMAs that read the last one's Q are done: so are its scores)
+      const float q_scale = split_query<D>(
+          mine ? P.q + (g.tok0 + tok) * P.q_stride + head * D : nullptr,
+          smem + La::oQ + h * La::kWide, row);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&M.q_full[h]);
+      const bool alone = g.t.n_rows <= half_rows;
+      float m = -INFINITY, l = 0.f;  // m: what weights are relative to
+      int R = 0;                     // the largest exponent of a value block so far
+#pragma unroll 1
+      for (int i = 0; i < g.n; ++i, ++tile) {
+        const int v0 = (g.first + i) * kKeys, key0 = window_key(g.t, v0);  // place, key
+        const int sc = (g.tile0 + i) % kScaleRing;
+        wait_quiet(&M.scales.full[sc], ((g.tile0 + i) / kScaleRing) & 1, abort_f);
+        float kc[kKeys / kBlock];  // of each block's keys, times the row's own and c
+#pragma unroll
+        for (int b = 0; b < kKeys / kBlock; ++b)
+          kc[b] = fmaxf(M.scales.k[sc][b] * (q_scale * c), 1.2e-38f);
+        const int top = M.scales.top[sc];
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&M.scales.empty[sc]);
+          if (alone) ptx::mbar_arrive(&M.scales.empty[sc]);  // for the other half's warp
+        }
+        wait_quiet(&M.s_full[h], tile & 1, abort_f);
+        __syncwarp();
+        ptx::tc_fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int k = 0; k < kKeys; k += 32)
+          ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
+        ptx::tmem_ld_wait();
+        mask_scores(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0, s);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kKeys / kBlock; ++b) {
+          const float* x = s + b * kBlock;
+          float y = max3(x[0], x[1], x[2]), z = max3(x[3], x[4], x[5]);
+#pragma unroll
+          for (int k = 6; k + 3 < kBlock; k += 4) {
+            y = max3(y, x[k], x[k + 1]);
+            z = max3(z, x[k + 2], x[k + 3]);
+          }
+          y = max3(y, x[kBlock - 2], x[kBlock - 1]);
+          mx = fmaxf(mx, fmaxf(y, z) * kc[b]);
+        }
+        // (rows that are not in use hold anything: they have no say)
+        if (top > R || __any_sync(0xffffffffu, mine && mx > m + kMost)) {
+          const float now = fmaxf(m, mx - kTop);
+          const float f = m == -INFINITY ? 0.f : exp2_fast(m - now);
+          m = now;
+          l *= f;
+          const float f_all = top - R < 127 ? f * scale_of(127 - (top - R)) : 0.f;
+          R = top;
+          if (i > 0) {
+            wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
+            __syncwarp();
+            ptx::tc_fence_after();
+            scale_result<D>(tm_o, f_all);
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const uint64_t neg2 = pack2(neg, neg);
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int k = 0; k < kKeys; k += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float a, b;
+            const float kx = kc[(k + 2 * x) / kBlock];
+            unpack2(fma2(pack2(s[k + 2 * x], s[k + 2 * x + 1]), pack2(kx, kx), neg2), &a, &b);
+            a = exp2_fast(a);
+            b = exp2_fast(b);
+            if (x & 1)
+              sum1 = add2(sum1, pack2(a, b));
+            else
+              sum0 = add2(sum0, pack2(a, b));
+            p[x] = pack_f16x2(a, b);
+          }
+          ptx::tmem_st16(tm_s + k / 2, p);
+          if (k == 32 || k == 96) {
+            // each half of the keys goes to the MMA as soon as it is there
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(k == 32 ? &M.p_half[h] : &M.p_full[h]);
+          }
+        }
+        float a, b;
+        unpack2(add2(sum0, sum1), &a, &b);
+        l += a + b;
+      }
+
+      // ---- the item, or this CTA's part of it, is done
+      finish_half<D>(P, g, h, row, mine, g.tok0 + tok, head, m, l, scale_of(max(R, 1)), tm_o, &M.o_done[h],
+                     (tile - 1) & 1, abort_f, &M.o_empty[h], &M.seg_empty[sg % kRing], &M.last[h], bar);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_f) flag_error(P.err, LORA_DEVERR_TIMEOUT);
+}
+
+template <int D, int kBlock>
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& P,
+                   cudaStream_t st, const DeviceInfo& dev) {
+  using La = Lay<D>;
+  constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<D>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
+  auto kern = attn_prefill_8bit_kernel<D, kBlock>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kDecodeScheduleCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, P)) != cudaSuccess || !P.join_after)
+    return e;
+  return launch_attn_join(P, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill_8bit(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                     const AttnParams& P, cudaStream_t st, const DeviceInfo& dev) {
+  if (P.kv.page_size == 8)
+    return P.kv.head_dim == 64 ? launch<64, 8>(tm_k, tm_v, P, st, dev)
+                               : launch<128, 8>(tm_k, tm_v, P, st, dev);
+  return P.kv.head_dim == 64 ? launch<64, 16>(tm_k, tm_v, P, st, dev)
+                             : launch<128, 16>(tm_k, tm_v, P, st, dev);
+}
+
+}  // namespace lora
