@@ -48,11 +48,9 @@ __device__ __forceinline__ float4* part_row(const AttnParams& P, int64_t slot, i
 
 // The scores of a tile's keys that a row does not see become -infinity: it sees those from lo
 // to hi, key0 being the tile's first, and the tile's first `first`.  A warp's rows, a
-// lane each; they are changed in tensor memory, by a loop, and read again: changing
-// them in registers takes 5 KB of instructions (prompt of 4000, 64 values a head: 182 : 167 us).
-__device__ __forceinline__ void mask_scores(uint32_t tm_s, int key0, int hi, int lo, int first,
-                                            float (&s)[kKeys]) {
-  if (!__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) return;
+// lane each, in tensor memory, by a loop; whether there were any.
+__device__ __forceinline__ bool mask_in_place(uint32_t tm_s, int key0, int hi, int lo, int first) {
+  if (!__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo)) return false;
 #pragma unroll 1
   for (int k = 0; k < kKeys; k += 32) {
     const uint32_t seen = (low_bits(hi + 1 - key0 - k) & ~low_bits(lo - key0 - k)) |
@@ -67,6 +65,13 @@ __device__ __forceinline__ void mask_scores(uint32_t tm_s, int key0, int hi, int
     ptx::tmem_st32(tm_s + k, x);
   }
   ptx::tmem_st_wait();
+  return true;
+}
+// The same for scores that have been read already: read again, since changing them in
+// registers takes 5 KB of instructions (prompt of 4000, 64 values a head: 182 : 167 us).
+__device__ __forceinline__ void mask_scores(uint32_t tm_s, int key0, int hi, int lo, int first,
+                                            float (&s)[kKeys]) {
+  if (!mask_in_place(tm_s, key0, hi, lo, first)) return;
 #pragma unroll
   for (int k = 0; k < kKeys; k += 32)
     ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
@@ -91,8 +96,8 @@ __device__ __forceinline__ void scale_result(uint32_t tm_o, float f) {
 // head `head`; `mine`: it is in use) leaves tensor memory, `unit` times what is there, at
 // maximum m (log2 units) and sum l.  Rows that several CTAs share are written as
 // parts and joined by the last CTA to arrive, or by a kernel after this one.  The last product
-// is waited for here (o_done).
-template <int D>
+// is waited for here (o_done).  kRolled: by short loops, in few registers.
+template <int D, bool kRolled = false>
 __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& g, int h, int row,
                                             bool mine, int64_t t, int head, float m, float l,
                                             float unit, uint32_t tm_o, uint64_t* o_done,
@@ -124,6 +129,54 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
       if (mine) out.write16(k, o);
     }
     read();
+    return;
+  }
+  if constexpr (kRolled) {
+    float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
+#pragma unroll 1
+    for (int k = 0; k < D; k += 16) {
+      float o[16];
+      ptx::tmem_ld16(tm_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 16 && mine; x += 4)
+        part_row<D>(P, slot, h, row)[(k + x) / 4 * kHalf] =
+            make_float4(o[x] * unit, o[x + 1] * unit, o[x + 2] * unit, o[x + 3] * unit);
+    }
+    read();
+    if (mine) ml[slot * 2 * kHalf] = make_float2(m, l);
+    if (!P.join_after && last_to_arrive(P, g, h, row == 0, last, bar, 128) && mine) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+      for (int q = 0; q < g.parts; ++q)
+        top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
+      const float ref = top == -INFINITY ? 0.f : top;
+      for (int q = 0; q < g.parts; ++q) {
+        const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
+        sum += exp2_fast(v.x - ref) * v.y;
+      }
+      const RowWriter<D> joined(P, g.shared, t, head, true, top, sum);
+#pragma unroll 1
+      for (int k = 0; k < D; k += 16) {
+        float o[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = 0.f;
+#pragma unroll 2
+        for (int q = 0; q < g.parts; ++q) {
+          const float f = exp2_fast(__ldcg(&ml[part_slot(g, q) * 2 * kHalf].x) - ref);
+          const float4* from = part_row<D>(P, part_slot(g, q), h, row) + k / 4 * kHalf;
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const float4 z = __ldcg(from + x / 4 * kHalf);
+            o[x] += f * z.x;
+            o[x + 1] += f * z.y;
+            o[x + 2] += f * z.z;
+            o[x + 3] += f * z.w;
+          }
+        }
+        joined.write16(k, o);
+      }
+    }
     return;
   }
   float o[D];

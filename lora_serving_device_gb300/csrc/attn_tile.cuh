@@ -290,64 +290,81 @@ __device__ __forceinline__ void init_scales(ScaleRing& S, int readers) {
   }
 }
 // Looks them up, one warp: a lane to a block, as many tiles at once as 32 lanes have blocks
-// of, the next ones' page ids on their way beside them.  It follows the segments of `ring`
-// until the first end.  Scales of blocks that no row sees are not read: 1 for keys, and for
-// values a byte that leaves `top` where it is.
-__device__ __forceinline__ void fill_scales(const AttnParams& P, ScaleRing& S, const Segment* ring,
-                                            int ring_size, uint64_t* seg_full, uint64_t* seg_empty,
-                                            volatile int* abort) {
-  const int lane = threadIdx.x & 31;
-  const int block = min(P.kv.page_size, kScaleBlock), per_tile = kKeys / block;
-  const int at_once = 32 / per_tile, lg_block = block == 8 ? 3 : 4;
-  const int page_blocks = P.kv.page_size >> lg_block;
-  const int mine = lane / per_tile, b = lane % per_tile;  // tile of a batch, block
+// of, the next ones' page ids on their way beside them.  Scales of blocks that no row sees
+// are not read: 1 for keys, and for values a byte that leaves `top` where it is.
+struct ScaleFinder {
+  int block, lg_block, per_tile, at_once;
+  int mine, b;    // this lane's tile of a batch, and its block there
+  int id, key0, top;
+  bool seen;
+  __device__ __forceinline__ explicit ScaleFinder(const AttnParams& P)
+      : block(min(P.kv.page_size, kScaleBlock)),
+        lg_block(block == 8 ? 3 : 4),
+        per_tile(kKeys / block),
+        at_once(32 / per_tile),
+        mine((threadIdx.x & 31) / per_tile),
+        b((threadIdx.x & 31) % per_tile) {}
+  __device__ __forceinline__ void fetch(const AttnParams& P, const Segment& g, int i0) {
+    const int v = (g.first + i0 + mine) * kKeys + b * block;
+    key0 = v < g.t.sink_places ? v : window_key(g.t, v);
+    seen = i0 + mine < g.n &&
+           ((key0 <= g.t.vis_hi && key0 + block - 1 >= g.t.vis_lo) || v < g.t.n_sink);
+    if (seen)
+      id = P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages + (key0 >> P.lg_page)];
+  }
+  __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
+    top = 0;
+    fetch(P, g, 0);
+  }
+  // Tiles i0 .. i0 + at_once - 1 of the segment; false once a wait of the CTA gave up.
+  __device__ __forceinline__ bool fill(const AttnParams& P, ScaleRing& S, const Segment& g, int i0,
+                                       volatile int* abort) {
+    const int lane = threadIdx.x & 31;
+    int kb = 127, vb = 1;
+    if (seen && id >= 0 && id < P.kv.n_pages) {
+      const int64_t at =
+          (static_cast<int64_t>(id) * P.kv.n_kv_heads + g.head) * (P.kv.page_size >> lg_block) +
+          ((key0 & (P.kv.page_size - 1)) >> lg_block);
+      kb = scale_read(P.k_scale[at]);
+      vb = scale_read(P.v_scale[at]);
+    }
+    if (i0 + at_once < g.n) fetch(P, g, i0 + at_once);
+    const int n = min(at_once, g.n - i0), tile = g.tile0 + i0;
+    for (int i = tile; i < tile + n; ++i)
+      if (i >= kScaleRing &&
+          !wait_all(&S.empty[i % kScaleRing], ((i / kScaleRing) & 1) ^ 1, abort))
+        return false;
+    const int slot = (tile + mine) % kScaleRing;
+    if (mine < n) {
+      S.k[slot][b] = scale_of(kb);
+      S.v[slot][b] = static_cast<uint8_t>(vb);
+    }
+    // the largest so far, tile by tile
+    for (int i = 0; i < n; ++i) {
+      top = max(top, __reduce_max_sync(0xffffffffu, mine == i ? vb : 0));
+      if (lane == 0) S.top[(tile + i) % kScaleRing] = top;
+    }
+    __syncwarp();
+    if (lane < n) ptx::mbar_arrive(&S.full[(tile + lane) % kScaleRing]);
+    return true;
+  }
+};
+
+// The whole of a warp's work: scales of all tiles of the segments in `ring`, to the first end.
+__device__ __forceinline__ void run_scales(const AttnParams& P, ScaleRing& S, const Segment* ring,
+                                           int ring_size, uint64_t* seg_full, uint64_t* seg_empty,
+                                           volatile int* abort) {
+  ScaleFinder find(P);
   bool ok = true;
   for (int sg = 0; ok; ++sg) {
     ok = wait_all(&seg_full[sg % ring_size], (sg / ring_size) & 1, abort);
     if (!ok) break;
-    const Segment g = ring[sg % ring_size];
+    const Segment& g = ring[sg % ring_size];
     if (g.n == 0) break;
-    bool seen;
-    int key0;
-    auto fetch = [&](int i0) {
-      const int v = (g.first + i0 + mine) * kKeys + b * block;
-      key0 = v < g.t.sink_places ? v : window_key(g.t, v);
-      seen = i0 + mine < g.n &&
-             ((key0 <= g.t.vis_hi && key0 + block - 1 >= g.t.vis_lo) || v < g.t.n_sink);
-      return seen ? P.kv.block_table[static_cast<int64_t>(g.table_row) * P.kv.max_pages +
-                                     (key0 >> P.lg_page)]
-                  : -1;
-    };
-    int id = fetch(0), top = 0;
-    for (int i0 = 0; i0 < g.n; i0 += at_once) {
-      int kb = 127, vb = 1;
-      if (seen && id >= 0 && id < P.kv.n_pages) {
-        const int64_t at = (static_cast<int64_t>(id) * P.kv.n_kv_heads + g.head) * page_blocks +
-                           ((key0 & (P.kv.page_size - 1)) >> lg_block);
-        kb = scale_read(P.k_scale[at]);
-        vb = scale_read(P.v_scale[at]);
-      }
-      if (i0 + at_once < g.n) id = fetch(i0 + at_once);
-      const int n = min(at_once, g.n - i0), tile = g.tile0 + i0;
-      for (int i = tile; i < tile + n && ok; ++i)
-        if (i >= kScaleRing)
-          ok = wait_all(&S.empty[i % kScaleRing], ((i / kScaleRing) & 1) ^ 1, abort);
-      if (!ok) break;
-      const int slot = (tile + mine) % kScaleRing;
-      if (mine < n) {
-        S.k[slot][b] = scale_of(kb);
-        S.v[slot][b] = static_cast<uint8_t>(vb);
-      }
-      // the largest so far, tile by tile
-      for (int i = 0; i < n; ++i) {
-        top = max(top, __reduce_max_sync(0xffffffffu, mine == i ? vb : 0));
-        if (lane == 0) S.top[(tile + i) % kScaleRing] = top;
-      }
-      __syncwarp();
-      if (lane < n) ptx::mbar_arrive(&S.full[(tile + lane) % kScaleRing]);
-    }
+    find.begin(P, g);
+    for (int i = 0; i < g.n && ok; i += find.at_once) ok = find.fill(P, S, g, i, abort);
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&seg_empty[sg % ring_size]);
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&seg_empty[sg % ring_size]);
   }
 }
 

@@ -35,21 +35,39 @@ __device__ __forceinline__ float2 unpack2_e4m3(uint32_t two) {
       __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3)));
 }
 
-// Two codes (the low 16 bits) as f16, exactly; two f16 times two; two fp32 rounded to f16.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
-  return h.x | static_cast<uint32_t>(h.y) << 16;
+// Eight codes as f16, exactly, times f2 (a power of two, twice).
+__device__ __forceinline__ void widen4_e4m3(uint32_t four, uint32_t f2, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 x, y;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, a;\n\tcvt.rn.f16x2.e4m3x2 y, b;\n\t"
+      "mul.rn.f16x2 %0, x, %3;\n\tmul.rn.f16x2 %1, y, %3;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four), "r"(f2));
 }
-__device__ __forceinline__ uint32_t scale2_f16(uint32_t x, uint32_t f) {
-  uint32_t y;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
+__device__ __forceinline__ uint4 widen8_e4m3(uint32_t a, uint32_t b, uint32_t f2) {
+  uint4 y;
+  widen4_e4m3(a, f2, y.x, y.y);
+  widen4_e4m3(b, f2, y.z, y.w);
   return y;
 }
+// Two fp32 rounded to f16.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t y;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
   return y;
+}
+
+// Four f16 (magnitudes up to 448) as the sum of two e4m3 terms.
+__device__ __forceinline__ void split4_e4m3(uint32_t a, uint32_t b, uint32_t& t1, uint32_t& t2) {
+  asm("{\n\t.reg .b16 p, q;\n\t.reg .b32 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, %2;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, %3;\n\t"
+      "mov.b32 %0, {p, q};\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, p;\n\tcvt.rn.f16x2.e4m3x2 y, q;\n\t"
+      "sub.rn.f16x2 x, %2, x;\n\tsub.rn.f16x2 y, %3, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, x;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, y;\n\t"
+      "mov.b32 %1, {p, q};\n\t}"
+      : "=&r"(t1), "=r"(t2)
+      : "r"(a), "r"(b));
 }
 
 }  // namespace lora

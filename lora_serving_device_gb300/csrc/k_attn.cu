@@ -14,8 +14,9 @@ cudaError_t launch_attn_decode_8bit(const CUtensorMap& tm_k, const CUtensorMap& 
 cudaError_t launch_attn_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                 const CUtensorMap& tm_v, const AttnParams& P, cudaStream_t st,
                                 const DeviceInfo& dev);
-cudaError_t launch_attn_prefill_8bit(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                     const AttnParams& P, cudaStream_t st, const DeviceInfo& dev);
+cudaError_t launch_attn_prefill_8bit(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                     const CUtensorMap& tm_v, const AttnParams& P,
+                                     cudaStream_t st, const DeviceInfo& dev);
 
 namespace {
 
@@ -167,11 +168,9 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     // 50.6 us.
     P.join_after = static_cast<int64_t>(kv.T) * P.group / P.rows * kv.n_kv_heads < 38;
     cudaError_t e;
-    if (w.shape[phase].prefill && bits8) {
-      e = launch_attn_prefill_8bit(tm_k, tm_v, P, st, dev);
-    } else if (w.shape[phase].prefill) {
+    if (w.shape[phase].prefill) {
       if (!encode_q_map(&tm_q, a, kv, P.group)) return cudaErrorInvalidValue;
-      e = launch_attn_prefill(tm_q, tm_k, tm_v, P, st, dev);
+      e = (bits8 ? launch_attn_prefill_8bit : launch_attn_prefill)(tm_q, tm_k, tm_v, P, st, dev);
     } else {
       e = (bits8 ? launch_attn_decode_8bit : launch_attn_decode)(tm_k, tm_v, P, st, dev);
     }

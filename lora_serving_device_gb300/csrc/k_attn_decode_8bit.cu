@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     __syncwarp();
   } else if (warp == 10) {
     // ---------------- scales ----------------------------------------------
-    fill_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
+    run_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
   } else {
     // ---------------- softmax and epilogue --------------------------------
     const int w = warp & 3;                 // TMEM lanes 32w .. 32w + 31

@@ -12,15 +12,15 @@
 // e4m3 terms, off by at most 2^-17 of its largest value; two products at twice bf16's rate
 // take its time.  V would need three terms of P, one and a half times that, so it
 // becomes f16 instead: a code is exact there, as is its block's power of two relative to
-// the largest so far, R (to 2^-33 of that), and P keeps 11 bits, where a bf16 has 8.  One
-// warp does it, between the loads and the MMAs; values that no row sees it
-// makes zeros on the way.  A key block's scale is a factor of its 16 scores beside c.
+// the largest so far, R (to 2^-33 of that), and P keeps 11 bits, where a bf16 has 8.  Four
+// warps do it, between the loads and the MMAs; values that no row sees they make zeros on
+// the way.  A key block's scale is a factor of its 16 scores beside c.
 //
 // Bound by the tensor cores, as the bf16 kernel (k_attn_prefill.cu), whose schedule of halves,
 // softmax and results this is; a tile's codes are half its bytes.
 //
 // Warps: 0-3 softmax of half 0, 4-7 of half 1 (Q in, results out), 8 schedule and TMA,
-// 9 MMA issue, 10 scales, 11 V to f16.  Every wait is bounded; on timeout the kernel
+// 9 MMA issue, 10 scales, 12-15 V to f16.  Every wait is bounded; on timeout the kernel
 // raises LORA_DEVERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
@@ -29,11 +29,8 @@
 namespace lora {
 namespace {
 
-// Three warpgroups: the softmax threads hold a row of 128 scores each and take
-// registers from the third, of which two warps work.  192 x 256 + 120 x 128 is
-// within the launch's 168 x 384.
-constexpr int kThreads = 384;
-constexpr int kRegsMost = 192, kRegsLeast = 120;
+constexpr int kThreads = 512;
+constexpr int kFirstWidener = 12, kWideners = 4;  // warps that widen V
 constexpr int kRing = 4;     // segments that the producer may run ahead
 // log2 of a row's largest weight when its reference is set, and of the largest that it then lets
 // pass: f16 holds 2^15, and what is 2^-30 of the first
@@ -60,7 +57,7 @@ struct Misc {
   uint64_t k_full[La::kK], k_empty[La::kK];
   uint64_t v_full[La::kV], v_empty[La::kV];
   uint64_t w_full[La::kW], w_empty[La::kW];
-  uint64_t q_full[2];
+  uint64_t q_in[2], q_full[2], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
   uint64_t seg_full[kRing], seg_empty[kRing];
   uint32_t tmem;
@@ -68,103 +65,107 @@ struct Misc {
   int last[2];
 };
 
-// V of a tile from codes to f16, one warp: times 2^(its block's exponent - top), the layout that
-// the MMA reads ([eight keys][64 values][8 keys][64 values], 128-byte swizzle).  Values that no
-// row sees become zeros.  Lanes take the 16-code chunks of a key first, so that reads and
-// writes (the two halves of the lanes in opposite order) hit all banks.
+// V of a tile from codes to f16, the blocks b0, b0 + step, ... by one warp: times 2^(the
+// block's exponent - top), in the layout that the MMA reads ([eight keys][64 values][8
+// keys][64 values], 128-byte swizzle).  Values that no row sees become zeros.  Eight lanes take
+// four 16-code chunks of keys q and q ^ 5: those lie in different halves of the banks
+// as codes (by bit 2 or, in rows of 64 bytes, bit 0) and in every other 16 bytes as f16 (by bit 0).
 template <int D, int kBlock>
 __device__ __forceinline__ void widen_values(const uint8_t* V, uint8_t* W, const uint8_t* bytes,
-                                             int top, const RowTile& t, int v0) {
-  constexpr int kChunks = D / 16, kRowsAtOnce = 32 / kChunks;
-  const int lane = threadIdx.x & 31, c = lane % kChunks, r0 = lane / kChunks;
+                                             int top, const RowTile& t, int v0, int b0, int step) {
+  constexpr int kHalves = D / 64, kTrips = kBlock / 8 * kHalves;  // eight keys, 64 values a trip
+  const int lane = threadIdx.x & 31, c = lane & 3, q = lane >> 3;
+  const int r = (lane & 4) != 0 ? q ^ 5 : q;  // key of eight
   const bool edge = tile_has_unseen(t, v0);
-  // the first of a lane's two stores: its chunk's first or second eight values
-  const int sub0 = D == 128 ? c / 4 : 0;
+  const uint8_t* from = V + r * D + (D == 128 ? c ^ (r & 3) : c ^ (r >> 1)) * 16;
+  uint8_t* to = W + r * 128 + ((c * 2 ^ r) << 4);
+  uint4 x[kTrips];
+  auto read = [&](int b, int k) {
+    // the upper four chunks of a row of 128 bytes lie 64 bytes from the lower ones; which come
+    // first goes by bit 2 of the key
+    const int half = D == 128 ? (((k % kHalves) * 4) ^ (r & 4)) * 16 : 0;
+    x[k] = *reinterpret_cast<const uint4*>(from + (b * kBlock + k / kHalves * 8) * D + half);
+  };
+#pragma unroll
+  for (int k = 0; k < kTrips; ++k) read(b0, k);
 #pragma unroll 1
-  for (int b = 0; b < kKeys / kBlock; ++b) {
+  for (int b = b0; b < kKeys / kBlock; b += step) {
     const int e = static_cast<int>(bytes[b]) - top;  // <= 0
-    const uint32_t f = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+    const uint32_t f =
+        e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
     const uint32_t f2 = f | f << 16;
-    uint4 x[kBlock / kRowsAtOnce > 0 ? kBlock / kRowsAtOnce : 1];
 #pragma unroll
-    for (int k = 0; k < kBlock / kRowsAtOnce; ++k) {
-      const int r = b * kBlock + k * kRowsAtOnce + r0;
-      const int at = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-      x[k] = *reinterpret_cast<const uint4*>(V + r * D + at * 16);
-    }
-#pragma unroll
-    for (int k = 0; k < kBlock / kRowsAtOnce; ++k) {
-      const int r = b * kBlock + k * kRowsAtOnce + r0;
-      const bool zero = edge && !place_seen(t, v0 + r);
-      uint32_t w[8];
-      const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[2 * i] = scale2_f16(e4m3x2_f16x2(in[i]), f2);
-        w[2 * i + 1] = scale2_f16(e4m3x2_f16x2(in[i] >> 16), f2);
-      }
-      if (zero)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 0;
-      uint8_t* row = W + (r / 8) * (D / 64) * 1024 + (c / 4) * 1024 + (r % 8) * 128;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int sub = s ^ sub0;
-        const uint4 y = sub ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(row + ((((c % 4) * 2 + sub) ^ (r & 7)) << 4)) = y;
-      }
+    for (int k = 0; k < kTrips; ++k) {
+      uint4 lo = widen8_e4m3(x[k].x, x[k].y, f2), hi = widen8_e4m3(x[k].z, x[k].w, f2);
+      if (b + step < kKeys / kBlock) read(b + step, k);
+      if (edge && !place_seen(t, v0 + b * kBlock + k / kHalves * 8 + r)) lo = hi = make_uint4(0, 0, 0, 0);
+      uint8_t* at = to + ((b * kBlock / 8 + k / kHalves) * kHalves + k % kHalves) * 1024;
+      *reinterpret_cast<uint4*>(at) = lo;
+      *reinterpret_cast<uint4*>(W + ((at - W) ^ 16)) = hi;
     }
   }
 }
 
-// A thread's row of Q (`from`, or null: zeros) as two e4m3 terms, each 128 bytes a row: planes
-// of kHalf rows, or the halves of one row with D = 64.  Returns the power of two that it was divided by.
+// The largest magnitude of kLanes lanes' eight values.
+template <int kLanes>
+__device__ __forceinline__ float row_top(const uint4& x) {
+  const uint32_t m = 0x7fff7fffu;
+  auto most = [](uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+  };
+  uint32_t y = most(most(x.x & m, x.y & m), most(x.z & m, x.w & m));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) y = most(y, __shfl_xor_sync(0xffffffffu, y, o));
+  return fmaxf(bf16_lo(y), bf16_hi(y));
+}
+
+// 32 rows of Q in shared memory, from `row0` on, from bf16 as TMA lays them ([64 values of a
+// head][rows][64 values], 128-byte swizzle) to two e4m3 terms in the same place, each 128
+// bytes a row (a plane each, or the halves of a row with D = 64), divided by powers of two,
+// of which a lane gets its row's.  One warp, D / 8 lanes to a row.
 template <int D>
-__device__ __forceinline__ float split_query(const bf16* from, uint8_t* Q, int row) {
-  uint4 x[D / 8];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-    x[i] = from ? *reinterpret_cast<const uint4*>(from + 8 * i) : make_uint4(0, 0, 0, 0);
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
+__device__ __forceinline__ float split_queries(uint8_t* Q, int row0) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  constexpr uint32_t kPlane = kHalf * 128;
+  const int lane = threadIdx.x & 31, i = lane % kLanes;
+  float scale = 1.f;
+#pragma unroll 1
+  for (int k = 0; k < 32; k += kAtOnce) {
+    const int row = row0 + k + lane / kLanes;
+    uint8_t* at = Q + row * 128;
+    const uint4 x = *reinterpret_cast<const uint4*>(at + (i / 8) * kPlane + (((i % 8) ^ (row & 7)) << 4));
+    const int byte = min(scale_byte(row_top<kLanes>(x)), 253);
+    const float inv = scale_of(254 - byte);
     float y[8];
-    load8(reinterpret_cast<const bf16*>(&x[i]), y);
+    load8(reinterpret_cast<const bf16*>(&x), y);
+    uint32_t t1[2], t2[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(y[k]));
+    for (int e = 0; e < 2; ++e)
+      split4_e4m3(pack_f16x2(y[4 * e] * inv, y[4 * e + 1] * inv),
+                  pack_f16x2(y[4 * e + 2] * inv, y[4 * e + 3] * inv), t1[e], t2[e]);
+    __syncwarp();  // (the rows have been read)
+    const int c = i / 2, c2 = D == 128 ? c : 4 + c;
+    at += (i & 1) * 8;
+    *reinterpret_cast<uint2*>(at + ((c ^ (row & 7)) << 4)) = make_uint2(t1[0], t1[1]);
+    *reinterpret_cast<uint2*>(at + (D == 128 ? kPlane : 0) + ((c2 ^ (row & 7)) << 4)) =
+        make_uint2(t2[0], t2[1]);
+    const int own = __shfl_sync(0xffffffffu, byte, lane % kAtOnce * kLanes);
+    if (lane / kAtOnce * kAtOnce == k) scale = scale_of(own);
   }
-  const int byte = min(scale_byte(top), 253);
-  const float inv = scale_of(254 - byte);
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    uint32_t t1[4], t2[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float y[8];
-      load8(reinterpret_cast<const bf16*>(&x[2 * c + i]), y);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] *= inv;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t t = pack4_e4m3(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-        const float2 lo = unpack2_e4m3(t), hi = unpack2_e4m3(t >> 16);
-        t1[2 * i + k] = t;
-        t2[2 * i + k] = pack4_e4m3(y[4 * k] - lo.x, y[4 * k + 1] - lo.y, y[4 * k + 2] - hi.x,
-                                   y[4 * k + 3] - hi.y);
-      }
-    }
-    uint8_t* to = Q + row * 128;
-    const int second = D == 128 ? kHalf * 128 : 0, c2 = D == 128 ? c : 4 + c;
-    *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-    *reinterpret_cast<uint4*>(to + second + ((c2 ^ (row & 7)) << 4)) =
-        make_uint4(t2[0], t2[1], t2[2], t2[3]);
-  }
-  return scale_of(byte);
+  return scale;
+}
+
+// What a row's scores of a block are multiplied with; never 0, which -infinity would make NaN.
+__device__ __forceinline__ float scale_with(float key, float row) {
+  return fmaxf(key * row, 1.2e-38f);
 }
 
 template <int D, int kBlock>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_prefill_8bit_kernel(const __grid_constant__ CUtensorMap tm_k,
+    attn_prefill_8bit_kernel(const __grid_constant__ CUtensorMap tm_q,
+                             const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
   using La = Lay<D>;
   constexpr int kK = La::kK, kV = La::kV, kW = La::kW;
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int half_rows = P.rows / 2;  // rows of a half that are in use
 
   if (tid == 0) {
+    ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
     for (int i = 0; i < kK; ++i) {
@@ -190,15 +192,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kV; ++i) {
       ptx::mbar_init(&M.v_full[i], 1);
-      ptx::mbar_init(&M.v_empty[i], 1);
+      ptx::mbar_init(&M.v_empty[i], kWideners);
     }
     for (int i = 0; i < kW; ++i) {
-      ptx::mbar_init(&M.w_full[i], 1);
+      ptx::mbar_init(&M.w_full[i], kWideners);
       ptx::mbar_init(&M.w_empty[i], 1);
     }
-    init_scales(M.scales, 9);
+    init_scales(M.scales, 8 + kWideners);
     for (int h = 0; h < 2; ++h) {
+      ptx::mbar_init(&M.q_in[h], 1);
       ptx::mbar_init(&M.q_full[h], 4);
+      ptx::mbar_init(&M.q_empty[h], 1);
       ptx::mbar_init(&M.s_full[h], 1);
       ptx::mbar_init(&M.p_half[h], 4);
       ptx::mbar_init(&M.p_full[h], 4);
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(&M.seg_full[i], 1);
-      ptx::mbar_init(&M.seg_empty[i], 11);
+      ptx::mbar_init(&M.seg_empty[i], 10 + kWideners);
     }
     M.abort = 0;
     ptx::fence_mbar_init();
@@ -229,10 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;  // S (and P) of half h at h * 128, O at 256 + h * 128
 
-  // (each role's branch begins with its own split, so that the compiler knows
-  // the number of registers on every path)
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLeast));
   if (warp == 8) {
     // ---------------- schedule and TMA ----------------------------------
     Walker walk;
@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_proxy_async_smem();
     __syncwarp();
     TileLoader<D, 1> load(P);
-    int nk = 0, nv = 0;  // tiles brought in
+    int nk = 0, nv = 0;     // tiles brought in
+    int q_use[2] = {0, 0};  // segments of each half
     bool ok = true;
     SplitItem mine = {};
     for (int sg = 0; ok; ++sg) {
@@ -257,6 +258,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       load.begin(P, g);
       if (P.join_after && g.parts > 1 && g.cta0 == blockIdx.x)
         mine = {g.parts, g.tok0, g.t.row0, g.t.n_rows, g.head, g.shared, {0, 0}};
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (g.t.n_rows <= h * half_rows) break;
+        if (q_use[h] > 0) ok = wait_all(&M.q_empty[h], (q_use[h] - 1) & 1, abort_f);
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&M.q_in[h], half_rows * D * 2);
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_rows(smem + La::oQ + h * La::kWide + x * (kHalf * 128), &tm_q, &M.q_in[h],
+                          g.head * P.group, g.tok0 + P.by_group(g.t.row0 + h * half_rows), x);
+        }
+        ++q_use[h];
+      }
+      __syncwarp();
       for (int i = 0; i < g.n && ok; ++i) {
         const int at = load.at(P, g, i);
         const uint32_t bytes = load.bytes(at);
@@ -274,6 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       // gave up: what is on its way into shared memory has to land first
       int none = 0;
+      for (int h = 0; h < 2; ++h)
+        if (q_use[h] > 0)
+          ptx::mbar_wait_bounded(&M.q_in[h], (q_use[h] - 1) & 1, &none, kAttnWaitNs / 8);
       for (int k = nk > kK ? nk - kK : 0; k < nk; ++k)
         ptx::mbar_wait_bounded(&M.k_full[k % kK], (k / kK) & 1, &none, kAttnWaitNs / 8);
       for (int k = nv > kV ? nv - kV : 0; k < nv; ++k)
@@ -289,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A bit for each half: parities of its Qs, of its tiles' P and of its O, and
       // whether it has had a segment.
       uint32_t q_par = 0, p_par = 0, o_par = 0, begun = 0;
-      auto issue_qk = [&](bool first, int n, int h, bool frees) {
+      auto issue_qk = [&](bool first, bool last, int n, int h, bool frees) {
         if (first) {
           wait_quiet(&M.q_full[h], (q_par >> h) & 1, abort_f);
           q_par ^= 1u << h;
@@ -306,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ks > 0 ? 1u : 0u);
         ptx::mma_commit(&M.s_full[h]);
         if (frees) ptx::mma_commit(&M.k_empty[st]);
+        if (last) ptx::mma_commit(&M.q_empty[h]);
       };
       auto issue_pv = [&](bool first, int n, int h, bool frees) {
         const int st = n % kW;
@@ -348,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (left > 0 && h <= two) issue_pv(first, n, h, h == two);
-          if (next > 0 && h <= next_two) issue_qk(next_first, n + 1, h, h == next_two);
+          if (next > 0 && h <= next_two) issue_qk(next_first, next == 1, n + 1, h, h == next_two);
         }
         if (next_first) {
           if (sg >= 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
@@ -363,25 +381,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 10) {
     // ---------------- scales ----------------------------------------------
-    fill_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
-  } else {
+    run_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
+  } else if (warp >= kFirstWidener) {
     // ---------------- V from codes to f16 ---------------------------------
     bool ok = true;
     int n = 0;
     for (int sg = 0; ok; ++sg) {
       ok = wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
       if (!ok) break;
-      const int tiles = M.ring[sg % kRing].n, first = M.ring[sg % kRing].first;
-      const RowTile t = M.ring[sg % kRing].t;
-      if (tiles == 0) break;
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
+      const Segment& g = M.ring[sg % kRing];
+      if (g.n == 0) break;
+      for (int i = 0; i < g.n && ok; ++i, ++n) {
         const int sc = n % kScaleRing;
         ok = wait_all(&M.scales.full[sc], (n / kScaleRing) & 1, abort_f) &&
              wait_all(&M.v_full[n % kV], (n / kV) & 1, abort_f) &&
              (n < kW || wait_all(&M.w_empty[n % kW], ((n / kW) & 1) ^ 1, abort_f));
         if (!ok) break;
         widen_values<D, kBlock>(smem + La::oV + n % kV * La::kTile, smem + La::oW + n % kW * La::kWide,
-                                M.scales.v[sc], M.scales.top[sc], t, (first + i) * kKeys);
+                                M.scales.v[sc], M.scales.top[sc], g.t, (g.first + i) * kKeys,
+                                warp - kFirstWidener, kWideners);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -390,11 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(&M.scales.empty[sc]);
         }
       }
+      __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
     }
-  }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMost));
+  } else if (warp < 8) {
     // ---------------- softmax and results ---------------------------------
     const int h = warp >> 2, w = warp & 3;
     const int row = w * 32 + lane;  // of the half, and the TMEM lane
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_s = tmem + lanes + h * 128, tm_o = tmem + lanes + 256 + h * 128;
     const float c = P.scale_log2;
     const int bar = 1 + h;
-    int tile = 0;  // tiles of this half so far
+    int tile = 0, segs = 0;  // tiles and segments of this half so far
     // The warpgroup's four warps meet at barriers: after a wait that gave up
     // they run on (every later wait returns at once) to the vote.
     for (int sg = 0;; ++sg) {
@@ -423,10 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
-      // (the MMAs that read the last one's Q are done: so are its scores)
-      const float q_scale = split_query<D>(
-          mine ? P.q + (g.tok0 + tok) * P.q_stride + head * D : nullptr,
-          smem + La::oQ + h * La::kWide, row);
+      wait_quiet(&M.q_in[h], segs++ & 1, abort_f);
+      const float q_scale = c * split_queries<D>(smem + La::oQ + h * La::kWide, w * 32);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&M.q_full[h]);
@@ -438,37 +453,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int v0 = (g.first + i) * kKeys, key0 = window_key(g.t, v0);  // place, key
         const int sc = (g.tile0 + i) % kScaleRing;
         wait_quiet(&M.scales.full[sc], ((g.tile0 + i) / kScaleRing) & 1, abort_f);
-        float kc[kKeys / kBlock];  // of each block's keys, times the row's own and c
-#pragma unroll
-        for (int b = 0; b < kKeys / kBlock; ++b)
-          kc[b] = fmaxf(M.scales.k[sc][b] * (q_scale * c), 1.2e-38f);
+        const float* key_scale = M.scales.k[sc];
         const int top = M.scales.top[sc];
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&M.scales.empty[sc]);
-          if (alone) ptx::mbar_arrive(&M.scales.empty[sc]);  // for the other half's warp
-        }
         wait_quiet(&M.s_full[h], tile & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
-        float s[kKeys];
-#pragma unroll
-        for (int k = 0; k < kKeys; k += 32)
-          ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
-        ptx::tmem_ld_wait();
-        mask_scores(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0, s);
+        mask_in_place(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0);
+        // The scores are read twice, 64 at a time: two short loops in place of one long
+        // piece of code (prompt of 8192: 821 us with all 128 in registers).
         float mx = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < kKeys; k += 64) {
+          float s[64];
+          ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s));
+          ptx::tmem_ld32(tm_s + k + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          ptx::tmem_ld_wait();
 #pragma unroll
-        for (int b = 0; b < kKeys / kBlock; ++b) {
-          const float* x = s + b * kBlock;
-          float y = max3(x[0], x[1], x[2]), z = max3(x[3], x[4], x[5]);
+          for (int b = 0; b < 64 / kBlock; ++b) {
+            const float* x = s + b * kBlock;
+            float y = max3(x[0], x[1], x[2]), z = max3(x[3], x[4], x[5]);
 #pragma unroll
-          for (int k = 6; k + 3 < kBlock; k += 4) {
-            y = max3(y, x[k], x[k + 1]);
-            z = max3(z, x[k + 2], x[k + 3]);
+            for (int j = 6; j + 3 < kBlock; j += 4) {
+              y = max3(y, x[j], x[j + 1]);
+              z = max3(z, x[j + 2], x[j + 3]);
+            }
+            y = max3(y, x[kBlock - 2], x[kBlock - 1]);
+            mx = fmaxf(mx, fmaxf(y, z) * scale_with(key_scale[k / kBlock + b], q_scale));
           }
-          y = max3(y, x[kBlock - 2], x[kBlock - 1]);
-          mx = fmaxf(mx, fmaxf(y, z) * kc[b]);
         }
         // (rows that are not in use hold anything: they have no say)
         if (top > R || __any_sync(0xffffffffu, mine && mx > m + kMost)) {
@@ -488,30 +499,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float neg = m == -INFINITY ? 0.f : -m;
         const uint64_t neg2 = pack2(neg, neg);
         uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll 1
+        for (int k = 0; k < kKeys; k += 64) {
+          float s[64];
+          ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s));
+          ptx::tmem_ld32(tm_s + k + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          ptx::tmem_ld_wait();
+          uint32_t p[32];
 #pragma unroll
-        for (int k = 0; k < kKeys; k += 32) {
-          uint32_t p[16];
+          for (int b = 0; b < 64 / kBlock; ++b) {
+            const float kc = scale_with(key_scale[k / kBlock + b], q_scale);
+            const uint64_t kc2 = pack2(kc, kc);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float a, b;
-            const float kx = kc[(k + 2 * x) / kBlock];
-            unpack2(fma2(pack2(s[k + 2 * x], s[k + 2 * x + 1]), pack2(kx, kx), neg2), &a, &b);
-            a = exp2_fast(a);
-            b = exp2_fast(b);
-            if (x & 1)
-              sum1 = add2(sum1, pack2(a, b));
-            else
-              sum0 = add2(sum0, pack2(a, b));
-            p[x] = pack_f16x2(a, b);
+            for (int x = b * kBlock; x < (b + 1) * kBlock; x += 2) {
+              float e0, e1;
+              unpack2(fma2(pack2(s[x], s[x + 1]), kc2, neg2), &e0, &e1);
+              e0 = exp2_fast(e0);
+              e1 = exp2_fast(e1);
+              if (x & 2)
+                sum1 = add2(sum1, pack2(e0, e1));
+              else
+                sum0 = add2(sum0, pack2(e0, e1));
+              p[x / 2] = pack_f16x2(e0, e1);
+            }
           }
-          ptx::tmem_st16(tm_s + k / 2, p);
-          if (k == 32 || k == 96) {
-            // each half of the keys goes to the MMA as soon as it is there
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(k == 32 ? &M.p_half[h] : &M.p_full[h]);
-          }
+          ptx::tmem_st32(tm_s + k / 2, p);
+          // each half of the keys goes to the MMA as soon as it is there
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(k == 0 ? &M.p_half[h] : &M.p_full[h]);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&M.scales.empty[sc]);
+          if (alone) ptx::mbar_arrive(&M.scales.empty[sc]);  // for the other half's warp
         }
         float a, b;
         unpack2(add2(sum0, sum1), &a, &b);
@@ -519,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the item, or this CTA's part of it, is done
-      finish_half<D>(P, g, h, row, mine, g.tok0 + tok, head, m, l, scale_of(max(R, 1)), tm_o, &M.o_done[h],
+      finish_half<D, true>(P, g, h, row, mine, g.tok0 + tok, head, m, l, scale_of(max(R, 1)), tm_o, &M.o_done[h],
                      (tile - 1) & 1, abort_f, &M.o_empty[h], &M.seg_empty[sg % kRing], &M.last[h], bar);
     }
   }
@@ -534,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int kBlock>
-cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& P,
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& P,
                    cudaStream_t st, const DeviceInfo& dev) {
   using La = Lay<D>;
   constexpr size_t smem = 1024 + La::oMisc + sizeof(Misc<D>);
@@ -554,20 +576,21 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnP
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, P)) != cudaSuccess || !P.join_after)
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, P)) != cudaSuccess || !P.join_after)
     return e;
   return launch_attn_join(P, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prefill_8bit(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                     const AttnParams& P, cudaStream_t st, const DeviceInfo& dev) {
+cudaError_t launch_attn_prefill_8bit(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                     const CUtensorMap& tm_v, const AttnParams& P,
+                                     cudaStream_t st, const DeviceInfo& dev) {
   if (P.kv.page_size == 8)
-    return P.kv.head_dim == 64 ? launch<64, 8>(tm_k, tm_v, P, st, dev)
-                               : launch<128, 8>(tm_k, tm_v, P, st, dev);
-  return P.kv.head_dim == 64 ? launch<64, 16>(tm_k, tm_v, P, st, dev)
-                             : launch<128, 16>(tm_k, tm_v, P, st, dev);
+    return P.kv.head_dim == 64 ? launch<64, 8>(tm_q, tm_k, tm_v, P, st, dev)
+                               : launch<128, 8>(tm_q, tm_k, tm_v, P, st, dev);
+  return P.kv.head_dim == 64 ? launch<64, 16>(tm_q, tm_k, tm_v, P, st, dev)
+                             : launch<128, 16>(tm_q, tm_k, tm_v, P, st, dev);
 }
 
 }  // namespace lora
