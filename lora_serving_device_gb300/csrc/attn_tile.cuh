@@ -274,21 +274,43 @@ struct TileLoader {
   }
 };
 
-// Scales of the 8-bit cache's key tiles, ahead of their use, by tile (of the CTA) % kScaleRing.
-constexpr int kScaleRing = 8;
+// Scales of the 8-bit cache's key tiles, a batch of P.scale_tiles of them at a time, ahead of
+// their use.  Batch n of the CTA lies in tiles 4 (n % kBatches) and on.
+template <int kBatches>
 struct ScaleRing {
-  float k[kScaleRing][16];    // of a tile's blocks of keys
-  uint8_t v[kScaleRing][16];  // bytes of its blocks of values
-  int top[kScaleRing];        // the largest of them since the segment's first tile
-  uint64_t full[kScaleRing], empty[kScaleRing];
+  float k[4 * kBatches][16];    // of a tile's blocks of keys
+  uint8_t v[4 * kBatches][16];  // bytes of its blocks of values
+  int top[4 * kBatches];        // the largest of them since the segment's first tile
+  uint64_t full[kBatches], empty[kBatches];
 };
-// One thread; `readers` arrivals free a tile's.
-__device__ __forceinline__ void init_scales(ScaleRing& S, int readers) {
-  for (int i = 0; i < kScaleRing; ++i) {
+// One thread; `readers` arrivals free a batch.
+template <int kBatches>
+__device__ __forceinline__ void init_scales(ScaleRing<kBatches>& S, int readers) {
+  for (int i = 0; i < kBatches; ++i) {
     ptx::mbar_init(&S.full[i], 1);
     ptx::mbar_init(&S.empty[i], readers);
   }
 }
+// A reader's way through them: of(i) before tile i of segment g, done(i) after it (all lanes).
+struct ScaleReader {
+  int lg;  // log2 of a batch' tiles
+  __device__ __forceinline__ explicit ScaleReader(const AttnParams& P) : lg(P.scale_tiles == 2 ? 1 : 2) {}
+  __device__ __forceinline__ int batch(const Segment& g, int i) const { return g.batch0 + (i >> lg); }
+  template <int kBatches>
+  __device__ __forceinline__ int of(ScaleRing<kBatches>& S, const Segment& g, int i, volatile int* abort) const {
+    const int n = batch(g, i), in = i & ((1 << lg) - 1);
+    if (in == 0) wait_quiet(&S.full[n % kBatches], (n / kBatches) & 1, abort);
+    return n % kBatches * 4 + in;
+  }
+  // `times`: for how many warps
+  template <int kBatches>
+  __device__ __forceinline__ void done(ScaleRing<kBatches>& S, const Segment& g, int i, int times = 1) const {
+    if ((i & ((1 << lg) - 1)) != (1 << lg) - 1 && i != g.n - 1) return;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+      for (int k = 0; k < times; ++k) ptx::mbar_arrive(&S.empty[batch(g, i) % kBatches]);
+  }
+};
 // Looks them up, one warp: a lane to a block, as many tiles at once as 32 lanes have blocks
 // of, the next ones' page ids on their way beside them.  Scales of blocks that no row sees
 // are not read: 1 for keys, and for values a byte that leaves `top` where it is.
@@ -301,7 +323,7 @@ struct ScaleFinder {
       : block(min(P.kv.page_size, kScaleBlock)),
         lg_block(block == 8 ? 3 : 4),
         per_tile(kKeys / block),
-        at_once(32 / per_tile),
+        at_once(P.scale_tiles),
         mine((threadIdx.x & 31) / per_tile),
         b((threadIdx.x & 31) % per_tile) {}
   __device__ __forceinline__ void fetch(const AttnParams& P, const Segment& g, int i0) {
@@ -317,8 +339,9 @@ struct ScaleFinder {
     fetch(P, g, 0);
   }
   // Tiles i0 .. i0 + at_once - 1 of the segment; false once a wait of the CTA gave up.
-  __device__ __forceinline__ bool fill(const AttnParams& P, ScaleRing& S, const Segment& g, int i0,
-                                       volatile int* abort) {
+  template <int kBatches>
+  __device__ __forceinline__ bool fill(const AttnParams& P, ScaleRing<kBatches>& S,
+                                       const Segment& g, int i0, volatile int* abort) {
     const int lane = threadIdx.x & 31;
     int kb = 127, vb = 1;
     if (seen && id >= 0 && id < P.kv.n_pages) {
@@ -329,31 +352,30 @@ struct ScaleFinder {
       vb = scale_read(P.v_scale[at]);
     }
     if (i0 + at_once < g.n) fetch(P, g, i0 + at_once);
-    const int n = min(at_once, g.n - i0), tile = g.tile0 + i0;
-    for (int i = tile; i < tile + n; ++i)
-      if (i >= kScaleRing &&
-          !wait_all(&S.empty[i % kScaleRing], ((i / kScaleRing) & 1) ^ 1, abort))
-        return false;
-    const int slot = (tile + mine) % kScaleRing;
+    const int n = min(at_once, g.n - i0), batch = g.batch0 + i0 / at_once;
+    const int slot = batch % kBatches;
+    if (batch >= kBatches && !wait_all(&S.empty[slot], ((batch / kBatches) & 1) ^ 1, abort))
+      return false;
     if (mine < n) {
-      S.k[slot][b] = scale_of(kb);
-      S.v[slot][b] = static_cast<uint8_t>(vb);
+      S.k[slot * 4 + mine][b] = scale_of(kb);
+      S.v[slot * 4 + mine][b] = static_cast<uint8_t>(vb);
     }
     // the largest so far, tile by tile
     for (int i = 0; i < n; ++i) {
       top = max(top, __reduce_max_sync(0xffffffffu, mine == i ? vb : 0));
-      if (lane == 0) S.top[(tile + i) % kScaleRing] = top;
+      if (lane == 0) S.top[slot * 4 + i] = top;
     }
     __syncwarp();
-    if (lane < n) ptx::mbar_arrive(&S.full[(tile + lane) % kScaleRing]);
+    if (lane == 0) ptx::mbar_arrive(&S.full[slot]);
     return true;
   }
 };
 
 // The whole of a warp's work: scales of all tiles of the segments in `ring`, to the first end.
-__device__ __forceinline__ void run_scales(const AttnParams& P, ScaleRing& S, const Segment* ring,
-                                           int ring_size, uint64_t* seg_full, uint64_t* seg_empty,
-                                           volatile int* abort) {
+template <int kBatches>
+__device__ __forceinline__ void run_scales(const AttnParams& P, ScaleRing<kBatches>& S,
+                                           const Segment* ring, int ring_size, uint64_t* seg_full,
+                                           uint64_t* seg_empty, volatile int* abort) {
   ScaleFinder find(P);
   bool ok = true;
   for (int sg = 0; ok; ++sg) {

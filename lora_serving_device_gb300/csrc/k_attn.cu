@@ -148,6 +148,8 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
   P.prior_lse = reinterpret_cast<float*>(base + w.prior_lse);
   P.k_scale = a.k_scale;
   P.v_scale = a.v_scale;
+  // (a warp's 32 lanes take a block of 16 tokens each, or of 8 in pages of 8)
+  P.scale_tiles = !bits8 ? 0 : kv.page_size == 8 ? 2 : 4;
   for (int phase = a.n_groups > 0 ? 1 : 0; phase >= 0; --phase) {
     P.groups_phase = phase == 1;
     P.rows = w.shape[phase].rows;

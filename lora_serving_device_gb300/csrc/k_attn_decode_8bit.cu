@@ -74,7 +74,7 @@ struct Misc {
   float4 red_max[W][A], red_sum[W][A];
   float m[W][A];
   float q_scale[W][La::N];
-  ScaleRing scales;
+  ScaleRing<4> scales;
   int row_hi[W][A], row_lo[W][A];
   uint64_t full_k[kStages], full_v[kStages], empty[kStages];
   uint64_t s_full[W][La::kSBufs], s_empty[W][La::kSBufs];
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     // wait that gave up they run on (every later wait returns at once) to
     // the vote at the next segment.
     uint32_t tile = 0;  // tiles of this warpgroup so far
+    const ScaleReader scales(P);
     for (int sg = wg;; sg += W) {
       wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
       if (named_any(kBar, 128, *abort_f != 0)) break;
@@ -391,12 +392,10 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         const int v0 = (g.first + i) * kKeys, v = v0 + j;  // places
         const int key0 = window_key(g.t, v0), key = key0 + j;
         const uint32_t in_cta = g.tile0 + i;
-        const uint32_t sc = in_cta % kScaleRing;
-        wait_quiet(&M.scales.full[sc], (in_cta / kScaleRing) & 1, abort_f);
+        const int sc = scales.of(M.scales, g, i, abort_f);
         const float kc = M.scales.k[sc][my_block] * c;
         const int vb = M.scales.v[sc][my_block], top_v = M.scales.top[sc];
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.scales.empty[sc]);
+        scales.done(M.scales, g, i);
         wait_quiet(&M.s_full[wg][tile % SB], (tile / SB) & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();

@@ -40,9 +40,9 @@ template <int D>
 struct Lay {
   static constexpr uint32_t kTile = kKeys * D;   // codes of K or V of a tile
   static constexpr uint32_t kWide = 2 * kTile;   // V of a tile in f16; Q's two terms of a half
-  static constexpr int kK = D == 128 ? 4 : 8;    // tiles of K in flight
+  static constexpr int kK = D == 128 ? 2 : 8;    // tiles of K in flight
   static constexpr int kV = D == 128 ? 2 : 4;    // of V as codes
-  static constexpr int kW = D == 128 ? 2 : 4;    // of V in f16
+  static constexpr int kW = D == 128 ? 3 : 4;    // of V in f16
   static constexpr uint32_t oV = kK * kTile;
   static constexpr uint32_t oW = oV + kV * kTile;
   static constexpr uint32_t oQ = oW + kW * kWide;
@@ -53,13 +53,14 @@ template <int D>
 struct Misc {
   using La = Lay<D>;
   Segment ring[kRing];
-  ScaleRing scales;
+  ScaleRing<2> scales;
   uint64_t k_full[La::kK], k_empty[La::kK];
   uint64_t v_full[La::kV], v_empty[La::kV];
   uint64_t w_full[La::kW], w_empty[La::kW];
   uint64_t q_in[2], q_full[2], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
   uint64_t seg_full[kRing], seg_empty[kRing];
+  uint8_t q_scale[2][2][kHalf];  // bytes of the rows of Q, by segment % 2 and half
   uint32_t tmem;
   int abort;
   int last[2];
@@ -124,14 +125,13 @@ __device__ __forceinline__ float row_top(const uint4& x) {
 // 32 rows of Q in shared memory, from `row0` on, from bf16 as TMA lays them ([64 values of a
 // head][rows][64 values], 128-byte swizzle) to two e4m3 terms in the same place, each 128
 // bytes a row (a plane each, or the halves of a row with D = 64), divided by powers of two,
-// of which a lane gets its row's.  One warp, D / 8 lanes to a row.
+// whose bytes go to `bytes`.  One warp, D / 8 lanes to a row.
 template <int D>
-__device__ __forceinline__ float split_queries(uint8_t* Q, int row0) {
+__device__ __forceinline__ void split_queries(uint8_t* Q, int row0, uint8_t* bytes) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
   constexpr uint32_t kPlane = kHalf * 128;
   const int lane = threadIdx.x & 31, i = lane % kLanes;
-  float scale = 1.f;
-#pragma unroll 1
+#pragma unroll 2
   for (int k = 0; k < 32; k += kAtOnce) {
     const int row = row0 + k + lane / kLanes;
     uint8_t* at = Q + row * 128;
@@ -151,10 +151,8 @@ __device__ __forceinline__ float split_queries(uint8_t* Q, int row0) {
     *reinterpret_cast<uint2*>(at + ((c ^ (row & 7)) << 4)) = make_uint2(t1[0], t1[1]);
     *reinterpret_cast<uint2*>(at + (D == 128 ? kPlane : 0) + ((c2 ^ (row & 7)) << 4)) =
         make_uint2(t2[0], t2[1]);
-    const int own = __shfl_sync(0xffffffffu, byte, lane % kAtOnce * kLanes);
-    if (lane / kAtOnce * kAtOnce == k) scale = scale_of(own);
+    if (i == 0) bytes[row] = static_cast<uint8_t>(byte);
   }
-  return scale;
 }
 
 // What a row's scores of a block are multiplied with; never 0, which -infinity would make NaN.
@@ -363,10 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_two = M.ring[(sg + 1) % kRing].t.n_rows > half_rows;
           next_first = true;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (left > 0 && h <= two) issue_pv(first, n, h, h == two);
-          if (next > 0 && h <= next_two) issue_qk(next_first, next == 1, n + 1, h, h == next_two);
+        // (the next segment's Q has to come first: it must not hold up the last products)
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          const int h = next_first ? x & 1 : x >> 1;
+          if ((next_first ? x >> 1 : x & 1) == 0) {
+            if (left > 0 && h <= two) issue_pv(first, n, h, h == two);
+          } else if (next > 0 && h <= next_two) {
+            issue_qk(next_first, next == 1, n + 1, h, h == next_two);
+          }
         }
         if (next_first) {
           if (sg >= 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
@@ -383,18 +386,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- scales ----------------------------------------------
     run_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
   } else if (warp >= kFirstWidener) {
-    // ---------------- V from codes to f16 ---------------------------------
+    // ---------------- Q into terms, V from codes to f16 --------------------
+    const ScaleReader scales(P);
     bool ok = true;
-    int n = 0;
+    int n = 0, q_use[2] = {0, 0};
     for (int sg = 0; ok; ++sg) {
       ok = wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
       if (!ok) break;
       const Segment& g = M.ring[sg % kRing];
       if (g.n == 0) break;
+      // Q first, beside the softmax warps' results of the segment before
+#pragma unroll 1
+      for (int h = 0; h < 2 && ok && g.t.n_rows > h * half_rows; ++h) {
+        ok = wait_all(&M.q_in[h], q_use[h]++ & 1, abort_f);
+        split_queries<D>(smem + La::oQ + h * La::kWide, (warp - kFirstWidener) * 32, M.q_scale[sg & 1][h]);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&M.q_full[h]);
+      }
       for (int i = 0; i < g.n && ok; ++i, ++n) {
-        const int sc = n % kScaleRing;
-        ok = wait_all(&M.scales.full[sc], (n / kScaleRing) & 1, abort_f) &&
-             wait_all(&M.v_full[n % kV], (n / kV) & 1, abort_f) &&
+        const int sc = scales.of(M.scales, g, i, abort_f);
+        ok = wait_all(&M.v_full[n % kV], (n / kV) & 1, abort_f) &&
              (n < kW || wait_all(&M.w_empty[n % kW], ((n / kW) & 1) ^ 1, abort_f));
         if (!ok) break;
         widen_values<D, kBlock>(smem + La::oV + n % kV * La::kTile, smem + La::oW + n % kW * La::kWide,
@@ -405,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ptx::mbar_arrive(&M.w_full[n % kW]);
           ptx::mbar_arrive(&M.v_empty[n % kV]);
-          ptx::mbar_arrive(&M.scales.empty[sc]);
         }
+        scales.done(M.scales, g, i);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
@@ -419,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_s = tmem + lanes + h * 128, tm_o = tmem + lanes + 256 + h * 128;
     const float c = P.scale_log2;
     const int bar = 1 + h;
+    const ScaleReader scales(P);
     int tile = 0, segs = 0;  // tiles and segments of this half so far
     // The warpgroup's four warps meet at barriers: after a wait that gave up
     // they run on (every later wait returns at once) to the vote.
@@ -440,19 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
-      wait_quiet(&M.q_in[h], segs++ & 1, abort_f);
-      const float q_scale = c * split_queries<D>(smem + La::oQ + h * La::kWide, w * 32);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&M.q_full[h]);
-      const bool alone = g.t.n_rows <= half_rows;
+      wait_quiet(&M.q_full[h], segs++ & 1, abort_f);
+      const float q_scale = c * scale_of(M.q_scale[sg & 1][h][row]);
+      const int readers = g.t.n_rows <= half_rows ? 2 : 1;  // the other half's warp too, if it has no rows
       float m = -INFINITY, l = 0.f;  // m: what weights are relative to
       int R = 0;                     // the largest exponent of a value block so far
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int v0 = (g.first + i) * kKeys, key0 = window_key(g.t, v0);  // place, key
-        const int sc = (g.tile0 + i) % kScaleRing;
-        wait_quiet(&M.scales.full[sc], ((g.tile0 + i) / kScaleRing) & 1, abort_f);
+        const int sc = scales.of(M.scales, g, i, abort_f);
         const float* key_scale = M.scales.k[sc];
         const int top = M.scales.top[sc];
         wait_quiet(&M.s_full[h], tile & 1, abort_f);
@@ -530,11 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(k == 0 ? &M.p_half[h] : &M.p_full[h]);
         }
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&M.scales.empty[sc]);
-          if (alone) ptx::mbar_arrive(&M.scales.empty[sc]);  // for the other half's warp
-        }
+        scales.done(M.scales, g, i, readers);
         float a, b;
         unpack2(add2(sum0, sum1), &a, &b);
         l += a + b;
