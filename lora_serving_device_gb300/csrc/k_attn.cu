@@ -160,7 +160,10 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     // Splitting an item costs each of its CTAs a part, so short ones stay whole:
     // up to 8 tiles of single tokens (the tokens after a prefix of 8K: 56.5 us,
     // split 59.8), two of prompts.
-    P.over = w.shape[phase].prefill ? 3 : 1;
+#ifndef EXP_OVER
+#define EXP_OVER 4
+#endif
+    P.over = w.shape[phase].prefill ? (bits8 ? EXP_OVER : 3) : 1;
     P.whole = w.shape[phase].prefill ? 2 : 8;
     // By the fewest items that this many rows can make: with 38 and more one has
     // a few parts, which the last CTA to arrive adds up; fewer items have many

@@ -20,7 +20,7 @@
 // softmax and results this is; a tile's codes are half its bytes.
 //
 // Warps: 0-3 softmax of half 0, 4-7 of half 1 (Q in, results out), 8 schedule and TMA,
-// 9 MMA issue, 10 scales, 12-15 V to f16.  Every wait is bounded; on timeout the kernel
+// 9 MMA issue, 10 scales, 12-15 Q and V.  Every wait is bounded; on timeout the kernel
 // raises LORA_DEVERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
@@ -43,6 +43,7 @@ struct Lay {
   static constexpr int kK = D == 128 ? 2 : 8;    // tiles of K in flight
   static constexpr int kV = D == 128 ? 2 : 4;    // of V as codes
   static constexpr int kW = D == 128 ? 3 : 4;    // of V in f16
+  static constexpr int kUsed = D == 128 ? 4 : 8;  // at least kK and kW
   static constexpr uint32_t oV = kK * kTile;
   static constexpr uint32_t oW = oV + kV * kTile;
   static constexpr uint32_t oQ = oW + kW * kWide;
@@ -54,9 +55,10 @@ struct Misc {
   using La = Lay<D>;
   Segment ring[kRing];
   ScaleRing<2> scales;
-  uint64_t k_full[La::kK], k_empty[La::kK];
+  uint64_t k_full[La::kK];
   uint64_t v_full[La::kV], v_empty[La::kV];
-  uint64_t w_full[La::kW], w_empty[La::kW];
+  uint64_t w_full[La::kW];
+  uint64_t used[La::kUsed];  // Q K^T of a tile and P V of the one before are done
   uint64_t q_in[2], q_full[2], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
   uint64_t seg_full[kRing], seg_empty[kRing];
@@ -131,7 +133,7 @@ __device__ __forceinline__ void split_queries(uint8_t* Q, int row0, uint8_t* byt
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
   constexpr uint32_t kPlane = kHalf * 128;
   const int lane = threadIdx.x & 31, i = lane % kLanes;
-#pragma unroll 2
+#pragma unroll 4
   for (int k = 0; k < 32; k += kAtOnce) {
     const int row = row0 + k + lane / kLanes;
     uint8_t* at = Q + row * 128;
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
   using La = Lay<D>;
-  constexpr int kK = La::kK, kV = La::kV, kW = La::kW;
+  constexpr int kK = La::kK, kV = La::kV, kW = La::kW, kUsed = La::kUsed;
   using Mi = Misc<D>;
   constexpr uint32_t kIdescQK = ptx::idesc_e4m3_f32(kHalf, kKeys, false, false);
   constexpr uint32_t kIdescPV = ptx::idesc_f16_f32(kHalf, D, false, true);
@@ -186,7 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&tm_v);
     for (int i = 0; i < kK; ++i) {
       ptx::mbar_init(&M.k_full[i], 1);
-      ptx::mbar_init(&M.k_empty[i], 1);
     }
     for (int i = 0; i < kV; ++i) {
       ptx::mbar_init(&M.v_full[i], 1);
@@ -194,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kW; ++i) {
       ptx::mbar_init(&M.w_full[i], kWideners);
-      ptx::mbar_init(&M.w_empty[i], 1);
     }
+    for (int i = 0; i < kUsed; ++i) ptx::mbar_init(&M.used[i], 1);
     init_scales(M.scales, 8 + kWideners);
     for (int h = 0; h < 2; ++h) {
       ptx::mbar_init(&M.q_in[h], 1);
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < g.n && ok; ++i) {
         const int at = load.at(P, g, i);
         const uint32_t bytes = load.bytes(at);
-        if (nk >= kK) ok = wait_all(&M.k_empty[nk % kK], ((nk / kK) & 1) ^ 1, abort_f);
+        if (nk >= kK) ok = wait_all(&M.used[(nk - kK) % kUsed], ((nk - kK) / kUsed) & 1, abort_f);
         if (!ok) break;
         load.load(&tm_k, &M.k_full[nk % kK], smem + nk % kK * La::kTile, at, bytes);
         ++nk;
@@ -296,89 +297,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ---------------- MMA issue ------------------------------------------
-    // One thread: P V of tile n and Q K^T of tile n + 1, half by half, so that
-    // the tensor cores have the other half's work while a softmax runs.
+    // One thread: P V of a tile, then Q K^T of the next, which takes P's place, half by half,
+    // so that the tensor cores have the other half's work while a softmax runs.  A commit
+    // takes this thread 150 to 200 cycles, so there are few: scores tell that the product
+    // before them is done too, and one a tile frees its K and the V before.
     if (elect_one()) {
+      const uint32_t q_tiles = desc_lo(ptx::smem_u32(smem + La::oQ), 16);
       const uint32_t k_tiles = desc_lo(ptx::smem_u32(smem), 16);
       const uint32_t w_tiles = desc_lo(ptx::smem_u32(smem + La::oW), 1024);
-      // A bit for each half: parities of its Qs, of its tiles' P and of its O, and
-      // whether it has had a segment.
-      uint32_t q_par = 0, p_par = 0, o_par = 0, begun = 0;
-      auto issue_qk = [&](bool first, bool last, int n, int h, bool frees) {
-        if (first) {
-          wait_quiet(&M.q_full[h], (q_par >> h) & 1, abort_f);
-          q_par ^= 1u << h;
-        }
-        const int st = n % kK;
-        wait_quiet(&M.k_full[st], (n / kK) & 1, abort_f);
-        ptx::tc_fence_after();
-        const uint32_t qa = desc_lo(ptx::smem_u32(smem + La::oQ + h * La::kWide), 16);
-        const uint32_t ka = k_tiles + st * (La::kTile / 16);
-#pragma unroll
-        for (int ks = 0; ks < 2 * D / 32; ++ks)  // both terms of Q against the same keys
-          mma_ss_8bit(tmem + h * 128, qa + ((ks / 4) * (kHalf * 128) + (ks % 4) * 32) / 16,
-                      desc_hi(1024), ka + ks % (D / 32) * 2, desc_hi_span(8 * D, D), kIdescQK,
-                      ks > 0 ? 1u : 0u);
-        ptx::mma_commit(&M.s_full[h]);
-        if (frees) ptx::mma_commit(&M.k_empty[st]);
-        if (last) ptx::mma_commit(&M.q_empty[h]);
-      };
-      auto issue_pv = [&](bool first, int n, int h, bool frees) {
-        const int st = n % kW;
-        const uint32_t va = w_tiles + st * (La::kWide / 16);
-        if (h == 0) wait_quiet(&M.w_full[st], (n / kW) & 1, abort_f);
-        if (first) {
-          // the half's previous segment has been read out of O
-          if ((begun >> h) & 1) {
-            wait_quiet(&M.o_empty[h], (o_par >> h) & 1, abort_f);
-            o_par ^= 1u << h;
-          }
-          begun |= 1u << h;
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          wait_quiet(x ? &M.p_full[h] : &M.p_half[h], (p_par >> h) & 1, abort_f);
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int ks = 4 * x; ks < 4 * x + 4; ++ks)
-            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
-                   va + ks * 2 * kGroupBytes / 16, desc_hi(kGroupBytes), kIdescPV,
-                   ks > 0 || !first ? 1u : 0u);
-        }
-        ptx::mma_commit(&M.o_done[h]);
-        if (frees) ptx::mma_commit(&M.w_empty[st]);
-        p_par ^= 1u << h;
-      };
-      int sg = -1, left = 0;  // the segment of tile n, and its key tiles to go
-      bool two = false, first = false;
+      // a bit for each half: parities of its tiles' P and of its segments, and whether it has had one
+      uint32_t p_par = 0, seg_par = 0, begun = 0;
+      int n = 0;  // tiles
 #pragma unroll 1
-      for (int n = -1; !*abort_f; ++n) {
-        int next = left - 1;
-        bool next_two = two, next_first = false;
-        if (next <= 0) {  // the next tile is of the next segment
-          wait_quiet(&M.seg_full[(sg + 1) % kRing], ((sg + 1) / kRing) & 1, abort_f);
-          next = M.ring[(sg + 1) % kRing].n;
-          next_two = M.ring[(sg + 1) % kRing].t.n_rows > half_rows;
-          next_first = true;
-        }
-        // (the next segment's Q has to come first: it must not hold up the last products)
+      for (int sg = 0;; ++sg) {
+        wait_quiet(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+        const int tiles = M.ring[sg % kRing].n, halves = M.ring[sg % kRing].t.n_rows > half_rows ? 2 : 1;
+        if (tiles == 0 || *abort_f) break;
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          const int h = next_first ? x & 1 : x >> 1;
-          if ((next_first ? x >> 1 : x & 1) == 0) {
-            if (left > 0 && h <= two) issue_pv(first, n, h, h == two);
-          } else if (next > 0 && h <= next_two) {
-            issue_qk(next_first, next == 1, n + 1, h, h == next_two);
+        for (int i = 0; i <= tiles && !*abort_f; ++i, ++n) {
+          const int w_at = (n - 1) % kW, k_at = n % kK;
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {
+            const uint32_t tm_s = tmem + h * 128, tm_o = tmem + 256 + h * 128;
+            if (i > 0) {
+              const uint32_t va = w_tiles + w_at * (La::kWide / 16);
+              if (h == 0) wait_quiet(&M.w_full[w_at], ((n - 1) / kW) & 1, abort_f);
+              // the half's previous segment has been read out of O
+              if (i == 1 && ((begun >> h) & 1) != 0)
+                wait_quiet(&M.o_empty[h], ((seg_par >> h) & 1) ^ 1, abort_f);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                wait_quiet(x ? &M.p_full[h] : &M.p_half[h], (p_par >> h) & 1, abort_f);
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int ks = 4 * x; ks < 4 * x + 4; ++ks)
+                  mma_ts(tm_o, tm_s + ks * 8, va + ks * 2 * kGroupBytes / 16,
+                         desc_hi(kGroupBytes), kIdescPV, ks > 0 || i > 1 ? 1u : 0u);
+              }
+              p_par ^= 1u << h;
+            }
+            if (i < tiles) {
+              const uint32_t qa = q_tiles + h * (La::kWide / 16), ka = k_tiles + k_at * (La::kTile / 16);
+              if (i == 0) wait_quiet(&M.q_full[h], (seg_par >> h) & 1, abort_f);
+              if (h == 0) wait_quiet(&M.k_full[k_at], (n / kK) & 1, abort_f);
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < 2 * D / 32; ++ks)  // both terms of Q against the same keys
+                mma_ss_8bit(tm_s, qa + ((ks / 4) * (kHalf * 128) + (ks % 4) * 32) / 16,
+                            desc_hi(1024), ka + ks % (D / 32) * 2, desc_hi_span(8 * D, D),
+                            kIdescQK, ks > 0 ? 1u : 0u);
+              ptx::mma_commit(&M.s_full[h]);
+              if (i == tiles - 1) ptx::mma_commit(&M.q_empty[h]);
+            } else {
+              ptx::mma_commit(&M.o_done[h]);
+              seg_par ^= 1u << h;
+              begun |= 1u << h;
+            }
           }
+          if (i < tiles) ptx::mma_commit(&M.used[n % kUsed]);
         }
-        if (next_first) {
-          if (sg >= 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
-          ++sg;
-        }
-        if (next <= 0) break;
-        left = next;
-        two = next_two;
-        first = next_first;
+        --n;
+        ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
       }
     }
     __syncwarp();
@@ -407,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < g.n && ok; ++i, ++n) {
         const int sc = scales.of(M.scales, g, i, abort_f);
         ok = wait_all(&M.v_full[n % kV], (n / kV) & 1, abort_f) &&
-             (n < kW || wait_all(&M.w_empty[n % kW], ((n / kW) & 1) ^ 1, abort_f));
+             (n < kW || wait_all(&M.used[(n - kW + 1) % kUsed], ((n - kW + 1) / kUsed) & 1, abort_f));
         if (!ok) break;
         widen_values<D, kBlock>(smem + La::oV + n % kV * La::kTile, smem + La::oW + n % kW * La::kWide,
                                 M.scales.v[sc], M.scales.top[sc], g.t, (g.first + i) * kKeys,
@@ -499,9 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f_all = top - R < 127 ? f * scale_of(127 - (top - R)) : 0.f;
           R = top;
           if (i > 0) {
-            wait_quiet(&M.o_done[h], (tile - 1) & 1, abort_f);
-            __syncwarp();
-            ptx::tc_fence_after();
+            // (the product before these scores is done)
             scale_result<D>(tm_o, f_all);
           }
         }
@@ -547,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the item, or this CTA's part of it, is done
       finish_half<D, true>(P, g, h, row, mine, g.tok0 + tok, head, m, l, scale_of(max(R, 1)), tm_o, &M.o_done[h],
-                     (tile - 1) & 1, abort_f, &M.o_empty[h], &M.seg_empty[sg % kRing], &M.last[h], bar);
+                     (segs - 1) & 1, abort_f, &M.o_empty[h], &M.seg_empty[sg % kRing], &M.last[h], bar);
     }
   }
 
