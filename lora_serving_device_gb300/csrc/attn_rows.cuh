@@ -177,48 +177,48 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
         joined.write16(k, o);
       }
     }
-    return;
-  }
-  float o[D];
+  } else {
+    float o[D];
 #pragma unroll
-  for (int k = 0; k < D; k += 32)
-    ptx::tmem_ld32(tm_o + k, *reinterpret_cast<uint32_t(*)[32]>(o + k));
-  ptx::tmem_ld_wait();
-  read();
-  float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
-  if (mine) {
-    float4* part = part_row<D>(P, slot, h, row);
+    for (int k = 0; k < D; k += 32)
+      ptx::tmem_ld32(tm_o + k, *reinterpret_cast<uint32_t(*)[32]>(o + k));
+    ptx::tmem_ld_wait();
+    read();
+    float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
+    if (mine) {
+      float4* part = part_row<D>(P, slot, h, row);
 #pragma unroll
-    for (int k = 0; k < D; k += 4)
-      part[(k / 4) * kHalf] = make_float4(o[k] * unit, o[k + 1] * unit, o[k + 2] * unit, o[k + 3] * unit);
-    ml[slot * 2 * kHalf] = make_float2(m, l);
-  }
-  if (!P.join_after && last_to_arrive(P, g, h, row == 0, last, bar, 128) && mine) {
-    // few parts: the last to arrive adds them up, in their order
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int q = 0; q < g.parts; ++q)
-      top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
-#pragma unroll
-    for (int k = 0; k < D; ++k) o[k] = 0.f;
-#pragma unroll 1
-    for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
-      const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
-      const float f = exp2_fast(v.x - top);
-      sum += f * v.y;
-      const float4* from = part_row<D>(P, part_slot(g, q), h, row);
-#pragma unroll
-      for (int k = 0; k < D; k += 4) {
-        const float4 z = __ldcg(from + (k / 4) * kHalf);
-        o[k] += f * z.x;
-        o[k + 1] += f * z.y;
-        o[k + 2] += f * z.z;
-        o[k + 3] += f * z.w;
-      }
+      for (int k = 0; k < D; k += 4)
+        part[(k / 4) * kHalf] = make_float4(o[k] * unit, o[k + 1] * unit, o[k + 2] * unit, o[k + 3] * unit);
+      ml[slot * 2 * kHalf] = make_float2(m, l);
     }
-    const RowWriter<D> joined(P, g.shared, t, head, true, top, sum);
+    if (!P.join_after && last_to_arrive(P, g, h, row == 0, last, bar, 128) && mine) {
+      // few parts: the last to arrive adds them up, in their order
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+      for (int q = 0; q < g.parts; ++q)
+        top = fmaxf(top, __ldcg(&ml[part_slot(g, q) * 2 * kHalf].x));
 #pragma unroll
-    for (int k = 0; k < D; k += 16) joined.write16(k, o + k);
+      for (int k = 0; k < D; ++k) o[k] = 0.f;
+#pragma unroll 1
+      for (int q = 0; q < g.parts && top > -INFINITY; ++q) {
+        const float2 v = __ldcg(&ml[part_slot(g, q) * 2 * kHalf]);
+        const float f = exp2_fast(v.x - top);
+        sum += f * v.y;
+        const float4* from = part_row<D>(P, part_slot(g, q), h, row);
+#pragma unroll
+        for (int k = 0; k < D; k += 4) {
+          const float4 z = __ldcg(from + (k / 4) * kHalf);
+          o[k] += f * z.x;
+          o[k + 1] += f * z.y;
+          o[k + 2] += f * z.z;
+          o[k + 3] += f * z.w;
+        }
+      }
+      const RowWriter<D> joined(P, g.shared, t, head, true, top, sum);
+#pragma unroll
+      for (int k = 0; k < D; k += 16) joined.write16(k, o + k);
+    }
   }
 }
 
