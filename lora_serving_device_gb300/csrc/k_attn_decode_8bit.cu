@@ -24,8 +24,8 @@
 // multiplications; a warp of its own looks them up, tiles ahead.
 // The terms of P lie as [key][term, row]: a thread stores its key's in 16 bytes at once.
 //
-// Warps: 0 = schedule and TMA, 1 = MMA issue, 2-5 and 6-9 = softmax and epilogue, 10 =
-// scales.  Every wait is bounded; on timeout the kernel raises LORA_DEVERR_TIMEOUT.
+// Warps: 0 = schedule and TMA of K, 1 = MMA issue, 2-5 and 6-9 = softmax and epilogue, 10 =
+// scales, 11 = TMA of V.  Every wait is bounded; on timeout the kernel raises LORA_DEVERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
 #include "attn.cuh"
@@ -45,7 +45,7 @@ constexpr float kTerm = 16.f; // a term of P against the one before
 template <int D, int A>
 struct Lay {
   static constexpr int W = 2;
-  static constexpr int kThreads = 96 + 128 * W;
+  static constexpr int kThreads = 128 + 128 * W;
   static constexpr int N = 16;
   static constexpr int kPV = (3 * A + 15) / 16 * 16;
   static constexpr uint32_t kTile = kKeys * D;  // K or V of a tile
@@ -85,6 +85,13 @@ struct Misc {
   int abort;
   int last[W];
 };
+
+// After a wait that gave up: what is on its way into shared memory has to land first.
+__device__ __forceinline__ void drain(uint64_t* full, int stages, int tiles) {
+  int none = 0;
+  for (int k = tiles > stages ? tiles - stages : 0; k < tiles; ++k)
+    ptx::mbar_wait_bounded(&full[k % stages], (k / stages) & 1, &none, kAttnWaitNs / 8);
+}
 
 template <int D, int A>
 __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
@@ -130,7 +137,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(&M.seg_full[i], 1);
-      ptx::mbar_init(&M.seg_empty[i], 6);
+      ptx::mbar_init(&M.seg_empty[i], 7);
     }
     init_scales(M.scales, 4);
     M.abort = 0;
@@ -185,19 +192,10 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
         const int st = tile % kStages;
         if (tile >= kStages) ok = wait_all(&M.empty[st], ((tile / kStages) & 1) ^ 1, abort_f);
         if (!ok) break;
-        uint8_t* K = smem + st * La::kStage;
-        load.load(&tm_k, &M.full_k[st], K, at, bytes);
-        load.load(&tm_v, &M.full_v[st], K + La::kTile, at, bytes);
+        load.load(&tm_k, &M.full_k[st], smem + st * La::kStage, at, bytes);
       }
     }
-    if (!ok) {
-      // gave up: what is on its way into shared memory has to land first
-      int none = 0;
-      for (int k = tile > kStages ? tile - kStages : 0; k < tile; ++k) {
-        ptx::mbar_wait_bounded(&M.full_k[k % kStages], (k / kStages) & 1, &none, kAttnWaitNs / 8);
-        ptx::mbar_wait_bounded(&M.full_v[k % kStages], (k / kStages) & 1, &none, kAttnWaitNs / 8);
-      }
-    }
+    if (!ok) drain(M.full_k, kStages, tile);
   } else if (warp == 1) {
     // ---------------- MMA issue ------------------------------------------
     // One thread with two cursors over the same tiles: O += of tile pv as soon
@@ -288,6 +286,31 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
   } else if (warp == 10) {
     // ---------------- scales ----------------------------------------------
     run_scales(P, M.scales, M.ring, kRing, M.seg_full, M.seg_empty, abort_f);
+  } else if (warp == 11) {
+    // ---------------- TMA of V ---------------------------------------------
+    // A warp of its own: a box takes the warp that issues it ~40 ns, and pages of 16 tokens
+    // make 16 boxes a tile (64 tokens on 8K: one warp for K and V 109 us).
+    TileLoader<D, 1> load(P);
+    int tile = 0;
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      ok = wait_all(&M.seg_full[sg % kRing], (sg / kRing) & 1, abort_f);
+      if (!ok) break;
+      const Segment g = M.ring[sg % kRing];
+      if (g.n == 0) break;
+      load.begin(P, g);
+      for (int i = 0; i < g.n; ++i, ++tile) {
+        const int at = load.at(P, g, i);
+        const uint32_t bytes = load.bytes(at);
+        const int st = tile % kStages;
+        if (tile >= kStages) ok = wait_all(&M.empty[st], ((tile / kStages) & 1) ^ 1, abort_f);
+        if (!ok) break;
+        load.load(&tm_v, &M.full_v[st], smem + st * La::kStage + La::kTile, at, bytes);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
+    }
+    if (!ok) drain(M.full_v, kStages, tile);
   } else {
     // ---------------- softmax and epilogue --------------------------------
     const int w = warp & 3;                 // TMEM lanes 32w .. 32w + 31
