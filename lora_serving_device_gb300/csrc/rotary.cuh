@@ -49,15 +49,6 @@ __device__ __forceinline__ void load_rot(const AppendArgs& a, int T, int t, int 
   }
 }
 
-// The error of a row that is not rotated: one of its positions is outside the table.
-__device__ __forceinline__ void flag_bad_pos(const AppendArgs& a, int T, int t, int p) {
-  for (int i = 0, first = 0; i < a.n_axes && a.rot_dim > 0; first = a.axis_end[i++]) {
-    if (a.axis_end[i] == first) continue;  // an axis without pairs
-    const int x = a.pos != nullptr ? a.pos[static_cast<int64_t>(i) * T + t] : p;
-    if (x < 0 || x >= a.n_pos) flag_error(a.err, LORA_DEVERR_BAD_POS);
-  }
-}
-
 // A unit's two vectors of eight, x[0 .. 8) and x[8 .. 16): the pairs are (x[j], x[8 + j]),
 // or neighbours with kInter.
 template <bool kInter>
