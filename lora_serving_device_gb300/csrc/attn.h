@@ -43,7 +43,11 @@ struct PlanArgs {
   uint32_t* err;
   int32_t* top;        // pages on the stack before any is taken
   int32_t* take_off;   // [n_seqs] pages that the sequences before take
+  // where kernels of their own count and push the ended requests' pages:
+  int64_t* give_off;   // [n_seqs] their places on the stack
+  int32_t *give, *span;  // [n_seqs] how many, and [n_seqs][2] the entries that hold them
   bool fill_here;      // one kernel does all
+  bool apart;
 };
 // see k_batch_plan.cu
 cudaError_t launch_batch_plan(const PlanArgs& a, cudaStream_t st);

@@ -223,7 +223,7 @@ lora_status_t lora_attn_prefix_8bit(const lora_paged_kv_t* kv, const uint8_t* k_
 }
 
 size_t lora_batch_plan_workspace_bytes(int32_t n_seqs) {
-  return n_seqs < 1 || n_seqs > LORA_MAX_SEQS ? 16 : 256 + static_cast<size_t>(n_seqs) * 4;
+  return n_seqs < 1 || n_seqs > LORA_MAX_SEQS ? 16 : 256 + static_cast<size_t>(n_seqs) * 24;
 }
 
 lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
@@ -262,7 +262,10 @@ lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
   a.slots = slots, a.pos = pos, a.n_free_out = n_free_out;
   a.err = static_cast<uint32_t*>(ws);
   a.top = reinterpret_cast<int32_t*>(base + 128);
-  a.take_off = reinterpret_cast<int32_t*>(base + 256);
+  a.give_off = reinterpret_cast<int64_t*>(base + 256);
+  a.take_off = reinterpret_cast<int32_t*>(a.give_off + n_seqs);
+  a.give = a.take_off + n_seqs;
+  a.span = a.give + n_seqs;
   return launch_batch_plan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK
                                                                                 : LORA_ERR_CUDA;
 }

@@ -2,14 +2,16 @@
 // of its requests (lora_batch_plan).
 //
 // Two sums run over the sequences: rows (q_off) and pages (given back, then
-// taken); the rest is a lookup a row.  One block makes the sums, kThreads
-// sequences at a time, and pushes the pages of ended requests (a warp to a
-// request); its prefix sums leave by the workspace.  Rows are then independent: a
-// thread finds its row's sequence in q_off, and its page either in the table or, if
+// taken); the rest is a lookup a row.  One block makes the sums, kThreads sequences at
+// a time, and up to that many leave their ended requests' pages to it too (a warp to a
+// request); with more, kernels before and after it count and push them, a warp each over
+// the whole GPU (3000 requests, 333 of them ended: 31 us in the one block, 19 us).  Rows are then
+// independent: a thread finds its row's sequence in q_off, and its page either in the table or, if
 // the page is new, on the stack at the place that the sums give it.  A page's first
 // new row writes the page's table entry.
 //
-// Bound by latency: 20 bytes a sequence and 12 a row.
+// Bound by latency: 20 bytes a sequence and 12 a row (64 single tokens: 4.1 us, of which an
+// empty launch takes half).
 #include "attn.h"
 #include "attn.cuh"
 
@@ -78,6 +80,59 @@ __device__ __forceinline__ Sums block_scan(Sums x, Sums* warp_sums, Sums* total)
   return y;
 }
 
+// Pages [from, to) of sequence s's row, by one warp: how many there are (all lanes), and
+// onto the stack from place `at` on.
+__device__ __forceinline__ int count_pages(const PlanArgs& a, int s, int from, int to) {
+  const int32_t* row = a.block_table + static_cast<int64_t>(s) * a.max_pages;
+  int n = 0;
+#pragma unroll 4
+  for (int c = from + (threadIdx.x & 31); c < to; c += 32) n += row[c] >= 0 && row[c] < a.n_pages ? 1 : 0;
+  return __reduce_add_sync(0xffffffffu, n);
+}
+__device__ __forceinline__ void push_pages(const PlanArgs& a, int s, int from, int to, int64_t at) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* row = a.block_table + static_cast<int64_t>(s) * a.max_pages;
+#pragma unroll 4
+  for (int c = from; c < to; c += 32) {
+    const int id = c + lane < to ? row[c + lane] : -1;
+    const bool page = id >= 0 && id < a.n_pages;
+    const uint32_t pages = __ballot_sync(0xffffffffu, page);
+    const int64_t place = at + __popc(pages & ((1u << lane) - 1u));
+    if (page && place < a.free_cap) a.free_pages[place] = id;
+    at += __popc(pages);
+  }
+  if (lane == 0 && at > a.free_cap) flag_error(a.err, LORA_DEVERR_BAD_LEN);
+}
+// The pages that sequence s holds alone: [from, to) of its row.
+__device__ __forceinline__ void own_pages(const PlanArgs& a, int s, int* from, int* to) {
+  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.lg_page;
+  const int64_t cached = min(max(static_cast<int64_t>(a.n_cached[s]), int64_t{0}), cap);
+  *from = a.n_shared != nullptr ? max(a.n_shared[s], 0) : 0;
+  *to = static_cast<int>((cached + a.page_size - 1) >> a.lg_page);
+}
+
+// Of the ended requests, a warp each, before the sums (kPush: after them).
+template <bool kPush>
+__global__ void __launch_bounds__(kFillThreads) batch_plan_given_kernel(const PlanArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int s = (blockIdx.x * kFillThreads + threadIdx.x) / 32;
+  if (s >= a.n_seqs || a.n_new[s] >= 0) return;
+  if constexpr (kPush) {
+    // (n_cached may have become kv_len: the entries are those that were counted)
+    push_pages(a, s, a.span[2 * s], a.span[2 * s + 1], a.give_off[s]);
+  } else {
+    int from, to;
+    own_pages(a, s, &from, &to);
+    const int n = count_pages(a, s, from, to);
+    if ((threadIdx.x & 31) == 0) {
+      a.give[s] = n;
+      a.span[2 * s] = from;
+      a.span[2 * s + 1] = to;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) {
   __shared__ Sums warp_sums[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -117,17 +172,18 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
     const int have = static_cast<int>((cached + a.page_size - 1) >> a.lg_page);
     const int need = static_cast<int>((min(len, cap) + a.page_size - 1) >> a.lg_page);
     const int take = ended ? 0 : need - have;
-    // pages of ended requests: a warp counts those of its lanes, one after another
     int give = 0;
-    const int32_t* table = a.block_table;
-    for (uint32_t left = __ballot_sync(0xffffffffu, ended && have > shared); left != 0; left &= left - 1) {
-      const int src = __ffs(left) - 1;
-      const int from = __shfl_sync(0xffffffffu, shared, src), to = __shfl_sync(0xffffffffu, have, src);
-      const int32_t* row = table + static_cast<int64_t>(s0 + (tid & ~31) + src) * a.max_pages;
-      int n = 0;
-      for (int c = from + lane; c < to; c += 32) n += row[c] >= 0 && row[c] < a.n_pages ? 1 : 0;
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == src) give = n;
+    if (a.apart) {
+      if (ended && s < a.n_seqs) give = a.give[s];
+    } else {
+      // pages of ended requests: a warp counts those of its lanes, one after another
+      for (uint32_t left = __ballot_sync(0xffffffffu, ended && have > shared); left != 0;
+           left &= left - 1) {
+        const int src = __ffs(left) - 1;
+        const int from = __shfl_sync(0xffffffffu, shared, src), to = __shfl_sync(0xffffffffu, have, src);
+        const int n = count_pages(a, s0 + (tid & ~31) + src, from, to);
+        if (lane == src) give = n;
+      }
     }
     const Sums p = block_scan({take, give}, warp_sums, &total);
     if (s < a.n_seqs) {
@@ -137,20 +193,14 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
       if (bad) flag_error(a.err, bad);
     }
     const int64_t first = n_free + given + p.b - give;
-    for (uint32_t left = __ballot_sync(0xffffffffu, give > 0); left != 0; left &= left - 1) {
-      const int src = __ffs(left) - 1;
-      const int from = __shfl_sync(0xffffffffu, shared, src), to = __shfl_sync(0xffffffffu, have, src);
-      int64_t at = __shfl_sync(0xffffffffu, first, src);
-      const int32_t* row = table + static_cast<int64_t>(s0 + (tid & ~31) + src) * a.max_pages;
-      for (int c = from; c < to; c += 32) {
-        const int id = c + lane < to ? row[c + lane] : -1;
-        const bool page = id >= 0 && id < a.n_pages;
-        const uint32_t pages = __ballot_sync(0xffffffffu, page);
-        const int64_t place = at + __popc(pages & ((1u << lane) - 1u));
-        if (page && place < a.free_cap) a.free_pages[place] = id;
-        at += __popc(pages);
+    if (a.apart) {
+      if (s < a.n_seqs) a.give_off[s] = first;
+    } else {
+      for (uint32_t left = __ballot_sync(0xffffffffu, give > 0); left != 0; left &= left - 1) {
+        const int src = __ffs(left) - 1;
+        const int from = __shfl_sync(0xffffffffu, shared, src), to = __shfl_sync(0xffffffffu, have, src);
+        push_pages(a, s0 + (tid & ~31) + src, from, to, __shfl_sync(0xffffffffu, first, src));
       }
-      if (lane == 0 && at > a.free_cap) flag_error(a.err, LORA_DEVERR_BAD_LEN);
     }
     taken += total.a;
     given += total.b;
@@ -181,20 +231,30 @@ __global__ void __launch_bounds__(kFillThreads) batch_plan_fill_kernel(const Pla
 cudaError_t launch_batch_plan(const PlanArgs& args, cudaStream_t st) {
   PlanArgs a = args;
   a.fill_here = a.T <= 2 * kThreads;
+  a.apart = a.n_seqs > kThreads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, batch_plan_kernel, a);
-  if (e != cudaSuccess || a.fill_here) return e;
-  cfg.gridDim = dim3((a.T + kFillThreads - 1) / kFillThreads);
-  cfg.blockDim = dim3(kFillThreads);
-  return cudaLaunchKernelEx(&cfg, batch_plan_fill_kernel, a);
+  auto run = [&](void (*kernel)(PlanArgs), int blocks, int threads) {
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+  };
+  const int seq_blocks = (a.n_seqs * 32 + kFillThreads - 1) / kFillThreads;
+  cudaError_t e = cudaSuccess;
+  if (a.apart) {
+    a.fill_here = false;
+    e = run(batch_plan_given_kernel<false>, seq_blocks, kFillThreads);
+  }
+  if (e == cudaSuccess) e = run(batch_plan_kernel, 1, kThreads);
+  if (e == cudaSuccess && a.apart) e = run(batch_plan_given_kernel<true>, seq_blocks, kFillThreads);
+  if (e == cudaSuccess && !a.fill_here && a.T > 0)
+    e = run(batch_plan_fill_kernel, (a.T + kFillThreads - 1) / kFillThreads, kFillThreads);
+  return e;
 }
 
 }  // namespace lora
