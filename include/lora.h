@@ -696,12 +696,16 @@ lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
  * of a call may append to one block.
  *
  * lora_attn_paged_8bit, lora_attn_prefix_8bit: lora_attn_paged and lora_attn_prefix over
- * it; the same masks, workspaces (lora_attn_workspace_bytes) and errors.  Weights and q enter their products
- * as sums of e4m3 terms where the keys stand in the MMA's M (where lora_attn_paged has
- * the weights as a pair of bf16): three terms of a weight, exact to 2^-12 of itself and
- * 2^-23 of the row's largest (at the largest v_scale seen), and two of q, exact to 2^-17
- * of its row's largest value.  Elsewhere codes become bf16 values, exactly, and the weights are
- * one bf16, as in lora_attn_paged.  Scales of blocks that no row sees may hold anything.
+ * it; the same masks, workspaces (lora_attn_workspace_bytes) and errors.  The keys' codes
+ * enter their product as they are, and a row of q as two e4m3 terms, off by at most 2^-17 of its
+ * largest value.  Where the keys stand in the MMA's M (where lora_attn_paged has the
+ * weights as a pair of bf16) a weight enters its product as three e4m3 terms, off by 2^-12 of
+ * itself or 2^-23 of the row's largest, whichever is more, and by as much of the product's
+ * at the largest v_scale seen; elsewhere as one f16, off by 2^-11 of itself, beside values that are
+ * f16, off by at most 2^-33 of the largest scale's.  Scores, maxima, sums and the accumulator
+ * are fp32, and the result is rounded once.  So max_q_len, and a prompt in the same batch, change the
+ * rounding of a single token's weights.  Scales of blocks that no row sees may hold
+ * anything.
  */
 lora_status_t lora_kv_append_8bit(const lora_paged_kv_t* kv, uint8_t* k_scale, uint8_t* v_scale,
                                   const void* q, int64_t q_stride, const void* k,

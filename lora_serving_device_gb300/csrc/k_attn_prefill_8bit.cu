@@ -59,10 +59,13 @@ struct Misc {
   uint64_t v_full[La::kV], v_empty[La::kV];
   uint64_t w_full[La::kW];
   uint64_t used[La::kUsed];  // Q K^T of a tile and P V of the one before are done
-  uint64_t q_in[2], q_full[2], q_empty[2];
+  uint64_t q_in[2], q_empty[2];
+  // Of a half's segments in turn: the next one's Q can be there before the softmax warps have
+  // waited for this one's, and one barrier would then be two phases on.
+  uint64_t q_full[2][2];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
   uint64_t seg_full[kRing], seg_empty[kRing];
-  uint8_t q_scale[2][2][kHalf];  // bytes of the rows of Q, by segment % 2 and half
+  uint8_t q_scale[2][2][kHalf];  // bytes of the rows of Q, by the half's segment % 2 and half
   uint32_t tmem;
   int abort;
   int last[2];
@@ -200,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     init_scales(M.scales, 8 + kWideners);
     for (int h = 0; h < 2; ++h) {
       ptx::mbar_init(&M.q_in[h], 1);
-      ptx::mbar_init(&M.q_full[h], 4);
+      ptx::mbar_init(&M.q_full[h][0], kWideners);
+      ptx::mbar_init(&M.q_full[h][1], kWideners);
       ptx::mbar_init(&M.q_empty[h], 1);
       ptx::mbar_init(&M.s_full[h], 1);
       ptx::mbar_init(&M.p_half[h], 4);
@@ -305,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_tiles = desc_lo(ptx::smem_u32(smem + La::oQ), 16);
       const uint32_t k_tiles = desc_lo(ptx::smem_u32(smem), 16);
       const uint32_t w_tiles = desc_lo(ptx::smem_u32(smem + La::oW), 1024);
-      // a bit for each half: parities of its tiles' P and of its segments, and whether it has had one
-      uint32_t p_par = 0, seg_par = 0, begun = 0;
+      // of each half: the parity of its tiles' P, its segments (modulo 4), whether it has had one
+      uint32_t p_par = 0, segs = 0, begun = 0;
       int n = 0;  // tiles
 #pragma unroll 1
       for (int sg = 0;; ++sg) {
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (h == 0) wait_quiet(&M.w_full[w_at], ((n - 1) / kW) & 1, abort_f);
               // the half's previous segment has been read out of O
               if (i == 1 && ((begun >> h) & 1) != 0)
-                wait_quiet(&M.o_empty[h], ((seg_par >> h) & 1) ^ 1, abort_f);
+                wait_quiet(&M.o_empty[h], ((segs >> 2 * h) & 1) ^ 1, abort_f);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 wait_quiet(x ? &M.p_full[h] : &M.p_half[h], (p_par >> h) & 1, abort_f);
@@ -338,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (i < tiles) {
               const uint32_t qa = q_tiles + h * (La::kWide / 16), ka = k_tiles + k_at * (La::kTile / 16);
-              if (i == 0) wait_quiet(&M.q_full[h], (seg_par >> h) & 1, abort_f);
+              if (i == 0)
+                wait_quiet(&M.q_full[h][(segs >> 2 * h) & 1], (segs >> (2 * h + 1)) & 1, abort_f);
               if (h == 0) wait_quiet(&M.k_full[k_at], (n / kK) & 1, abort_f);
               ptx::tc_fence_after();
 #pragma unroll
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i == tiles - 1) ptx::mma_commit(&M.q_empty[h]);
             } else {
               ptx::mma_commit(&M.o_done[h]);
-              seg_par ^= 1u << h;
+              segs = (segs & ~(3u << 2 * h)) | ((segs >> 2 * h) + 1 & 3u) << 2 * h;
               begun |= 1u << h;
             }
           }
@@ -377,11 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Q first, beside the softmax warps' results of the segment before
 #pragma unroll 1
       for (int h = 0; h < 2 && ok && g.t.n_rows > h * half_rows; ++h) {
-        ok = wait_all(&M.q_in[h], q_use[h]++ & 1, abort_f);
-        split_queries<D>(smem + La::oQ + h * La::kWide, (warp - kFirstWidener) * 32, M.q_scale[sg & 1][h]);
+        ok = wait_all(&M.q_in[h], q_use[h] & 1, abort_f);
+        split_queries<D>(smem + La::oQ + h * La::kWide, (warp - kFirstWidener) * 32, M.q_scale[q_use[h] & 1][h]);
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.q_full[h]);
+        if (lane == 0) ptx::mbar_arrive(&M.q_full[h][q_use[h] & 1]);
+        ++q_use[h];
       }
       for (int i = 0; i < g.n && ok; ++i, ++n) {
         const int sc = scales.of(M.scales, g, i, abort_f);
@@ -432,8 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
-      wait_quiet(&M.q_full[h], segs++ & 1, abort_f);
-      const float q_scale = c * scale_of(M.q_scale[sg & 1][h][row]);
+      wait_quiet(&M.q_full[h][segs & 1], (segs >> 1) & 1, abort_f);
+      ++segs;
+      const float q_scale = c * scale_of(M.q_scale[(segs - 1) & 1][h][row]);
       const int readers = g.t.n_rows <= half_rows ? 2 : 1;  // the other half's warp too, if it has no rows
       float m = -INFINITY, l = 0.f;  // m: what weights are relative to
       int R = 0;                     // the largest exponent of a value block so far

@@ -906,6 +906,10 @@ class BatchPlan(collections.namedtuple("BatchPlan", "q_off kv_len slots pos n_fr
                                   (T, torch.int32), (1, torch.int32))))
 
 
+_PLAN_ARRAYS = ("n_cached", "n_new", "n_shared", "n_free", "out.q_off", "out.kv_len", "out.slots", "out.pos",
+                "out.n_free", "block_table", "free_pages")
+
+
 def batch_plan_workspace(n_seqs, device="cuda"):
     """A zero-filled workspace for batch_plan_t."""
     import torch
@@ -922,29 +926,31 @@ def batch_plan_t(block_table, n_cached, n_new, free_pages, n_free, page_size, n_
     one that the caller keeps (its kv_len may be n_cached, its n_free may be n_free: then
     a decode loop calls this with the same arrays in every step; slots or pos may be None)."""
     import torch
-    n_seqs, dev, i32 = n_cached.numel(), block_table.device, torch.int32
+    n_seqs, i32, dev = n_cached.numel(), torch.int32, block_table.get_device()
     if out is None:
-        out = _on(stream, BatchPlan.empty, n_seqs, 0 if T is None else T, device=dev)
+        out = _on(stream, BatchPlan.empty, n_seqs, 0 if T is None else T, device=block_table.device)
+    q_off, kv_len, slots, pos, n_free_out = out
     if T is None:
-        T = next((t.numel() for t in (out.slots, out.pos) if t is not None), 0)
-    for name, t, n, kind in (("block_table", block_table, None, i32), ("n_cached", n_cached, n_seqs, i32),
-                             ("n_new", n_new, n_seqs, i32), ("n_shared", n_shared, n_seqs, i32),
-                             ("free_pages", free_pages, None, i32), ("n_free", n_free, 1, i32),
-                             ("out.q_off", out.q_off, n_seqs + 1, i32), ("out.kv_len", out.kv_len, n_seqs, i32),
-                             ("out.slots", out.slots, T, torch.int64), ("out.pos", out.pos, T, i32),
-                             ("out.n_free", out.n_free, 1, i32)):
-        if t is None and name in ("n_shared", "out.slots", "out.pos"):
-            continue
-        if t.dtype is not kind or not t.is_contiguous() or t.device != dev or n not in (None, t.numel()):
-            raise TypeError(f"{name}: contiguous {kind}{'' if n is None else f' [{n}]'} on the block table's device")
+        T = slots.numel() if slots is not None else pos.numel() if pos is not None else 0
+    arrays = ((n_cached, i32, n_seqs), (n_new, i32, n_seqs), (n_shared, i32, n_seqs), (n_free, i32, 1),
+              (q_off, i32, n_seqs + 1), (kv_len, i32, n_seqs), (slots, torch.int64, T), (pos, i32, T),
+              (n_free_out, i32, 1), (block_table, i32, None), (free_pages, i32, None))
+    for i, (t, kind, n) in enumerate(arrays):
+        if t is None:
+            if i not in (2, 6, 7):
+                raise TypeError(f"{_PLAN_ARRAYS[i]}: missing")
+        elif t.dtype is not kind or t.get_device() != dev or not t.is_contiguous() or (n != t.numel() and n is not None):
+            raise TypeError(f"{_PLAN_ARRAYS[i]}: contiguous {kind}{'' if n is None else f' [{n}]'} on the block "
+                            "table's device")
     if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
         raise ValueError("block_table: [n_seqs, max_pages]")
-    if not block_table.is_cuda or torch.cuda.current_device() != dev.index:
-        raise ValueError(f"the block table is on {dev}; it has to be on the current CUDA device")
-    check(load().lora_batch_plan(_ptr(n_cached), _ptr(n_new), _ptr(n_shared), n_seqs, T, page_size,
-                                 block_table.shape[1], n_pages, _ptr(free_pages), free_pages.numel(), _ptr(n_free),
-                                 _ptr(block_table), _ptr(out.q_off), _ptr(out.kv_len), _ptr(out.slots),
-                                 _ptr(out.pos), _ptr(out.n_free), _ptr(ws), ws.numel(), _stream(stream)),
+    if dev < 0 or torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"the block table is on {block_table.device}; it has to be on the current CUDA device")
+    check(load().lora_batch_plan(n_cached.data_ptr(), n_new.data_ptr(), _ptr(n_shared), n_seqs, T, page_size,
+                                 block_table.shape[1], n_pages, free_pages.data_ptr(), free_pages.numel(),
+                                 n_free.data_ptr(), block_table.data_ptr(), q_off.data_ptr(), kv_len.data_ptr(),
+                                 _ptr(slots), _ptr(pos), n_free_out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream),
           "lora_batch_plan")
     return out
 
