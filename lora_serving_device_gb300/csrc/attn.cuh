@@ -247,7 +247,7 @@ struct Segment {
   RowTile t;
   int cta0, parts;   // the CTAs that share the item: cta0 .. cta0 + parts - 1
   int tile0;         // key tiles of this CTA before the segment
-  int batch0;        // batches of P.scale_tiles key tiles of this CTA before it
+  int batch0;        // batches of P.scale_tiles key tiles before it (a cache in 8 bits)
   int once;          // no other CTA reads these key tiles
   int slot;          // where this CTA's part goes, if parts > 1
 };
@@ -342,7 +342,7 @@ struct Walker {
   int u, begin, end; // next unit, the share's
   int total, share;  // units of the call, units of a CTA
   int tile_unit;     // first unit of the row tile
-  int done, batches; // key tiles of the segments so far, and batches of them
+  int done;          // key tiles of the segments so far
   int n_prob;
 
   __device__ __forceinline__ int units(const AttnParams& P) const {  // of the row tile
@@ -352,7 +352,7 @@ struct Walker {
   __device__ __forceinline__ void start(const AttnParams& P, ProblemSize* sizes) {
     const int hk = P.kv.n_kv_heads, lane = threadIdx.x & 31;
     n_prob = P.groups_phase ? P.n_groups : P.kv.n_seqs;
-    done = batches = 0;
+    done = 0;
     // the sizes of all problems, then the equal share of a CTA
     int64_t units = 0, items = 0;
     for (int p0 = 0; p0 < n_prob; p0 += 32) {
@@ -467,10 +467,8 @@ struct Walker {
     }
     g.slot = blockIdx.x == g.cta0 ? 1 : 0;
     g.tile0 = done;
-    g.batch0 = batches;
     g.once = pr.n_rows <= P.rows ? 1 : 0;
     done += g.n;
-    if (P.scale_tiles > 0) batches += (g.n + P.scale_tiles - 1) / P.scale_tiles;
     return g;
   }
 };

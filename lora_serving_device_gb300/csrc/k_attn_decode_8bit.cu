@@ -169,10 +169,12 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     ptx::fence_proxy_async_smem();
     __syncwarp();
     TileLoader<D, 1> load(P);
-    int tile = 0, ends = 0;
+    int tile = 0, ends = 0, batches = 0;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
-      const Segment g = walk.next(P);
+      Segment g = walk.next(P);
+      g.batch0 = batches;
+      batches += (g.n + P.scale_tiles - 1) / P.scale_tiles;
       if (sg >= kRing)
         ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
       if (!ok) break;

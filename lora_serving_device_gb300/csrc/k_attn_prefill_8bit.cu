@@ -244,11 +244,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     TileLoader<D, 1> load(P);
     int nk = 0, nv = 0;     // tiles brought in
+    int batches = 0;        // of their scales
     int q_use[2] = {0, 0};  // segments of each half
     bool ok = true;
     SplitItem mine = {};
     for (int sg = 0; ok; ++sg) {
-      const Segment g = walk.next(P);
+      Segment g = walk.next(P);
+      g.batch0 = batches;
+      batches += (g.n + P.scale_tiles - 1) / P.scale_tiles;
       if (sg >= kRing)
         ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
       if (!ok) break;
