@@ -29,7 +29,10 @@
 namespace lora {
 namespace {
 
+// Four warpgroups, of which two are the softmax's: 160 x 256 + 96 x 256 registers are the
+// launch's 128 x 512 (with 128 each, 48 bytes spill: 434 us for 427).
 constexpr int kThreads = 512;
+constexpr int kRegsMost = 160, kRegsLeast = 96;
 constexpr int kFirstWidener = 12, kWideners = 4;  // warps that widen V
 constexpr int kRing = 4;     // segments that the producer may run ahead
 // log2 of a row's largest weight when its reference is set, and of the largest that it then lets
@@ -40,14 +43,20 @@ template <int D>
 struct Lay {
   static constexpr uint32_t kTile = kKeys * D;   // codes of K or V of a tile
   static constexpr uint32_t kWide = 2 * kTile;   // V of a tile in f16; Q's two terms of a half
-  static constexpr int kK = D == 128 ? 2 : 8;    // tiles of K in flight
+  static constexpr int kK = D == 128 ? 2 : 4;    // tiles of K in flight
   static constexpr int kV = D == 128 ? 2 : 4;    // of V as codes
   static constexpr int kW = D == 128 ? 3 : 4;    // of V in f16
-  static constexpr int kUsed = D == 128 ? 4 : 8;  // at least kK and kW
+  static constexpr int kUsed = 4;  // at least kK and kW
+  // Buffers of a half's Q: with room for two the next segment's is there before this one's
+  // results are written.
+  static constexpr int kQ = D == 128 ? 1 : 2;
+  // Barriers and scale bytes of a half's Q, a segment each in turn: the softmax warps can come for
+  // a segment's when the Qs of kQ later ones are there, and have to find its own.
+  static constexpr int kQTurns = 2 * kQ;
   static constexpr uint32_t oV = kK * kTile;
   static constexpr uint32_t oW = oV + kV * kTile;
   static constexpr uint32_t oQ = oW + kW * kWide;
-  static constexpr uint32_t oMisc = oQ + 2 * kWide;
+  static constexpr uint32_t oMisc = oQ + 2 * kQ * kWide;  // [half][buffer]
 };
 
 template <int D>
@@ -59,13 +68,10 @@ struct Misc {
   uint64_t v_full[La::kV], v_empty[La::kV];
   uint64_t w_full[La::kW];
   uint64_t used[La::kUsed];  // Q K^T of a tile and P V of the one before are done
-  uint64_t q_in[2], q_empty[2];
-  // Of a half's segments in turn: the next one's Q can be there before the softmax warps have
-  // waited for this one's, and one barrier would then be two phases on.
-  uint64_t q_full[2][2];
+  uint64_t q_in[2][La::kQ], q_empty[2][La::kQ], q_full[2][La::kQTurns];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2];
   uint64_t seg_full[kRing], seg_empty[kRing];
-  uint8_t q_scale[2][2][kHalf];  // bytes of the rows of Q, by the half's segment % 2 and half
+  uint8_t q_scale[2][La::kQTurns][kHalf];  // bytes of the rows of Q
   uint32_t tmem;
   int abort;
   int last[2];
@@ -172,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap tm_v, const AttnParams P) {
   using La = Lay<D>;
   constexpr int kK = La::kK, kV = La::kV, kW = La::kW, kUsed = La::kUsed;
+  constexpr int kQ = La::kQ, kQTurns = La::kQTurns;
   using Mi = Misc<D>;
   constexpr uint32_t kIdescQK = ptx::idesc_e4m3_f32(kHalf, kKeys, false, false);
   constexpr uint32_t kIdescPV = ptx::idesc_f16_f32(kHalf, D, false, true);
@@ -202,10 +209,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kUsed; ++i) ptx::mbar_init(&M.used[i], 1);
     init_scales(M.scales, 8 + kWideners);
     for (int h = 0; h < 2; ++h) {
-      ptx::mbar_init(&M.q_in[h], 1);
-      ptx::mbar_init(&M.q_full[h][0], kWideners);
-      ptx::mbar_init(&M.q_full[h][1], kWideners);
-      ptx::mbar_init(&M.q_empty[h], 1);
+      for (int i = 0; i < kQ; ++i) {
+        ptx::mbar_init(&M.q_in[h][i], 1);
+        ptx::mbar_init(&M.q_empty[h][i], 1);
+      }
+      for (int i = 0; i < kQTurns; ++i) ptx::mbar_init(&M.q_full[h][i], kWideners);
       ptx::mbar_init(&M.s_full[h], 1);
       ptx::mbar_init(&M.p_half[h], 4);
       ptx::mbar_init(&M.p_full[h], 4);
@@ -236,6 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = M.tmem;  // S (and P) of half h at h * 128, O at 256 + h * 128
 
+  // (each role's branch begins with its own split, so that the compiler knows
+  // the number of registers on every path)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLeast));
   if (warp == 8) {
     // ---------------- schedule and TMA ----------------------------------
     Walker walk;
@@ -266,13 +278,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mine = {g.parts, g.tok0, g.t.row0, g.t.n_rows, g.head, g.shared, {0, 0}};
       for (int h = 0; h < 2 && ok; ++h) {
         if (g.t.n_rows <= h * half_rows) break;
-        if (q_use[h] > 0) ok = wait_all(&M.q_empty[h], (q_use[h] - 1) & 1, abort_f);
+        const int use = q_use[h], buf = use % kQ;
+        if (use >= kQ) ok = wait_all(&M.q_empty[h][buf], ((use / kQ) & 1) ^ 1, abort_f);
         if (!ok) break;
         if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&M.q_in[h], half_rows * D * 2);
+          ptx::mbar_arrive_expect_tx(&M.q_in[h][buf], half_rows * D * 2);
           for (int x = 0; x < D / 64; ++x)
-            tma_load_rows(smem + La::oQ + h * La::kWide + x * (kHalf * 128), &tm_q, &M.q_in[h],
-                          g.head * P.group, g.tok0 + P.by_group(g.t.row0 + h * half_rows), x);
+            tma_load_rows(smem + La::oQ + (h * kQ + buf) * La::kWide + x * (kHalf * 128), &tm_q,
+                          &M.q_in[h][buf], g.head * P.group,
+                          g.tok0 + P.by_group(g.t.row0 + h * half_rows), x);
         }
         ++q_use[h];
       }
@@ -295,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // gave up: what is on its way into shared memory has to land first
       int none = 0;
       for (int h = 0; h < 2; ++h)
-        if (q_use[h] > 0)
-          ptx::mbar_wait_bounded(&M.q_in[h], (q_use[h] - 1) & 1, &none, kAttnWaitNs / 8);
+        for (int k = q_use[h] > kQ ? q_use[h] - kQ : 0; k < q_use[h]; ++k)
+          ptx::mbar_wait_bounded(&M.q_in[h][k % kQ], (k / kQ) & 1, &none, kAttnWaitNs / 8);
       for (int k = nk > kK ? nk - kK : 0; k < nk; ++k)
         ptx::mbar_wait_bounded(&M.k_full[k % kK], (k / kK) & 1, &none, kAttnWaitNs / 8);
       for (int k = nv > kV ? nv - kV : 0; k < nv; ++k)
@@ -312,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_tiles = desc_lo(ptx::smem_u32(smem + La::oQ), 16);
       const uint32_t k_tiles = desc_lo(ptx::smem_u32(smem), 16);
       const uint32_t w_tiles = desc_lo(ptx::smem_u32(smem + La::oW), 1024);
-      // of each half: the parity of its tiles' P, its segments (modulo 4), whether it has had one
-      uint32_t p_par = 0, segs = 0, begun = 0;
+      // of each half: the parity of its tiles' P, and its segments so far
+      uint32_t p_par = 0;
+      int segs0 = 0, segs1 = 0;
       int n = 0;  // tiles
 #pragma unroll 1
       for (int sg = 0;; ++sg) {
@@ -326,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int h = 0; h < halves; ++h) {
             const uint32_t tm_s = tmem + h * 128, tm_o = tmem + 256 + h * 128;
+            const int use = h == 0 ? segs0 : segs1;
             if (i > 0) {
               const uint32_t va = w_tiles + w_at * (La::kWide / 16);
               if (h == 0) wait_quiet(&M.w_full[w_at], ((n - 1) / kW) & 1, abort_f);
               // the half's previous segment has been read out of O
-              if (i == 1 && ((begun >> h) & 1) != 0)
-                wait_quiet(&M.o_empty[h], ((segs >> 2 * h) & 1) ^ 1, abort_f);
+              if (i == 1 && use > 0) wait_quiet(&M.o_empty[h], (use & 1) ^ 1, abort_f);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 wait_quiet(x ? &M.p_full[h] : &M.p_half[h], (p_par >> h) & 1, abort_f);
@@ -344,9 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               p_par ^= 1u << h;
             }
             if (i < tiles) {
-              const uint32_t qa = q_tiles + h * (La::kWide / 16), ka = k_tiles + k_at * (La::kTile / 16);
-              if (i == 0)
-                wait_quiet(&M.q_full[h][(segs >> 2 * h) & 1], (segs >> (2 * h + 1)) & 1, abort_f);
+              const uint32_t qa = q_tiles + (h * kQ + use % kQ) * (La::kWide / 16), ka = k_tiles + k_at * (La::kTile / 16);
+              if (i == 0) wait_quiet(&M.q_full[h][use % kQTurns], (use / kQTurns) & 1, abort_f);
               if (h == 0) wait_quiet(&M.k_full[k_at], (n / kK) & 1, abort_f);
               ptx::tc_fence_after();
 #pragma unroll
@@ -355,11 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             desc_hi(1024), ka + ks % (D / 32) * 2, desc_hi_span(8 * D, D),
                             kIdescQK, ks > 0 ? 1u : 0u);
               ptx::mma_commit(&M.s_full[h]);
-              if (i == tiles - 1) ptx::mma_commit(&M.q_empty[h]);
+              if (i == tiles - 1) ptx::mma_commit(&M.q_empty[h][use % kQ]);
             } else {
               ptx::mma_commit(&M.o_done[h]);
-              segs = (segs & ~(3u << 2 * h)) | ((segs >> 2 * h) + 1 & 3u) << 2 * h;
-              begun |= 1u << h;
+              if (h == 0) ++segs0; else ++segs1;
             }
           }
           if (i < tiles) ptx::mma_commit(&M.used[n % kUsed]);
@@ -385,11 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Q first, beside the softmax warps' results of the segment before
 #pragma unroll 1
       for (int h = 0; h < 2 && ok && g.t.n_rows > h * half_rows; ++h) {
-        ok = wait_all(&M.q_in[h], q_use[h] & 1, abort_f);
-        split_queries<D>(smem + La::oQ + h * La::kWide, (warp - kFirstWidener) * 32, M.q_scale[q_use[h] & 1][h]);
+        const int use = q_use[h], buf = use % kQ;
+        ok = wait_all(&M.q_in[h][buf], (use / kQ) & 1, abort_f);
+        split_queries<D>(smem + La::oQ + (h * kQ + buf) * La::kWide, (warp - kFirstWidener) * 32,
+                         M.q_scale[h][use % kQTurns]);
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&M.q_full[h][q_use[h] & 1]);
+        if (lane == 0) ptx::mbar_arrive(&M.q_full[h][use % kQTurns]);
         ++q_use[h];
       }
       for (int i = 0; i < g.n && ok; ++i, ++n) {
@@ -411,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&M.seg_empty[sg % kRing]);
     }
-  } else if (warp < 8) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMost));
     // ---------------- softmax and results ---------------------------------
     const int h = warp >> 2, w = warp & 3;
     const int row = w * 32 + lane;  // of the half, and the TMEM lane
@@ -441,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
-      wait_quiet(&M.q_full[h][segs & 1], (segs >> 1) & 1, abort_f);
+      wait_quiet(&M.q_full[h][segs % kQTurns], (segs / kQTurns) & 1, abort_f);
+      const float q_scale = c * scale_of(M.q_scale[h][segs % kQTurns][row]);
       ++segs;
-      const float q_scale = c * scale_of(M.q_scale[(segs - 1) & 1][h][row]);
       const int readers = g.t.n_rows <= half_rows ? 2 : 1;  // the other half's warp too, if it has no rows
       float m = -INFINITY, l = 0.f;  // m: what weights are relative to
       int R = 0;                     // the largest exponent of a value block so far
