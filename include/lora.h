@@ -702,7 +702,7 @@ lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
  * weights as a pair of bf16) a weight enters its product as three e4m3 terms, off by 2^-12 of
  * itself or 2^-23 of the row's largest, whichever is more, and by as much of the product's
  * at the largest v_scale seen; elsewhere as one f16, off by 2^-11 of itself, beside values that are
- * f16, off by at most 2^-33 of the largest scale's.  Scores, maxima, sums and the accumulator
+ * f16, off by at most 2^-16 of the largest v_scale seen.  Scores, maxima, sums and the accumulator
  * are fp32, and the result is rounded once.  So max_q_len, and a prompt in the same batch, change the
  * rounding of a single token's weights.  Scales of blocks that no row sees may hold
  * anything.

@@ -12,15 +12,22 @@
 // e4m3 terms, off by at most 2^-17 of its largest value; two products at twice bf16's rate
 // take its time.  V would need three terms of P, one and a half times that, so it
 // becomes f16 instead: a code is exact there, as is its block's power of two relative to
-// the largest so far, R (to 2^-33 of that), and P keeps 11 bits, where a bf16 has 8.  Four
+// the largest so far, R (but for 448 x 2^-25 of that at most), and P keeps 11 bits, where a bf16 has 8.  Four
 // warps do it, between the loads and the MMAs; values that no row sees they make zeros on
 // the way.  A key block's scale is a factor of its 16 scores beside c.
 //
-// Bound by the tensor cores, as the bf16 kernel (k_attn_prefill.cu), whose schedule of halves,
-// softmax and results this is; a tile's codes are half its bytes.
+// The bf16 kernel's (k_attn_prefill.cu) schedule of halves, softmax and results, and its floor:
+// the tensor cores.  Measured: prompt of 8192, 32 / 8 heads of 128: 427 us (1288 TFLOP/s,
+// 0.67 of the measured burst rate; bf16 cache 347 us); chunks with a window of 1024, 64 / 8
+// heads of 64: 208 us.  The tensor pipe is active for 55% of the cycles, no other pipe for
+// more than 40.  A half's chain bounds it: 2900 cycles from scores to weights and 900 back
+// through the MMAs, a tile, and 7000 an item.  The roles take 55% more instructions
+// a tile than the bf16 kernel's, so what counted most was to keep them short (all 128
+// scores of a row in registers, one long piece of code: 821 us; loops over 64: 467) and the issuing
+// thread's commits few (six a tile 467 us, three 433).
 //
-// Warps: 0-3 softmax of half 0, 4-7 of half 1 (Q in, results out), 8 schedule and TMA,
-// 9 MMA issue, 10 scales, 12-15 Q and V.  Every wait is bounded; on timeout the kernel
+// Warps: 0-3 softmax and results of half 0, 4-7 of half 1, 8 schedule and TMA, 9 MMA issue,
+// 10 scales, 11 idle, 12-15 Q into its terms and V into f16.  Every wait is bounded; on timeout the kernel
 // raises LORA_DEVERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
@@ -474,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ptx::tc_fence_after();
         mask_in_place(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0);
-        // The scores are read twice, 64 at a time: two short loops in place of one long
-        // piece of code (prompt of 8192: 821 us with all 128 in registers).
+        // (the scores are read twice, 64 at a time)
         float mx = -INFINITY;
 #pragma unroll 1
         for (int k = 0; k < kKeys; k += 64) {

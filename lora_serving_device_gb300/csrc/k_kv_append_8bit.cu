@@ -16,6 +16,10 @@
 // rows' cosines and sines wait in shared memory.
 //
 // Bound by memory: every value is read once and written once, k and v in half the bytes.
+// Measured: prompt of 8192, 32 / 8 heads of 128: 39 us, 4.8 TB/s of 6.69 (lookups, then loads
+// that the few warps which 128 registers leave room for do not keep in flight all the time; more
+// warps with fewer registers took longer, 48 us at 96); 5238 tokens of 28 / 4 heads, three
+// axes: 23.4 us, 3.5 TB/s; 64 tokens 4.9 us.
 #include <algorithm>
 
 #include "attn.cuh"
