@@ -698,7 +698,7 @@ lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
  * lora_attn_paged_8bit, lora_attn_prefix_8bit: lora_attn_paged and lora_attn_prefix over
  * it; the same masks, workspaces (lora_attn_workspace_bytes) and errors.  The keys' codes
  * enter their product as they are, and a row of q as two e4m3 terms, off by at most 2^-17 of its
- * largest value.  Where the keys stand in the MMA's M (where lora_attn_paged has the
+ * largest value (q has to be finite).  Where the keys stand in the MMA's M (where lora_attn_paged has the
  * weights as a pair of bf16) a weight enters its product as three e4m3 terms, off by 2^-12 of
  * itself or 2^-23 of the row's largest, whichever is more, and by as much of the product's
  * at the largest v_scale seen; elsewhere as one f16, off by 2^-11 of itself, beside values that are

@@ -779,6 +779,11 @@ def _c_counts(counts):
     return (ctypes.c_int32 * len(counts))(*counts)
 
 
+def _check_ws(ws, device):
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise TypeError("ws: contiguous memory on the call's device")
+
+
 def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream):
     """Checks the arguments of an append; the C call's, from q to the stream, and q_out."""
     n_q = q_stride = q_out_stride = 0
@@ -830,6 +835,7 @@ def kv_append_8bit_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interl
     """kv_append_t into a PagedKV8bit (lora_kv_append_8bit): k and v become e4m3 codes, at one
     scale for each block of tokens and head, which grows as the block's values do."""
     kv.needs(8)
+    _check_ws(ws, kv._device)
     args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
     check(load().lora_kv_append_8bit(kv.ref, *kv.scales, *args), "lora_kv_append_8bit")
     return q_out
@@ -869,6 +875,7 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
 def attn_paged_8bit_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
     """attn_paged_t over a PagedKV8bit (lora_attn_paged_8bit)."""
     kv.needs(8)
+    _check_ws(ws, kv._device)
     rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
     check(load().lora_attn_paged_8bit(kv.ref, *kv.scales, *rows, window, n_sink, *rest), "lora_attn_paged_8bit")
     return out
@@ -887,6 +894,7 @@ def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream
 def attn_prefix_8bit_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
     """attn_prefix_t over a PagedKV8bit (lora_attn_prefix_8bit)."""
     kv.needs(8)
+    _check_ws(ws, kv._device)
     groups = _group_args(kv, group_off, prefix_len)
     rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
     check(load().lora_attn_prefix_8bit(kv.ref, *kv.scales, *groups, *rows, *rest), "lora_attn_prefix_8bit")
@@ -942,6 +950,7 @@ def batch_plan_t(block_table, n_cached, n_new, free_pages, n_free, page_size, n_
         elif t.dtype is not kind or t.get_device() != dev or not t.is_contiguous() or (n != t.numel() and n is not None):
             raise TypeError(f"{_PLAN_ARRAYS[i]}: contiguous {kind}{'' if n is None else f' [{n}]'} on the block "
                             "table's device")
+    _check_ws(ws, dev)
     if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
         raise ValueError("block_table: [n_seqs, max_pages]")
     if dev < 0 or torch._C._cuda_getDevice() != dev:

@@ -199,3 +199,54 @@ def test_append_of_a_long_prompt_past_the_first_blocks(L):
         step = torch.exp2(cache[i + 2][table[0].long()].repeat_interleave(16, -1).transpose(1, 2)
                           .reshape(-1, hkv)[:n].double() - 137)[..., None]
         assert ((x.double() - y).abs() <= 2.0 ** -4 * x.double().abs() + step).all()
+
+
+def test_two_streams_at_once(L):
+    """Calls over one cache on two streams with workspaces of their own: the bits of the calls alone."""
+    import torch
+    torch.manual_seed(0)
+    hq, hkv, d, page, n = 8, 2, 128, 16, 30
+    codes, scales = random_cache_t(torch, n * 80, hkv, page, d)
+    table = torch.randperm(n * 80, device="cuda").int().view(n, 80)
+    jobs = []
+    for q_lens in ([1] * n, [40 + i for i in range(n)]):
+        off = torch.tensor([0] + q_lens, device="cuda").cumsum(0).int()
+        lens = torch.randint(200, 80 * page, (n,), device="cuda", dtype=torch.int32)
+        kv = L.PagedKV8bit(*codes, *scales, table, off, lens, sum(q_lens), max_q_len=max(q_lens))
+        q = torch.randn(kv.T, hq, d, device="cuda").bfloat16()
+        ws = L.attn_workspace(kv, hq)
+        want = L.attn_paged_8bit_t(kv, q, ws)
+        jobs.append((kv, q, L.attn_workspace(kv, hq), want, torch.empty_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for kv, q, ws, want, out, st in jobs:
+            L.attn_paged_8bit_t(kv, q, ws, out=out, stream=st)
+    torch.cuda.synchronize()
+    for kv, q, ws, want, out, st in jobs:
+        assert torch.equal(out, want) and L.get_error_t(ws) == 0
+
+
+def random_cache_t(torch, n_pages, hkv, page, d):
+    codes = [torch.randint(0, 127, (n_pages, hkv, page, d), dtype=torch.uint8, device="cuda") ^
+             torch.randint(0, 2, (n_pages, hkv, page, d), dtype=torch.uint8, device="cuda") * 128 for _ in range(2)]
+    scales = [torch.randint(116, 120, (n_pages, hkv, page // min(16, page)), dtype=torch.uint8, device="cuda")
+              for _ in range(2)]
+    return codes, scales
+
+
+def test_workspaces_elsewhere_are_refused(L):
+    """A workspace in host memory, or not contiguous, reaches no kernel."""
+    import torch
+    hq, hkv, d, page = 4, 2, 64, 16
+    cache = L.PagedKV8bit.empty_cache(2, hkv, page, d)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, off, lens = i32([[0, 1]]), i32([0, 1]), i32([1])
+    kv = L.PagedKV8bit(*cache, table, off, lens, 1)
+    q, k = (torch.zeros(1, h, d, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv))
+    bad = [torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 21, dtype=torch.uint8, device="cuda")[::2]]
+    for ws in bad:
+        for call in (lambda: L.kv_append_8bit_t(kv, q, k, k, None, ws), lambda: L.attn_paged_8bit_t(kv, q, ws),
+                     lambda: L.attn_prefix_8bit_t(kv, q, i32([0, 1]), i32([0]), ws),
+                     lambda: L.batch_plan_t(table, lens, i32([0]), i32([0]), i32([1]), page, 2, ws, T=1)):
+            with pytest.raises(TypeError, match="ws"):
+                call()
