@@ -161,7 +161,7 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     // Splitting an item costs each of its CTAs a part, so short ones stay whole:
     // up to 8 tiles of single tokens (the tokens after a prefix of 8K: 56.5 us,
     // split 59.8), two of prompts.
-    P.over = !w.shape[phase].prefill ? 1 : bits8 ? 5 : 3;
+    P.over = !w.shape[phase].prefill ? 1 : bits8 ? 4 : 3;
     P.whole = w.shape[phase].prefill ? 2 : 8;
     // By the fewest items that this many rows can make: with 38 and more one has
     // a few parts, which the last CTA to arrive adds up; fewer items have many

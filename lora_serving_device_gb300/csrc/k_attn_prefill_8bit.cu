@@ -125,50 +125,60 @@ __device__ __forceinline__ void widen_values(const uint8_t* V, uint8_t* W, const
   }
 }
 
-// The largest magnitude of kLanes lanes' eight values.
-template <int kLanes>
-__device__ __forceinline__ float row_top(const uint4& x) {
+// 32 rows of Q in shared memory, from `row0` on, from bf16 as TMA lays them ([64 values of a
+// head][rows][64 values], 128-byte swizzle) to two e4m3 terms in the same place, each 128
+// bytes a row (a plane each, or the halves of a row with D = 64), divided by powers of two,
+// whose bytes go to `bytes`.  One warp, four lanes to a row: eight rows at once, with a quarter of
+// a row's values in a lane, have enough under way that its latencies overlap (16 lanes to a row:
+// 5700 cycles, which an item's first scores wait for).
+template <int D>
+__device__ __forceinline__ void split_queries(uint8_t* Q, int row0, uint8_t* bytes) {
+  constexpr int kChunks = D / 32;  // of eight values, of a lane
+  constexpr uint32_t kPlane = kHalf * 128;
+  const int lane = threadIdx.x & 31, i = lane & 3;
   const uint32_t m = 0x7fff7fffu;
   auto most = [](uint32_t a, uint32_t b) {
     uint32_t y;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
   };
-  uint32_t y = most(most(x.x & m, x.y & m), most(x.z & m, x.w & m));
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) y = most(y, __shfl_xor_sync(0xffffffffu, y, o));
-  return fmaxf(bf16_lo(y), bf16_hi(y));
-}
-
-// 32 rows of Q in shared memory, from `row0` on, from bf16 as TMA lays them ([64 values of a
-// head][rows][64 values], 128-byte swizzle) to two e4m3 terms in the same place, each 128
-// bytes a row (a plane each, or the halves of a row with D = 64), divided by powers of two,
-// whose bytes go to `bytes`.  One warp, D / 8 lanes to a row.
-template <int D>
-__device__ __forceinline__ void split_queries(uint8_t* Q, int row0, uint8_t* bytes) {
-  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-  constexpr uint32_t kPlane = kHalf * 128;
-  const int lane = threadIdx.x & 31, i = lane % kLanes;
-#pragma unroll 4
-  for (int k = 0; k < 32; k += kAtOnce) {
-    const int row = row0 + k + lane / kLanes;
+#pragma unroll 1
+  for (int k = 0; k < 32; k += 8) {
+    const int row = row0 + k + lane / 4, r = row & 7;
     uint8_t* at = Q + row * 128;
-    const uint4 x = *reinterpret_cast<const uint4*>(at + (i / 8) * kPlane + (((i % 8) ^ (row & 7)) << 4));
-    const int byte = min(scale_byte(row_top<kLanes>(x)), 253);
-    const float inv = scale_of(254 - byte);
-    float y[8];
-    load8(reinterpret_cast<const bf16*>(&x), y);
-    uint32_t t1[2], t2[2];
+    uint4 x[kChunks];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      split4_e4m3(pack_f16x2(y[4 * e] * inv, y[4 * e + 1] * inv),
-                  pack_f16x2(y[4 * e + 2] * inv, y[4 * e + 3] * inv), t1[e], t2[e]);
+    for (int c = 0; c < kChunks; ++c) {
+      const int chunk = i * kChunks + c;
+      x[c] = *reinterpret_cast<const uint4*>(at + (chunk / 8) * kPlane + (((chunk & 7) ^ r) << 4));
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      top = most(top, most(most(x[c].x & m, x[c].y & m), most(x[c].z & m, x[c].w & m)));
+    top = most(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = most(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int byte = min(scale_byte(fmaxf(bf16_lo(top), bf16_hi(top))), 253);
+    const float inv = scale_of(254 - byte);
     __syncwarp();  // (the rows have been read)
-    const int c = i / 2, c2 = D == 128 ? c : 4 + c;
-    at += (i & 1) * 8;
-    *reinterpret_cast<uint2*>(at + ((c ^ (row & 7)) << 4)) = make_uint2(t1[0], t1[1]);
-    *reinterpret_cast<uint2*>(at + (D == 128 ? kPlane : 0) + ((c2 ^ (row & 7)) << 4)) =
-        make_uint2(t2[0], t2[1]);
+    const int c0 = i * (kChunks / 2);  // the first 16 codes of a term
+#pragma unroll
+    for (int c = 0; c < kChunks; c += 2) {
+      uint32_t t1[4], t2[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y[8];
+        load8(reinterpret_cast<const bf16*>(&x[c + e]), y);
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          split4_e4m3(pack_f16x2(y[4 * z] * inv, y[4 * z + 1] * inv),
+                      pack_f16x2(y[4 * z + 2] * inv, y[4 * z + 3] * inv), t1[2 * e + z], t2[2 * e + z]);
+      }
+      const int to = c0 + c / 2;
+      *reinterpret_cast<uint4*>(at + ((to ^ r) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+      *reinterpret_cast<uint4*>(at + (D == 128 ? kPlane : 0) + (((D == 128 ? to : 4 + to) ^ r) << 4)) =
+          make_uint4(t2[0], t2[1], t2[2], t2[3]);
+    }
     if (i == 0) bytes[row] = static_cast<uint8_t>(byte);
   }
 }
@@ -481,26 +491,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ptx::tc_fence_after();
         mask_in_place(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0);
-        // (the scores are read twice, 64 at a time)
+        // (the scores are read twice, 64 at a time: here for the largest of each block)
         float mx = -INFINITY;
 #pragma unroll 1
         for (int k = 0; k < kKeys; k += 64) {
-          float s[64];
-          ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s));
-          ptx::tmem_ld32(tm_s + k + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          float s[64 / kBlock][kBlock], top_s[64 / kBlock];
+#pragma unroll
+          for (int b = 0; b < 64 / kBlock; ++b) ptx::tmem_ld_top(tm_s + k + b * kBlock, s[b], top_s[b]);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int b = 0; b < 64 / kBlock; ++b) {
-            const float* x = s + b * kBlock;
-            float y = max3(x[0], x[1], x[2]), z = max3(x[3], x[4], x[5]);
-#pragma unroll
-            for (int j = 6; j + 3 < kBlock; j += 4) {
-              y = max3(y, x[j], x[j + 1]);
-              z = max3(z, x[j + 2], x[j + 3]);
-            }
-            y = max3(y, x[kBlock - 2], x[kBlock - 1]);
-            mx = fmaxf(mx, fmaxf(y, z) * scale_with(key_scale[k / kBlock + b], q_scale));
-          }
+          for (int b = 0; b < 64 / kBlock; ++b)
+            mx = fmaxf(mx, top_s[b] * scale_with(key_scale[k / kBlock + b], q_scale));
         }
         // (rows that are not in use hold anything: they have no say)
         if (top > R || __any_sync(0xffffffffu, mine && mx > m + kMost)) {
