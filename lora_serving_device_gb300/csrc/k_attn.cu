@@ -156,12 +156,12 @@ cudaError_t launch_attn(const lora_paged_kv_t& kv, const AttnArgs& a, cudaStream
     P.by_rows = FastDiv::of(P.rows);
     // Beside its key tiles an item costs its first scores and its results: in the
     // prefill kernel as much as three tiles (prompt of 8192: 346 us; 2, 4 and 5
-    // units 352, 349 and 355), in its 8-bit form five (432 us; 3, 4 and 6 units 527, 451 and
-    // 436: there Q is split between two items), in the other, where a second warpgroup is at work, one.
+    // units 352, 349 and 355; its 8-bit form 396, with 4 and 5 units 399 and 405), in the
+    // other, where a second warpgroup is at work, one.
     // Splitting an item costs each of its CTAs a part, so short ones stay whole:
     // up to 8 tiles of single tokens (the tokens after a prefix of 8K: 56.5 us,
     // split 59.8), two of prompts.
-    P.over = !w.shape[phase].prefill ? 1 : bits8 ? 4 : 3;
+    P.over = w.shape[phase].prefill ? 3 : 1;
     P.whole = w.shape[phase].prefill ? 2 : 8;
     // By the fewest items that this many rows can make: with 38 and more one has
     // a few parts, which the last CTA to arrive adds up; fewer items have many
