@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.base + tok;
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
+      const int min_hi = __reduce_min_sync(0xffffffffu, hi), max_lo = __reduce_max_sync(0xffffffffu, lo);
       wait_quiet(&M.q_full[h][segs % kQTurns], (segs / kQTurns) & 1, abort_f);
       const float q_scale = c * scale_of(M.q_scale[h][segs % kQTurns][row]);
       ++segs;
@@ -490,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_quiet(&M.s_full[h], tile & 1, abort_f);
         __syncwarp();
         ptx::tc_fence_after();
-        mask_in_place(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0);
+        if (key0 + kKeys - 1 > min_hi || key0 < max_lo)
+          mask_in_place(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0);
         // (the scores are read twice: here for the largest of each block, all at once or, with 64
         // values a head, 64 keys at a time: 400 us against 405, and 200 against 202)
         constexpr int kTops = D == 128 && kBlock == 16 ? kKeys : 64;
@@ -500,10 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s[kTops / kBlock][kBlock], top_s[kTops / kBlock];
 #pragma unroll
           for (int b = 0; b < kTops / kBlock; ++b) ptx::tmem_ld_top(tm_s + k + b * kBlock, s[b], top_s[b]);
+          float kc[kTops / kBlock];  // (read beside the scores)
+#pragma unroll
+          for (int b = 0; b < kTops / kBlock; ++b) kc[b] = scale_with(key_scale[k / kBlock + b], q_scale);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int b = 0; b < kTops / kBlock; ++b)
-            mx = fmaxf(mx, top_s[b] * scale_with(key_scale[k / kBlock + b], q_scale));
+          for (int b = 0; b < kTops / kBlock; ++b) mx = fmaxf(mx, top_s[b] * kc[b]);
         }
         // (rows that are not in use hold anything: they have no say)
         if (top > R || __any_sync(0xffffffffu, mine && mx > m + kMost)) {
@@ -526,12 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s[64];
           ptx::tmem_ld32(tm_s + k, *reinterpret_cast<uint32_t(*)[32]>(s));
           ptx::tmem_ld32(tm_s + k + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          float key_c[64 / kBlock];
+#pragma unroll
+          for (int b = 0; b < 64 / kBlock; ++b) key_c[b] = scale_with(key_scale[k / kBlock + b], q_scale);
           ptx::tmem_ld_wait();
           uint32_t p[32];
 #pragma unroll
           for (int b = 0; b < 64 / kBlock; ++b) {
-            const float kc = scale_with(key_scale[k / kBlock + b], q_scale);
-            const uint64_t kc2 = pack2(kc, kc);
+            const uint64_t kc2 = pack2(key_c[b], key_c[b]);
 #pragma unroll
             for (int x = b * kBlock; x < (b + 1) * kBlock; x += 2) {
               float e0, e1;
