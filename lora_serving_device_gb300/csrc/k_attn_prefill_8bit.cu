@@ -17,14 +17,15 @@
 // the way.  A key block's scale is a factor of its 16 scores beside c.
 //
 // The bf16 kernel's (k_attn_prefill.cu) schedule of halves, softmax and results, and its floor:
-// the tensor cores.  Measured: prompt of 8192, 32 / 8 heads of 128: 427 us (1288 TFLOP/s,
-// 0.67 of the measured burst rate; bf16 cache 347 us); chunks with a window of 1024, 64 / 8
-// heads of 64: 208 us.  The tensor pipe is active for 55% of the cycles, no other pipe for
-// more than 40.  A half's chain bounds it: 2900 cycles from scores to weights and 900 back
-// through the MMAs, a tile, and 7000 an item.  The roles take 55% more instructions
-// a tile than the bf16 kernel's, so what counted most was to keep them short (all 128
-// scores of a row in registers, one long piece of code: 821 us; loops over 64: 467) and the issuing
-// thread's commits few (six a tile 467 us, three 433).
+// the tensor cores.  Measured: prompt of 8192, 32 / 8 heads of 128: 393 to 407 us (1400 TFLOP/s,
+// 0.73 of the measured burst rate; bf16 cache 347 us); chunks with a window of 1024, 64 / 8
+// heads of 64: 197 us.  The tensor pipe is active for 60% of the cycles, no other pipe for
+// more than 35.  A half's chain bounds it, 2400 cycles from scores to weights and 500 back
+// through the MMAs, a tile, beside the issuing thread, which is never idle.  The roles
+// take more instructions a tile than the bf16 kernel's, so what counted most was to keep them short
+// (all 128 scores of a row in registers, one long piece of code: 821 us; loops over 64: 467), the issuing
+// thread's commits few (six a tile 467 us, three 433), and Q's split short (429, now 419: an
+// item's first scores wait for it).
 //
 // Warps: 0-3 softmax and results of half 0, 4-7 of half 1, 8 schedule and TMA, 9 MMA issue,
 // 10 scales, 11 idle, 12-15 Q into its terms and V into f16.  Every wait is bounded; on timeout the kernel
