@@ -241,12 +241,17 @@ struct TileLoader {
     }
     return (id * P.kv.n_kv_heads + g.head) * (page / 8) + (first_key(g, i0) & (page - 1)) / 8;
   }
-  __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
+  // The segment's first page ids, on their way: place(P, g, 0, id, seen) has to become `now`.
+  __device__ __forceinline__ int ask(const AttnParams& P, const Segment& g, bool& seen) {
     policy = l2_policy(g.once != 0);
-    bool seen;
     const int id = fetch(P, g, 0, seen);
     next_seen = false;
     if (g.n > per) next = fetch(P, g, per, next_seen);
+    return id;
+  }
+  __device__ __forceinline__ void begin(const AttnParams& P, const Segment& g) {
+    bool seen;
+    const int id = ask(P, g, seen);
     now = place(P, g, 0, id, seen);
   }
   // The place of this lane's box of tile i (lanes below `boxes`).

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
     for (int sg = 0; ok; ++sg) {
       Segment g = walk.next(P);
       g.batch0 = batches;
-      batches += (g.n + P.scale_tiles - 1) / P.scale_tiles;
+      batches += (g.n + P.scale_tiles - 1) >> (P.scale_tiles == 2 ? 1 : 2);
       if (sg >= kRing)
         ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
       if (!ok) break;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int sg = 0; ok; ++sg) {
       Segment g = walk.next(P);
       g.batch0 = batches;
-      batches += (g.n + P.scale_tiles - 1) / P.scale_tiles;
+      batches += (g.n + P.scale_tiles - 1) >> (P.scale_tiles == 2 ? 1 : 2);
       if (sg >= kRing)
         ok = wait_all(&M.seg_empty[sg % kRing], ((sg / kRing) & 1) ^ 1, abort_f);
       if (!ok) break;
@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (g.n == 0) break;
-      load.begin(P, g);
+      bool seen;
+      const int id = load.ask(P, g, seen);
       if (P.join_after && g.parts > 1 && g.cta0 == blockIdx.x)
         mine = {g.parts, g.tok0, g.t.row0, g.t.n_rows, g.head, g.shared, {0, 0}};
       for (int h = 0; h < 2 && ok; ++h) {
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++q_use[h];
       }
       __syncwarp();
+      load.now = load.place(P, g, 0, id, seen);  // (asked for before Q, looked at after)
       for (int i = 0; i < g.n && ok; ++i) {
         const int at = load.at(P, g, i);
         const uint32_t bytes = load.bytes(at);
