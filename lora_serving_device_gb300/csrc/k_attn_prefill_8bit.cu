@@ -19,7 +19,7 @@
 // The bf16 kernel's (k_attn_prefill.cu) schedule of halves, softmax and results, and its floor:
 // the tensor cores.  Measured: prompt of 8192, 32 / 8 heads of 128: 393 to 407 us (1400 TFLOP/s,
 // 0.73 of the measured burst rate; bf16 cache 347 us); chunks with a window of 1024, 64 / 8
-// heads of 64: 197 us.  The tensor pipe is active for 60% of the cycles, no other pipe for
+// heads of 64: 193 us.  The tensor pipe is active for 60% of the cycles, no other pipe for
 // more than 35.  A half's chain bounds it, 2400 cycles from scores to weights and 500 back
 // through the MMAs, a tile, beside the issuing thread, which is never idle.  The roles
 // take more instructions a tile than the bf16 kernel's, so what counted most was to keep them short
@@ -496,9 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         if (key0 + kKeys - 1 > min_hi || key0 < max_lo)
           mask_in_place(tm_s, key0, hi, lo, min(g.t.n_sink, hi + 1) - v0);
-        // (the scores are read twice: here for the largest of each block, all at once or, with 64
-        // values a head, 64 keys at a time: 400 us against 405, and 200 against 202)
-        constexpr int kTops = D == 128 && kBlock == 16 ? kKeys : 64;
+        // (the scores are read twice: here for the largest of each block, all at once: prompt of
+        // 8192 400 us, 64 keys at a time 405; with a window 193 and 196; blocks of 8 keys
+        // have twice the maxima, more than the registers hold, and keep to 64 keys)
+        constexpr int kTops = kBlock == 16 ? kKeys : 64;
         float mx = -INFINITY;
 #pragma unroll 1
         for (int k = 0; k < kKeys; k += kTops) {
