@@ -63,6 +63,12 @@ struct Lay {
   static constexpr uint32_t kPAll = kPBufs * kP > kStaging ? kPBufs * kP : kStaging;
   static constexpr int kSBufs = 2;
   static constexpr int kStages = 196608u / kStage;
+  // A warpgroup waits for the scales of its own segments only, by one bit of a barrier's phase: when it
+  // comes for a segment's first batch, the one before it in the ring's place has to be there.  The
+  // header that it comes by follows the last key tile of the other's segment, so kStages tiles of that may
+  // be without scales: their batches, of two tiles at least but for the last, have to be fewer than the ring's.
+  static constexpr int kScaleBatches = D == 128 ? 4 : 8;
+  static_assert(1 + (kStages - 1) / 2 < kScaleBatches, "a batch of scales two phases behind");
   static constexpr uint32_t oQ = kStages * kStage;
   static constexpr uint32_t oP = oQ + W * kQ;
   static constexpr uint32_t oMisc = oP + W * kPAll;
@@ -79,7 +85,7 @@ struct Misc {
   float4 red_max[W][A], red_sum[W][A];
   float m[W][A];
   float q_scale[W][La::N];
-  ScaleRing<4> scales;
+  ScaleRing<La::kScaleBatches> scales;
   int row_hi[W][A], row_lo[W][A];
   uint64_t full_k[kStages], full_v[kStages], empty[kStages];
   uint64_t s_full[W][La::kSBufs], s_empty[W][La::kSBufs];

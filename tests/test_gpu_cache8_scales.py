@@ -1,0 +1,109 @@
+"""Scales of the 8-bit cache on the GPU: long segments in pages of 8, blocks of very different size,
+and how far results may be off, part by part.
+
+Tolerances (tight: one bf16 a weight would not keep them).  With the cache's values as given, w the
+weights before their sum, w_max a row's largest and 2^R the largest scale of a block of values
+that some row of the call sees:
+  result     one rounding to bf16: U |ref|
+  weights    three e4m3 terms (keys in M): the first leaves 2^-4 of a value, the others 2^-4 of what is left,
+             so 2^-12 w_j, or where the last is subnormal half its step, 2^-10 / 16^2 = 2^-18 of P 2^(vb - R), whose
+             largest P is at least 2^5: 2^-23 w_max 2^(R - vb);
+             one f16 (rows in M): 2^-11 w_j, or below 2^-14 half of 2^-24, where the largest is at least
+             2^6: 2^-31 w_max
+  values     e4m3 codes (keys in M) exactly; f16 (rows in M) of code x 2^(vb - R): lost where vb - R < -24, half
+             of 2^-24 where that is below -15, else exactly
+  scores     q as two terms is off by 2^-17 of the row's largest, the fp32 sums by as much: a weight by
+             scale 2^-17 max|q| max_j |k_j|_1 twice, against numerator and sum: four times that
+  the rest   exponentials and fp32 sums: 2^-20 of the weights
+"""
+import numpy as np
+import pytest
+
+from tests.test_gpu_cache8 import dequantize_t, random_cache
+from tests.test_gpu_attn import U, L  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def check_tight(torch, got, q, k, v, vb, top, first_pos, few, window=0, n_sink=0, scale=None):
+    """Rows got, q [rows, hq, d] at positions first_pos .. over keys k, v [n, hq, d] (fp64), vb [n, hq] the
+    exponents of the values' blocks, top the largest that is seen."""
+    rows, n, d = q.shape[0], k.shape[0], q.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    x = torch.einsum("thd,nhd->htn", q.double(), k) * scale
+    pos = torch.arange(first_pos, first_pos + rows, device="cuda")[:, None]
+    key = torch.arange(n, device="cuda")
+    seen = key <= pos
+    if window:
+        seen &= (key > pos - window) | (key < n_sink)
+    w = x.masked_fill(~seen, -float("inf")).softmax(-1)
+    w_max = w.amax(-1, keepdim=True) * seen
+    size, down = v.abs(), (top - vb).double()
+    if few:
+        err = torch.maximum(2.0 ** -12 * w, 2.0 ** -23 * w_max * torch.exp2(down.clamp(max=900)).t()[:, None])
+        err = torch.einsum("htn,nhd->thd", torch.minimum(err, w + 2.0 ** -12 * w), size)
+    else:
+        rounding = torch.where(down > 24, size.amax(-1), torch.where(down > 15, 2.0 ** -25 * 2.0 ** top, 0.0))
+        err = torch.einsum("htn,nhd->thd", 2.0 ** -11 * w + 2.0 ** -31 * w_max, size) + \
+            torch.einsum("htn,nh->th", w, rounding)[..., None]
+    ref, wv = (torch.einsum("htn,nhd->thd", w, y) for y in (v, size))
+    score = scale * 2.0 ** -17 * q.abs().max().double() * k.abs().sum(-1).max()
+    bound = U * ref.abs() + (1 + U) * (err + (4 * score + 2.0 ** -20) * wv)
+    worst = ((got.double() - ref).abs() / (bound + 1e-300)).max()
+    assert torch.isfinite(got).all() and worst <= 1, float(worst)
+
+
+def sequence(torch, cache, row, n, group):
+    """k, v [n, hq, d] and the values' exponents [n, hq] of the pages in `row`."""
+    ids = row.long()
+    hkv, d, page = cache[0].shape[1], cache[0].shape[3], cache[0].shape[2]
+    k, v = (dequantize_t(torch, cache[i][ids], cache[i + 2][ids]).transpose(1, 2).reshape(-1, hkv, d)[:n]
+            .repeat_interleave(group, 1) for i in (0, 1))
+    vb = (cache[3][ids].int().clamp(1, 253) - 127).repeat_interleave(min(16, page), -1).transpose(1, 2)
+    return k, v, vb.reshape(-1, hkv)[:n].repeat_interleave(group, 1)
+
+
+def batch(L, torch, cache, q_lens, kv_len, hq, seed=0, size=0.05, window=0, n_sink=0, repeats=2):
+    """A batch over the cache: every sequence against check_tight, and equal bits from equal calls."""
+    n_pages, hkv, page, d = cache[0].shape
+    n, group = len(q_lens), hq // hkv
+    pages = n_pages // n
+    torch.manual_seed(seed)
+    table = torch.randperm(n_pages, device="cuda")[:n * pages].to(torch.int32).view(n, pages)
+    off = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    T = int(off[-1])
+    q = (size * torch.randn(T, hq, d, device="cuda")).to(torch.bfloat16)
+    kv = L.PagedKV8bit(*cache, table, torch.from_numpy(off).cuda(),
+                       torch.from_numpy(np.asarray(kv_len, np.int32)).cuda(), T, max_q_len=int(max(q_lens)))
+    ws = L.attn_workspace(kv, hq)
+    got = L.attn_paged_8bit_t(kv, q, ws, window=window, n_sink=n_sink)
+    assert L.get_error_t(ws) == 0
+    few = max(q_lens) * group <= 16 or group > 128
+    for s in range(n):
+        m, a, b = int(kv_len[s]), int(off[s]), int(off[s + 1])
+        if a == b:
+            continue
+        k, v, vb = sequence(torch, cache, table[s], m, group)
+        check_tight(torch, got[a:b], q[a:b], k, v, vb, int(vb.max()), m - (b - a), few, window, n_sink)
+    for _ in range(repeats):
+        assert torch.equal(L.attn_paged_8bit_t(kv, q, ws, window=window, n_sink=n_sink).view(torch.int16),
+                           got.view(torch.int16))
+    assert L.get_error_t(ws) == 0
+    return got
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 64), (8, 8, 64), (64, 8, 64), (16, 1, 64), (32, 8, 128), (32, 2, 128)])
+@pytest.mark.parametrize("page", [8, 16])
+def test_long_segments_of_single_tokens(L, hq, hkv, d, page):
+    """Shares of several segments of many key tiles: in pages of 8 a batch of scales is two tiles, and a
+    warpgroup comes for its own while the other's of up to twelve tiles may be on their way."""
+    import torch
+    rng = np.random.default_rng(hq + page)
+    n = 60
+    kv_len = rng.integers(1000, 4000, n)
+    torch.manual_seed(hq)
+    cache = random_cache(torch, n * -(-4000 // page), hkv, page, d)
+    # exponents all over, so that another block's would show
+    for c in cache[2:]:
+        c.copy_(torch.randint(112, 123, c.shape, device="cuda", dtype=torch.uint8))
+    batch(L, torch, cache, [1] * n, kv_len, hq, seed=hq, repeats=30)
