@@ -698,6 +698,7 @@ class PagedKV:
         self.ref = ctypes.addressof(self.struct)
         self._device = k_cache.get_device()
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self._scale = head_dim ** -0.5
         self.new_like = torch.empty_like
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self._current_device = torch._C._cuda_getDevice
@@ -786,23 +787,25 @@ def _check_ws(ws, device):
 
 def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream):
     """Checks the arguments of an append; the C call's, from q to the stream, and q_out."""
-    n_q = q_stride = q_out_stride = 0
+    from_q = to_q = table = at = pairs = None
+    n_q = q_stride = q_out_stride = n_pos = rot = 0
     if q is not None:
         n_q = q.shape[1]
         q_stride = kv.rows(q, n_q, "q")
         if q_out is None:
-            q_out = _on(stream, kv.new_like, q)
+            q_out = kv.new_like(q) if stream is None else _on(stream, kv.new_like, q)
             q_out_stride = n_q * kv.head_dim
         else:
             q_out_stride = kv.rows(q_out, n_q, "q_out")
-    n_pos = rot = 0
+        from_q, to_q = q.data_ptr(), q_out.data_ptr()
     if cos_sin is not None:
         n_pos, rot = cos_sin.shape
+        table = cos_sin.data_ptr()
         if cos_sin.dtype is not kv._f32 or not cos_sin.is_contiguous() or cos_sin.get_device() != kv._device:
             raise TypeError("cos_sin: contiguous fp32 [n_pos, rot_dim] on the cache's device")
-    n_axes, pairs = 1, None
+    n_axes = 1
     if pos is not None:
-        shape = pos.shape
+        shape, at = pos.shape, pos.data_ptr()
         n_axes = shape[0] if len(shape) == 2 else 1
         if shape[-1] != kv.T or pos.dtype is not kv._i32 or not pos.is_contiguous() or \
                 pos.get_device() != kv._device:
@@ -812,9 +815,9 @@ def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, 
             raise ValueError(f"axis_pairs: {len(axis_pairs)} counts for {n_axes} axes")
         pairs = _c_counts(tuple(axis_pairs))
     hk = kv.n_kv_heads
-    return (_ptr(q), q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(), kv.rows(v, hk, "v"), n_q,
-            _ptr(cos_sin), n_pos, rot, _ptr(pos), n_axes, pairs, 1 if interleaved else 0, _ptr(q_out), q_out_stride,
-            ws.data_ptr(), ws.numel(), kv.stream(stream)), q_out
+    return (from_q, q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(), kv.rows(v, hk, "v"), n_q, table, n_pos,
+            rot, at, n_axes, pairs, 1 if interleaved else 0, to_q, q_out_stride, ws.data_ptr(), ws.numel(),
+            kv.stream(stream)), q_out
 
 
 def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
@@ -824,9 +827,12 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
     allowed).  q None: keys and values only.  cos_sin [n_pos, rot_dim] fp32 (rope_table) or
     None for no rotation.  pos: None (the position in the cache), [T], or [n_axes, T] with
     axis_pairs, the rotated pairs of each axis."""
-    kv.needs(16)
+    if kv.bits != 16:
+        kv.needs(16)
     args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
-    check(load().lora_kv_append(kv.ref, *args), "lora_kv_append")
+    status = (_lib or load()).lora_kv_append(kv.ref, *args)
+    if status:
+        check(status, "lora_kv_append")
     return q_out
 
 
@@ -834,25 +840,25 @@ def kv_append_8bit_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interl
                      stream=None):
     """kv_append_t into a PagedKV8bit (lora_kv_append_8bit): k and v become e4m3 codes, at one
     scale for each block of tokens and head, which grows as the block's values do."""
-    kv.needs(8)
+    if kv.bits != 8:
+        kv.needs(8)
     _check_ws(ws, kv._device)
     args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
-    check(load().lora_kv_append_8bit(kv.ref, *kv.scales, *args), "lora_kv_append_8bit")
+    status = (_lib or load()).lora_kv_append_8bit(kv.ref, *kv.scales, *args)
+    if status:
+        check(status, "lora_kv_append_8bit")
     return q_out
 
 
-def _attn_args(kv, q, ws, scale, out, stream):
-    """Checks the rows of an attention call; the C call's arguments from q to the scale, those
-    from out to the stream, and out."""
+# (a call of a few rows takes as long on the host as on the GPU, so the helpers below and above run
+# through few functions)
+def _attn_rows(kv, q, out, stream):
+    """Checks the rows of an attention call: query heads, distance of q's tokens, out and its."""
     n_q = q.shape[1]
     q_stride = kv.rows(q, n_q, "q")
     if out is None:
-        out = _on(stream, kv.new_like, q)
-        out_stride = n_q * kv.head_dim
-    else:
-        out_stride = kv.rows(out, n_q, "out")
-    return ((q.data_ptr(), q_stride, n_q, kv.head_dim ** -0.5 if scale is None else scale),
-            (out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(), kv.stream(stream)), out)
+        return n_q, q_stride, kv.new_like(q) if stream is None else _on(stream, kv.new_like, q), n_q * kv.head_dim
+    return n_q, q_stride, out, kv.rows(out, n_q, "out")
 
 
 def _group_args(kv, group_off, prefix_len):
@@ -866,38 +872,58 @@ def _group_args(kv, group_off, prefix_len):
 def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
     """Causal attention of q [T, n_q_heads, D] over kv's cache (lora_attn_paged); scale
     defaults to D^-0.5, window 0 is none."""
-    kv.needs(16)
-    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
-    check(load().lora_attn_paged(kv.ref, *rows, window, n_sink, *rest), "lora_attn_paged")
+    if kv.bits != 16:
+        kv.needs(16)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
+    status = (_lib or load()).lora_attn_paged(kv.ref, q.data_ptr(), q_stride, n_q,
+        kv._scale if scale is None else scale, window, n_sink, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
+        kv.stream(stream))
+    if status:
+        check(status, "lora_attn_paged")
     return out
 
 
 def attn_paged_8bit_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=None):
     """attn_paged_t over a PagedKV8bit (lora_attn_paged_8bit)."""
-    kv.needs(8)
+    if kv.bits != 8:
+        kv.needs(8)
     _check_ws(ws, kv._device)
-    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
-    check(load().lora_attn_paged_8bit(kv.ref, *kv.scales, *rows, window, n_sink, *rest), "lora_attn_paged_8bit")
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
+    status = (_lib or load()).lora_attn_paged_8bit(kv.ref, *kv.scales, q.data_ptr(), q_stride, n_q,
+        kv._scale if scale is None else scale, window, n_sink, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
+        kv.stream(stream))
+    if status:
+        check(status, "lora_attn_paged_8bit")
     return out
 
 
 def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
     """attn_paged_t for groups of sequences that share a prefix (lora_attn_prefix):
     group_off [n_groups + 1], prefix_len [n_groups] int32 on the device."""
-    kv.needs(16)
-    groups = _group_args(kv, group_off, prefix_len)
-    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
-    check(load().lora_attn_prefix(kv.ref, *groups, *rows, *rest), "lora_attn_prefix")
+    if kv.bits != 16:
+        kv.needs(16)
+    off, lens, n_groups = _group_args(kv, group_off, prefix_len)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
+    status = (_lib or load()).lora_attn_prefix(kv.ref, off, lens, n_groups, q.data_ptr(), q_stride, n_q,
+        kv._scale if scale is None else scale, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
+        kv.stream(stream))
+    if status:
+        check(status, "lora_attn_prefix")
     return out
 
 
 def attn_prefix_8bit_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream=None):
     """attn_prefix_t over a PagedKV8bit (lora_attn_prefix_8bit)."""
-    kv.needs(8)
+    if kv.bits != 8:
+        kv.needs(8)
     _check_ws(ws, kv._device)
-    groups = _group_args(kv, group_off, prefix_len)
-    rows, rest, out = _attn_args(kv, q, ws, scale, out, stream)
-    check(load().lora_attn_prefix_8bit(kv.ref, *kv.scales, *groups, *rows, *rest), "lora_attn_prefix_8bit")
+    off, lens, n_groups = _group_args(kv, group_off, prefix_len)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
+    status = (_lib or load()).lora_attn_prefix_8bit(kv.ref, *kv.scales, off, lens, n_groups, q.data_ptr(), q_stride, n_q,
+        kv._scale if scale is None else scale, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
+        kv.stream(stream))
+    if status:
+        check(status, "lora_attn_prefix_8bit")
     return out
 
 
