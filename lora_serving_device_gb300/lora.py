@@ -780,13 +780,14 @@ def _c_counts(counts):
     return (ctypes.c_int32 * len(counts))(*counts)
 
 
-def _check_ws(ws, device):
-    if ws.get_device() != device or not ws.is_contiguous():
-        raise TypeError("ws: contiguous memory on the call's device")
+def _refuse_ws():
+    raise TypeError("ws: contiguous memory on the call's device")
 
 
 def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream):
     """Checks the arguments of an append; the C call's, from q to the stream, and q_out."""
+    if ws.get_device() != kv._device or not ws.is_contiguous():
+        _refuse_ws()
     from_q = to_q = table = at = pairs = None
     n_q = q_stride = q_out_stride = n_pos = rot = 0
     if q is not None:
@@ -842,7 +843,6 @@ def kv_append_8bit_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interl
     scale for each block of tokens and head, which grows as the block's values do."""
     if kv.bits != 8:
         kv.needs(8)
-    _check_ws(ws, kv._device)
     args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
     status = (_lib or load()).lora_kv_append_8bit(kv.ref, *kv.scales, *args)
     if status:
@@ -852,8 +852,11 @@ def kv_append_8bit_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interl
 
 # (a call of a few rows takes as long on the host as on the GPU, so the helpers below and above run
 # through few functions)
-def _attn_rows(kv, q, out, stream):
-    """Checks the rows of an attention call: query heads, distance of q's tokens, out and its."""
+def _attn_rows(kv, q, ws, out, stream):
+    """Checks the workspace and the rows of an attention call: query heads, distance of q's tokens, out
+    and its."""
+    if ws.get_device() != kv._device or not ws.is_contiguous():
+        _refuse_ws()
     n_q = q.shape[1]
     q_stride = kv.rows(q, n_q, "q")
     if out is None:
@@ -874,7 +877,7 @@ def attn_paged_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, stream=Non
     defaults to D^-0.5, window 0 is none."""
     if kv.bits != 16:
         kv.needs(16)
-    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, ws, out, stream)
     status = (_lib or load()).lora_attn_paged(kv.ref, q.data_ptr(), q_stride, n_q,
         kv._scale if scale is None else scale, window, n_sink, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
         kv.stream(stream))
@@ -887,8 +890,7 @@ def attn_paged_8bit_t(kv, q, ws, scale=None, window=0, n_sink=0, out=None, strea
     """attn_paged_t over a PagedKV8bit (lora_attn_paged_8bit)."""
     if kv.bits != 8:
         kv.needs(8)
-    _check_ws(ws, kv._device)
-    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, ws, out, stream)
     status = (_lib or load()).lora_attn_paged_8bit(kv.ref, *kv.scales, q.data_ptr(), q_stride, n_q,
         kv._scale if scale is None else scale, window, n_sink, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
         kv.stream(stream))
@@ -902,8 +904,8 @@ def attn_prefix_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, stream
     group_off [n_groups + 1], prefix_len [n_groups] int32 on the device."""
     if kv.bits != 16:
         kv.needs(16)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, ws, out, stream)
     off, lens, n_groups = _group_args(kv, group_off, prefix_len)
-    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
     status = (_lib or load()).lora_attn_prefix(kv.ref, off, lens, n_groups, q.data_ptr(), q_stride, n_q,
         kv._scale if scale is None else scale, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
         kv.stream(stream))
@@ -916,9 +918,8 @@ def attn_prefix_8bit_t(kv, q, group_off, prefix_len, ws, scale=None, out=None, s
     """attn_prefix_t over a PagedKV8bit (lora_attn_prefix_8bit)."""
     if kv.bits != 8:
         kv.needs(8)
-    _check_ws(ws, kv._device)
+    n_q, q_stride, out, out_stride = _attn_rows(kv, q, ws, out, stream)
     off, lens, n_groups = _group_args(kv, group_off, prefix_len)
-    n_q, q_stride, out, out_stride = _attn_rows(kv, q, out, stream)
     status = (_lib or load()).lora_attn_prefix_8bit(kv.ref, *kv.scales, off, lens, n_groups, q.data_ptr(), q_stride, n_q,
         kv._scale if scale is None else scale, out.data_ptr(), out_stride, ws.data_ptr(), ws.numel(),
         kv.stream(stream))
@@ -976,7 +977,8 @@ def batch_plan_t(block_table, n_cached, n_new, free_pages, n_free, page_size, n_
         elif t.dtype is not kind or t.get_device() != dev or not t.is_contiguous() or (n != t.numel() and n is not None):
             raise TypeError(f"{_PLAN_ARRAYS[i]}: contiguous {kind}{'' if n is None else f' [{n}]'} on the block "
                             "table's device")
-    _check_ws(ws, dev)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _refuse_ws()
     if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
         raise ValueError("block_table: [n_seqs, max_pages]")
     if dev < 0 or torch._C._cuda_getDevice() != dev:

@@ -1,5 +1,6 @@
 """The paged-cache helpers on the host, where a small call spends its time (an attention of one token
-takes less on the GPU than its call): how many functions of the binding one runs through.  The library's calls get a null cache, so nothing is launched."""
+takes less on the GPU than its call): how many functions of the binding one runs through, and which
+workspaces it refuses.  The library's calls get a null cache, so nothing is launched."""
 import sys
 
 import pytest
@@ -29,8 +30,9 @@ def cache(L, bits):
     return kv
 
 
-def calls(L, bits, ws):
+def calls(L, bits, ws, device=-1):
     kv = cache(L, bits)
+    kv._device = device
     q, k = (torch.zeros(T, h, D, dtype=torch.bfloat16) for h in (HQ, HKV))
     off, lens = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     cs, pos = torch.zeros(10, D), torch.zeros(T, dtype=torch.int32)
@@ -58,3 +60,15 @@ def test_wide_calls_run_through_few_functions(L, what, most):
     finally:
         sys.setprofile(None)
     assert 2 <= n <= most
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("what", ["append", "paged", "prefix"])
+def test_workspaces_elsewhere_or_with_gaps_are_refused(L, bits, what):
+    """A workspace with gaps is said to have all bytes up to its last, of which it owns a part."""
+    for ws, device in ((torch.zeros(1 << 21, dtype=torch.uint8)[::2], -1), (torch.zeros(1 << 20, dtype=torch.uint8), 0)):
+        f = calls(L, bits, ws, device)[what]
+        with pytest.raises(TypeError, match="ws"):
+            f()
+    with pytest.raises(L.LoraError):
+        calls(L, bits, torch.zeros(1 << 20, dtype=torch.uint8))[what]()
