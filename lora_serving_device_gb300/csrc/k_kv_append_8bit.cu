@@ -44,6 +44,11 @@ __device__ __forceinline__ RunInfo row_info(const lora_paged_kv_t& kv, int t, in
                                             uint32_t* err) {
   RunInfo x = {-1, 1, 0, 0};
   const int begin = kv.q_off[s], end = kv.q_off[s + 1];
+  if (end <= t) {  // offsets out of order: s is not the row's sequence, and a run would have no rows
+    flag_error(err, LORA_DEVERR_BAD_LEN);
+    x.in_seq = 0;
+    return x;
+  }
   x.p = kv.kv_len[s] - end + t;
   if (x.p < 0) return x;
   const int col = x.p / kv.page_size;

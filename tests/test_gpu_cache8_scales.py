@@ -107,3 +107,25 @@ def test_long_segments_of_single_tokens(L, hq, hkv, d, page):
     for c in cache[2:]:
         c.copy_(torch.randint(112, 123, c.shape, device="cuda", dtype=torch.uint8))
     batch(L, torch, cache, [1] * n, kv_len, hq, seed=hq, repeats=30)
+
+
+def test_append_with_offsets_out_of_order(L):
+    """Rows whose sequence the offsets do not give are reported and not cached (a run from them would have
+    fewer rows than none)."""
+    import torch
+    hq, hkv, d, page = 4, 2, 64, 16
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = L.PagedKV8bit.empty_cache(6, hkv, page, d)
+    for c in cache[2:]:
+        c.fill_(77)
+    # rows 2 and 3 look like sequence 1's, which ends in front of them
+    off, lens, table = i32([0, 50, 2, 4]), i32([50, 15, 0]), i32([[0, 1, 2, 3], [4, 5, -1, -1], [-1] * 4])
+    q, k = (torch.ones(4, h, d, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv))
+    for max_q in (1, 64):
+        kv = L.PagedKV8bit(*cache, table, off, lens, 4, max_q_len=max_q)
+        ws = L.attn_workspace(kv, hq)
+        L.kv_append_8bit_t(kv, q, k, k, None, ws)
+        if max_q == 1:
+            assert L.get_error_t(ws) == L.DEVERR_BAD_LEN
+        for c, s in ((cache[0], cache[2]), (cache[1], cache[3])):
+            assert not c.view(torch.uint8)[1:].any() and (s[1:] == 77).all()
