@@ -106,7 +106,11 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
                                             int bar) {
   const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
   RowWriter<D> out(P, g.shared, t, head, mine && g.parts == 1, m, l);
-  out.own *= unit;
+  // (a small unit is no part of the factor: with the sum's inverse that would be below the normal
+  // numbers, and so lose bits, where a result is not)
+  const bool small = unit < 0x1p-40f;
+  const float first = small ? unit : 1.f;
+  out.own *= small ? 1.f : unit;
   wait_quiet(o_done, parity, abort);
   __syncwarp();
   ptx::tc_fence_after();
@@ -126,6 +130,8 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
       float o[16];
       ptx::tmem_ld16(tm_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
       ptx::tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[x] *= first;
       if (mine) out.write16(k, o);
     }
     read();
