@@ -106,11 +106,8 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
                                             int bar) {
   const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + g.slot;
   RowWriter<D> out(P, g.shared, t, head, mine && g.parts == 1, m, l);
-  // (a small unit is no part of the factor: with the sum's inverse that would be below the normal
-  // numbers, and so lose bits, where a result is not)
-  const bool small = unit < 0x1p-40f;
-  const float first = small ? unit : 1.f;
-  out.own *= small ? 1.f : unit;
+  const RowUnit by(unit);
+  out.own *= by.factor;
   wait_quiet(o_done, parity, abort);
   __syncwarp();
   ptx::tc_fence_after();
@@ -131,7 +128,7 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
       ptx::tmem_ld16(tm_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
       ptx::tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 16; ++x) o[x] *= first;
+      for (int x = 0; x < 16; ++x) o[x] *= by.first;
       if (mine) out.write16(k, o);
     }
     read();
@@ -139,18 +136,20 @@ __device__ __forceinline__ void finish_half(const AttnParams& P, const Segment& 
   }
   if constexpr (kRolled) {
     float2* ml = reinterpret_cast<float2*>(P.part_ml) + h * kHalf + row;
+    const PartScale part(l);
 #pragma unroll 1
     for (int k = 0; k < D; k += 16) {
       float o[16];
       ptx::tmem_ld16(tm_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
       ptx::tmem_ld_wait();
 #pragma unroll
+      for (int x = 0; x < 16; ++x) o[x] = o[x] * part.down * unit;
+#pragma unroll
       for (int x = 0; x < 16 && mine; x += 4)
-        part_row<D>(P, slot, h, row)[(k + x) / 4 * kHalf] =
-            make_float4(o[x] * unit, o[x + 1] * unit, o[x + 2] * unit, o[x + 3] * unit);
+        part_row<D>(P, slot, h, row)[(k + x) / 4 * kHalf] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
     }
     read();
-    if (mine) ml[slot * 2 * kHalf] = make_float2(m, l);
+    if (mine) ml[slot * 2 * kHalf] = make_float2(m + part.up, l * part.down);
     if (!P.join_after && last_to_arrive(P, g, h, row == 0, last, bar, 128) && mine) {
       float top = -INFINITY, sum = 0.f;
 #pragma unroll 4

@@ -461,6 +461,29 @@ struct RowWriter {
   }
 };
 
+// Of a row's weights over an 8-bit cache, whose values lack a power of two, their `unit`: the
+// weights' sum l over a part of the keys is brought into [1, 2) and the maximum moved with it, so
+// that a part is as large as a value, not as all weights together, which the ends of fp32 would
+// not hold.  `down`: what l and the values are to be multiplied with, `up` its inverse, in log2.
+struct PartScale {
+  float down, up;
+  __device__ __forceinline__ explicit PartScale(float l) {
+    const int e = l > 0.f ? min(max(static_cast<int>(__float_as_uint(l) >> 23), 1), 253) : 127;
+    down = scale_of(254 - e);
+    up = static_cast<float>(e - 127);
+  }
+};
+// A whole row's, where its factor is 1 / l: a small unit is not made part of it, since the two
+// together would be below the normal numbers, and so lose bits, where a result is not.
+struct RowUnit {
+  float first, factor;  // of the values, and of 1 / l
+  __device__ __forceinline__ explicit RowUnit(float unit) {
+    const bool small = unit < 0x1p-40f;
+    first = small ? unit : 1.f;
+    factor = small ? 1.f : unit;
+  }
+};
+
 // The slot of the item's c-th part.
 __device__ __forceinline__ int64_t part_slot(const Segment& g, int c) {
   return static_cast<int64_t>(g.cta0 + c) * 2 + (c == 0 ? 1 : 0);
@@ -487,11 +510,12 @@ __device__ __forceinline__ bool last_to_arrive(const AttnParams& P, const Segmen
 // The end of an item, or of this CTA's part of it, in the kernels that have few rows
 // to a key head (A in a row tile): 128 threads of named barrier `bar` write the rows from
 // `stage` [A][D], maxima m [A] (log2 units) and the four warps' sums red_sum [A], joined with
-// the parts of other CTAs by the last to arrive.
-template <int D, int A>
+// the parts of other CTAs by the last to arrive.  kUnits: the rows are to be multiplied with `unit`.
+template <int D, int A, bool kUnits = false>
 __device__ __forceinline__ void finish_rows(const AttnParams& P, const Segment& g,
                                             const float* stage, const float* m,
-                                            const float4* red_sum, int tid, int* last, int bar) {
+                                            const float4* red_sum, int tid, int* last, int bar,
+                                            float unit = 1.f) {
   float2* ml = reinterpret_cast<float2*>(P.part_ml);
   const int vectors = g.t.n_rows * (D / 8);
   bool write = true;
@@ -500,10 +524,21 @@ __device__ __forceinline__ void finish_rows(const AttnParams& P, const Segment& 
 #pragma unroll 1
     for (int x = tid; x < vectors; x += 128) {
       const int n = x / (D / 8), k = x % (D / 8) * 8;
-      store8(P.part + (slot * A + n) * D + k,
-             *reinterpret_cast<const float(*)[8]>(stage + n * D + k));
       const float4 r = red_sum[n];
-      if (k == 0) ml[slot * A + n] = make_float2(m[n], r.x + r.y + r.z + r.w);
+      if constexpr (kUnits) {
+        const float l = r.x + r.y + r.z + r.w;
+        const PartScale by(l);
+        float o[8];
+        load8(stage + n * D + k, o);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) o[y] = o[y] * by.down * unit;
+        store8(P.part + (slot * A + n) * D + k, o);
+        if (k == 0) ml[slot * A + n] = make_float2(m[n] + by.up, l * by.down);
+      } else {
+        store8(P.part + (slot * A + n) * D + k,
+               *reinterpret_cast<const float(*)[8]>(stage + n * D + k));
+        if (k == 0) ml[slot * A + n] = make_float2(m[n], r.x + r.y + r.z + r.w);
+      }
     }
     write = last_to_arrive(P, g, 0, tid == 0, last, bar, 128);
   }
@@ -537,8 +572,14 @@ __device__ __forceinline__ void finish_rows(const AttnParams& P, const Segment& 
       }
     }
     const int r = g.t.row0 + n, tok = P.by_group(r);
-    const RowWriter<D> out(P, g.shared, g.tok0 + tok, g.head * P.group + r - tok * P.group, true,
-                           top, sum);
+    RowWriter<D> out(P, g.shared, g.tok0 + tok, g.head * P.group + r - tok * P.group, true,
+                     top, sum);
+    if (kUnits && g.parts == 1) {
+      const RowUnit by(unit);
+      out.own *= by.factor;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] *= by.first;
+    }
     out.write8(k, o);
   }
 }

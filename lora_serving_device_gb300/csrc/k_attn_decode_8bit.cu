@@ -556,12 +556,10 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
       for (int n = 0; n < kPV; n += 16)
         ptx::tmem_ld16(tm_o + n, *reinterpret_cast<uint32_t(*)[16]>(o + n));
       ptx::tmem_ld_wait();
-      const float fv = scale_of(max(R, 1));
       if (has_d) {
 #pragma unroll
         for (int n = 0; n < A; ++n)
-          stage[n * D + d] =
-              (o[n] + (1.f / kTerm) * (o[A + n] + (1.f / kTerm) * o[2 * A + n])) * fv;
+          stage[n * D + d] = o[n] + (1.f / kTerm) * (o[A + n] + (1.f / kTerm) * o[2 * A + n]);
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -571,7 +569,8 @@ __global__ void __launch_bounds__(Lay<D, A>::kThreads, 1)
       }
       named_bar(kBar, 128);
       if (late) pdl_wait();  // the prior parts are read, and the parts' memory is free
-      finish_rows<D, A>(P, g, stage, M.m[wg], red_sum, st_tid, &M.last[wg], kBar);
+      finish_rows<D, A, true>(P, g, stage, M.m[wg], red_sum, st_tid, &M.last[wg], kBar,
+                              scale_of(max(R, 1)));
       named_bar(kBar, 128);  // the sums and the limits are free
     }
   }

@@ -170,3 +170,108 @@ def test_a_shared_prefix_of_small_values(L):
     for s in range(n):
         k, v, vb = sequence(torch, cache, table[s], prefix + own, hq // hkv)
         check_tight(torch, got[s:s + 1], q[s:s + 1], k, v, vb, 3 - 127, prefix + own - 1, False)
+
+
+# ------------------------------------------------------------------ blocks of very different size
+
+def spread(torch, cache, low, high):
+    """The values' scales anywhere between two bytes, a tenth of them at either end."""
+    vs = cache[3]
+    x = torch.randint(low, high + 1, vs.shape, device="cuda")
+    pick = torch.rand(vs.shape, device="cuda")
+    x = torch.where(pick < 0.1, low, torch.where(pick > 0.9, high, x))
+    vs.copy_(x.to(torch.uint8))
+
+
+@pytest.mark.parametrize("low,high", [(110, 123), (100, 125), (95, 135), (20, 240)])
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 64, 1), (8, 2, 128, 4), (32, 2, 128, 1), (16, 4, 64, 70), (8, 2, 128, 200)])
+@pytest.mark.parametrize("page", [8, 32])
+def test_value_blocks_of_very_different_size(L, low, high, hq, hkv, d, rows, page):
+    """Ratios at which an f16 of a value is exact, rounded, and lost, and a weight's terms leave the range of
+    their type; past 2^127 a factor between blocks is no number of fp32's exponents."""
+    import torch
+    rng = np.random.default_rng(low + rows)
+    n = 12
+    q_lens = rng.integers(1, rows + 1, n)
+    q_lens[0] = rows
+    kv_len = q_lens + rng.integers(0, 900, n)
+    torch.manual_seed(high + page)
+    cache = random_cache(torch, n * -(-1200 // page), hkv, page, d)
+    spread(torch, cache, low, high)
+    batch(L, torch, cache, list(q_lens), kv_len, hq, seed=low)
+
+
+@pytest.mark.parametrize("more", [8, 13, 16, 20, 25, 40, 130])
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 64, 4), (4, 2, 128, 8), (8, 2, 64, 64), (8, 2, 128, 300)])
+def test_a_later_token_with_much_larger_values(L, more, hq, hkv, d, rows):
+    """The last block of a prompt has values 2^more times the others': rows in front of it do not see them,
+    but are rounded against their scale, within the bound of that."""
+    import torch
+    page, n = 16, 320
+    torch.manual_seed(more)
+    cache = random_cache(torch, n // page, hkv, page, d)
+    table = torch.randperm(n // page, device="cuda").int()[None]
+    cache[3].fill_(100)
+    cache[3][table[0, -1].long()] = 100 + more
+    kv = L.PagedKV8bit(*cache, table, torch.tensor([0, rows], dtype=torch.int32, device="cuda"),
+                       torch.tensor([n], dtype=torch.int32, device="cuda"), rows)
+    q = (0.05 * torch.randn(rows, hq, d, device="cuda")).to(torch.bfloat16)
+    ws = L.attn_workspace(kv, hq)
+    got = L.attn_paged_8bit_t(kv, q, ws)
+    assert L.get_error_t(ws) == 0
+    k, v, vb = sequence(torch, cache, table[0], n, hq // hkv)
+    check_tight(torch, got, q, k, v, vb, int(vb.max()), n - rows, rows * hq // hkv <= 16)
+
+
+# ------------------------------------------------------------------ windows, pages, parts and prefixes
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64), (64, 8, 64), (16, 1, 128), (24, 1, 64)])
+@pytest.mark.parametrize("rows", [1, 90])
+@pytest.mark.parametrize("page,window,n_sink", [(8, 0, 0), (16, 700, 4), (256, 0, 0), (64, 130, 40)])
+def test_batches_part_by_part(L, hq, hkv, d, rows, page, window, n_sink):
+    import torch
+    rng = np.random.default_rng(hq + rows + page)
+    n = 24
+    q_lens = rng.integers(1, rows + 1, n)
+    kv_len = q_lens + rng.integers(0, 2500, n)
+    torch.manual_seed(hq)
+    cache = random_cache(torch, n * -(-2700 // page), hkv, page, d)
+    batch(L, torch, cache, list(q_lens), kv_len, hq, seed=rows, window=window, n_sink=n_sink)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64), (16, 1, 128)])
+@pytest.mark.parametrize("rows", [1, 60])
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_prefixes_part_by_part(L, hq, hkv, d, rows, n):
+    """The two phases apart: each is rounded against the largest scale of its own keys."""
+    import torch
+    page, prefix, own = 16, 1500, 200
+    rng = np.random.default_rng(n + rows)
+    q_lens = [int(x) for x in rng.integers(1, rows + 1, n)]
+    torch.manual_seed(n + hq)
+    shared = -(-prefix // page)
+    mine = -(-(prefix + own) // page) - prefix // page
+    cache = random_cache(torch, shared + n * mine, hkv, page, d)
+    spread(torch, cache, 112, 122)
+    table = torch.full((n, prefix // page + mine), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    table[0, :shared] = torch.arange(shared, device="cuda")
+    for s in range(n):
+        at = shared + s * mine + torch.arange(mine, device="cuda")
+        table[s, prefix // page:] = at
+        for c in cache:     # the prefix' last page, a copy each
+            c.view(torch.uint8)[at[0]] = c.view(torch.uint8)[shared - 1]
+    off = torch.tensor([0] + q_lens, device="cuda").cumsum(0).int()
+    T = int(off[-1])
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    kv = L.PagedKV8bit(*cache, table, off, i32([prefix + own] * n), T, max_q_len=max(q_lens))
+    q = (0.05 * torch.randn(T, hq, d, device="cuda")).to(torch.bfloat16)
+    ws = L.attn_workspace(kv, hq, n_groups=1)
+    got = L.attn_prefix_8bit_t(kv, q, i32([0, n]), i32([prefix]), ws)
+    assert L.get_error_t(ws) == 0
+    few = T * (hq // hkv) <= 16 and max(q_lens) * (hq // hkv) <= 16
+    a = 0
+    for s, m in enumerate(q_lens):
+        row = torch.cat([table[0, :prefix // page], table[s, prefix // page:]])
+        k, v, vb = sequence(torch, cache, row, prefix + own, hq // hkv)
+        check_tight(torch, got[a:a + m], q[a:a + m], k, v, vb, int(vb.max()), prefix + own - m, few)
+        a += m
