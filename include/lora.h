@@ -663,8 +663,12 @@ lora_status_t lora_attn_prefix(const lora_paged_kv_t* kv, const int32_t* group_o
  * outside its range is cut, pages given back past free_cap are lost (LORA_DEVERR_BAD_LEN); with
  * no page left the entry becomes -1 (LORA_DEVERR_NO_PAGE); a row whose page is missing
  * has slot -1 (LORA_DEVERR_BAD_PAGE).
+ * After LORA_DEVERR_NO_PAGE the lengths have moved on all the same: the entry counts as held in
+ * the next call and is not asked for again, so the caller writes a page into it or lets the
+ * request end.
  * Shapes: page_size 8, 16, 32, 64, 128 or 256; 1 <= n_seqs <= LORA_MAX_SEQS; 0 <= T <=
- * LORA_MAX_TOKENS; max_pages as in lora_paged_kv_t; free_cap >= 1.
+ * LORA_MAX_TOKENS; max_pages * page_size + T at most 2^31 - 1024 (the positions of a full row
+ * and the rows after them); free_cap >= 1.
  * Workspace: lora_batch_plan_workspace_bytes(n_seqs).
  */
 size_t lora_batch_plan_workspace_bytes(int32_t n_seqs);
@@ -682,7 +686,8 @@ lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
  *   k_scale, v_scale [n_pages, n_kv_heads, page_size / B] uint8: one scale for B = 16 tokens
  *            (8 in pages of 8) of a head.  Byte b stands for 2^(b - 127), b = 1 .. 253; 0
  *            reads as 1, so zero-filled memory is a valid cache of zeros, and 254, 255 as 253.
- *   value    = code * 2^(b - 127), the same in every call; exact in bf16.
+ *   value    = code * 2^(b - 127), the same in every call; exact in bf16 for b = 3 .. 246 (below
+ *            and above that some codes leave its range).
  * A power of two is enough of a scale: e4m3 is a floating type, so the scale's fraction
  * would not make its rounding finer.  Caches, scales and rows 16-byte aligned.
  *
@@ -692,18 +697,29 @@ lora_status_t lora_batch_plan(const int32_t* n_cached, const int32_t* n_new,
  * that is larger (a block has one if its first position is not among the call's rows).
  * Where the scale grows, the codes of the block's earlier rows are moved to it, which is exact
  * but for codes that become subnormal.  So scales do not depend on how tokens are
- * divided over calls.  An infinite value becomes the largest code, NaN stays NaN.  No two sequences
- * of a call may append to one block.
+ * divided over calls.  An infinite value becomes the largest code at the scale that the type's
+ * largest finite value takes, 2^120, beside which the block's other values, earlier rows'
+ * too, are zeros from then on; NaN stays NaN and has no say in the scale.  Neither sets an error.
+ * No two sequences of a call may append to one block.  A row behind its sequence's
+ * end (q_off out of order) sets LORA_DEVERR_BAD_LEN and is not cached.
  *
  * lora_attn_paged_8bit, lora_attn_prefix_8bit: lora_attn_paged and lora_attn_prefix over
  * it; the same masks, workspaces (lora_attn_workspace_bytes) and errors.  The keys' codes
  * enter their product as they are, and a row of q as two e4m3 terms, off by at most 2^-17 of its
- * largest value (q has to be finite).  Where the keys stand in the MMA's M (where lora_attn_paged has the
- * weights as a pair of bf16) a weight enters its product as three e4m3 terms, off by 2^-12 of
- * itself or 2^-23 of the row's largest, whichever is more, and by as much of the product's
- * at the largest v_scale seen; elsewhere as one f16, off by 2^-11 of itself, beside values that are
- * f16, off by at most 2^-16 of the largest v_scale seen.  Scores, maxima, sums and the accumulator
- * are fp32, and the result is rounded once.  So max_q_len, and a prompt in the same batch, change the
+ * largest value (q has to be finite).  Let V be the largest v_scale of the blocks that the
+ * call's kernels take together: those that ANY row of the same sequence (in the prefix part
+ * of lora_attn_prefix, of the same group) sees, later tokens' among them.
+ *   Where the keys stand in the MMA's M (where lora_attn_paged has the weights as a pair of
+ *   bf16) a weight enters its product as three e4m3 terms: off by 2^-12 of itself, or by 2^-23
+ *   of the row's largest weight times V / v_scale, whichever is more, and never by more
+ *   than itself.
+ *   Elsewhere it is one f16: off by 2^-11 of itself, or by 2^-31 of the row's largest,
+ *   whichever is more; and the values are f16 of value / V: exact where v_scale is V / 2^15
+ *   or more, off by V / 2^25 down to V / 2^24, and 0 below.
+ * So a row is as exact as its weights while no scale that its sequence sees is far above its
+ * own values', by 2^11 or 2^15; behind a token whose values are larger by 2^24, the other
+ * rows of the call keep nothing of theirs.  Scores, maxima, sums and the accumulator
+ * are fp32, and the result is rounded once.  max_q_len, and a prompt in the same batch, change the
  * rounding of a single token's weights.  Scales of blocks that no row sees may hold
  * anything.
  */

@@ -959,7 +959,9 @@ def batch_plan_t(block_table, n_cached, n_new, free_pages, n_free, page_size, n_
     taken from the top of the stack free_pages[:n_free], a request with n_new < 0 gives its
     pages back.  Writes block_table and free_pages; returns a BatchPlan of T rows, or `out`,
     one that the caller keeps (its kv_len may be n_cached, its n_free may be n_free: then
-    a decode loop calls this with the same arrays in every step; slots or pos may be None)."""
+    a decode loop calls this with the same arrays in every step; slots or pos may be None).
+    T defaults to the rows of out's slots or pos, and without those to 0: give it if there are
+    new tokens, since rows from T on are dropped and reported (LORA_DEVERR_BAD_LEN)."""
     import torch
     n_seqs, i32, dev = n_cached.numel(), torch.int32, block_table.get_device()
     if out is None:
