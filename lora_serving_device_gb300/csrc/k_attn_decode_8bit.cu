@@ -26,7 +26,9 @@
 //
 // Measured (HBM's measured rate is 6.69 TB/s): 64 tokens on 500 - 8000, 32 / 8 heads of 128,
 // pages of 16: 90 us, 6.1 TB/s; 152 on 4000 186 us, 6.7 TB/s; 3 tokens on 90000 - 131000: 117 us,
-// 6.3 TB/s; one token on 500 9.4 us.  A batch of few items a CTA pays its first page ids,
+// 6.3 TB/s; one token on 500 9.2 us; 96 tokens with a window of 4096, 64 / 8 heads of 64, 102 us, 3.6 TB/s.  With
+// 9 to 16 rows of a key head one buffer of P is all that fits, and 36 (128 values a head) or 44 bytes
+// spill: 64 tokens on 8K with 32 / 2 heads of 128 42 us, 3.6 TB/s, with 64 / 4 of 64 58 us.  A batch of few items a CTA pays its first page ids,
 // tiles and results: 19 tokens on 8000, one item a CTA, 52 us, 6.0 TB/s.
 //
 // Warps: 0 = schedule and TMA of K, 1 = MMA issue, 2-5 and 6-9 = softmax and epilogue, 10 =

@@ -17,14 +17,15 @@
 // the way.  A key block's scale is a factor of its 16 scores beside c.
 //
 // The bf16 kernel's (k_attn_prefill.cu) schedule of halves, softmax and results, and its floor:
-// the tensor cores.  Measured: prompt of 8192, 32 / 8 heads of 128: 393 to 407 us (1400 TFLOP/s,
-// 0.73 of the measured burst rate; bf16 cache 347 us); chunks with a window of 1024, 64 / 8
-// heads of 64: 193 us.  The tensor pipe is active for 60% of the cycles, no other pipe for
+// the tensor cores.  Measured on a warm card: prompt of 8192, 32 / 8 heads of 128: 404 to 413 us (1330 to
+// 1360 TFLOP/s, 0.69 to 0.71 of the measured burst rate; 393 in the first moments on a cool one; bf16
+// cache 359 to 373); chunks with a window of 1024, 64 / 8 heads of 64: 193 us (117); 8 chunks of 300 behind a
+// shared prefix of 8K 333 (306).  The tensor pipe is active for 60% of the cycles, no other pipe for
 // more than 35.  A half's chain bounds it, 2400 cycles from scores to weights and 500 back
 // through the MMAs, a tile, beside the issuing thread, which is never idle.  The roles
 // take more instructions a tile than the bf16 kernel's, so what counted most was to keep them short
 // (all 128 scores of a row in registers, one long piece of code: 821 us; loops over 64: 467), the issuing
-// thread's commits few (six a tile 467 us, three 433), and Q's split short (429, now 419: an
+// thread's commits few (six a tile 467 us, three 433), and Q's split short (429 us, then 419: an
 // item's first scores wait for it).
 //
 // Warps: 0-3 softmax and results of half 0, 4-7 of half 1, 8 schedule and TMA, 9 MMA issue,
@@ -38,7 +39,7 @@ namespace lora {
 namespace {
 
 // Four warpgroups, of which two are the softmax's: 160 x 256 + 96 x 256 registers are the
-// launch's 128 x 512 (with 128 each, 48 bytes spill: 434 us for 427).
+// launch's 128 x 512 (with 128 each, 48 bytes spill: 434 us for 427; so, 24 with blocks of 16 keys).
 constexpr int kThreads = 512;
 constexpr int kRegsMost = 160, kRegsLeast = 96;
 constexpr int kFirstWidener = 12, kWideners = 4;  // warps that widen V
@@ -479,6 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = P.groups_phase ? g.t.vis_hi : min(pos, g.t.vis_hi);
       const int lo = P.groups_phase ? 0 : max(window_first(P, pos), g.k_lo);
       const int min_hi = __reduce_min_sync(0xffffffffu, hi), max_lo = __reduce_max_sync(0xffffffffu, lo);
+      // (this half may have left out segments, and with them batches of scales: the warps that split Q
+      // have used them all before)
       wait_quiet(&M.q_full[h][segs % kQTurns], (segs / kQTurns) & 1, abort_f);
       const float q_scale = c * scale_of(M.q_scale[h][segs % kQTurns][row]);
       ++segs;

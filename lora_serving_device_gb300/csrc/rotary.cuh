@@ -1,6 +1,7 @@
-// Rotation of 16-value units of a head by position (lora_kv_append and its
-// 8-bit form): (a, b) -> (a c - b s, b c + a s) for pair i, c and s from the
-// caller's table at the position of the pair's axis.
+// Rotation of 16-value units of a head by position: (a, b) -> (a c - b s, b c + a s) for
+// pair i, c and s from the caller's table at the position of the pair's axis.  load_rot
+// serves lora_kv_append, which rotates on the way to bf16; rotate_unit its 8-bit form,
+// which has the rows' cosines and sines in shared memory.
 #pragma once
 
 #include "attn.h"
