@@ -784,12 +784,15 @@ def _refuse_ws():
     raise TypeError("ws: contiguous memory on the call's device")
 
 
-def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream):
-    """Checks the arguments of an append; the C call's, from q to the stream, and q_out."""
+def _append(bits, kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream):
+    """Checks the arguments of an append to a cache of `bits` and makes the call; returns q_out."""
+    if kv.bits != bits:
+        kv.needs(bits)
     if ws.get_device() != kv._device or not ws.is_contiguous():
         _refuse_ws()
     from_q = to_q = table = at = pairs = None
     n_q = q_stride = q_out_stride = n_pos = rot = 0
+    n_axes = 1
     if q is not None:
         n_q = q.shape[1]
         q_stride = kv.rows(q, n_q, "q")
@@ -804,7 +807,6 @@ def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, 
         table = cos_sin.data_ptr()
         if cos_sin.dtype is not kv._f32 or not cos_sin.is_contiguous() or cos_sin.get_device() != kv._device:
             raise TypeError("cos_sin: contiguous fp32 [n_pos, rot_dim] on the cache's device")
-    n_axes = 1
     if pos is not None:
         shape, at = pos.shape, pos.data_ptr()
         n_axes = shape[0] if len(shape) == 2 else 1
@@ -816,9 +818,20 @@ def _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, 
             raise ValueError(f"axis_pairs: {len(axis_pairs)} counts for {n_axes} axes")
         pairs = _c_counts(tuple(axis_pairs))
     hk = kv.n_kv_heads
-    return (from_q, q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(), kv.rows(v, hk, "v"), n_q, table, n_pos,
-            rot, at, n_axes, pairs, 1 if interleaved else 0, to_q, q_out_stride, ws.data_ptr(), ws.numel(),
-            kv.stream(stream)), q_out
+    lib = _lib or load()
+    if bits == 16:
+        status = lib.lora_kv_append(kv.ref, from_q, q_stride, k.data_ptr(), kv.rows(k, hk, "k"), v.data_ptr(),
+                                    kv.rows(v, hk, "v"), n_q, table, n_pos, rot, at, n_axes, pairs,
+                                    1 if interleaved else 0, to_q, q_out_stride, ws.data_ptr(), ws.numel(),
+                                    kv.stream(stream))
+    else:
+        status = lib.lora_kv_append_8bit(kv.ref, *kv.scales, from_q, q_stride, k.data_ptr(), kv.rows(k, hk, "k"),
+                                         v.data_ptr(), kv.rows(v, hk, "v"), n_q, table, n_pos, rot, at, n_axes, pairs,
+                                         1 if interleaved else 0, to_q, q_out_stride, ws.data_ptr(), ws.numel(),
+                                         kv.stream(stream))
+    if status:
+        check(status, "lora_kv_append" if bits == 16 else "lora_kv_append_8bit")
+    return q_out
 
 
 def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
@@ -828,26 +841,14 @@ def kv_append_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved
     allowed).  q None: keys and values only.  cos_sin [n_pos, rot_dim] fp32 (rope_table) or
     None for no rotation.  pos: None (the position in the cache), [T], or [n_axes, T] with
     axis_pairs, the rotated pairs of each axis."""
-    if kv.bits != 16:
-        kv.needs(16)
-    args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
-    status = (_lib or load()).lora_kv_append(kv.ref, *args)
-    if status:
-        check(status, "lora_kv_append")
-    return q_out
+    return _append(16, kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
 
 
 def kv_append_8bit_t(kv, q, k, v, cos_sin, ws, pos=None, axis_pairs=None, interleaved=False, q_out=None,
                      stream=None):
     """kv_append_t into a PagedKV8bit (lora_kv_append_8bit): k and v become e4m3 codes, at one
     scale for each block of tokens and head, which grows as the block's values do."""
-    if kv.bits != 8:
-        kv.needs(8)
-    args, q_out = _append_args(kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
-    status = (_lib or load()).lora_kv_append_8bit(kv.ref, *kv.scales, *args)
-    if status:
-        check(status, "lora_kv_append_8bit")
-    return q_out
+    return _append(8, kv, q, k, v, cos_sin, ws, pos, axis_pairs, interleaved, q_out, stream)
 
 
 # (a call of a few rows takes as long on the host as on the GPU, so the helpers below and above run
